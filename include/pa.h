@@ -101,6 +101,42 @@ int pa_reshape_and_cache(const void *k_new, const void *v_new, void *k_cache, vo
                          int block_size, int head_dim, int dtype, pa_stream_t stream);
 
 /*
+ * pa_rope_reshape_and_cache -- pa_reshape_and_cache with rotary positions: the
+ * queries and the new keys are rotated by their token's position on the way,
+ * in one launch (values are stored as they are).
+ * Element pairs (x, y) of a head rotate by the angle a = position * inv_freq[i]
+ * of their frequency i in [0, rot_dim/2):
+ *   x' = x cos a - y sin a,  y' = x sin a + y cos a
+ * with (x, y) = elements (i, i + rot_dim/2), or (2i, 2i + 1) if interleaved;
+ * elements from rot_dim on are copied.  A token has one position per axis
+ * (one axis for text; time, height and width for images and video); the first
+ * sections[0] frequencies take axis 0's position, the next sections[1] axis
+ * 1's, and so on.  Angles are reduced in fp64, so far positions lose nothing;
+ * the rotation is fp32, rounded once.
+ *   q_out, q      [T][Hq][head_dim], k_new, v_new [T][Hkv][head_dim] (dtype);
+ *                 heads of a token contiguous, q_out_stride .. v_stride elements
+ *                 (a multiple of 16 bytes, at most 2^28) between tokens: slices
+ *                 of one fused projection are fine.  q_out may be q itself, and
+ *                 otherwise overlaps no input.
+ *   slot_mapping  int64 [T] as for pa_reshape_and_cache (a negative slot stores
+ *                 nothing; its query is rotated all the same)
+ *   positions     int64 [num_axes][T] device
+ *   inv_freq      float32 [rot_dim/2] device
+ *   sections      HOST int [num_axes], not negative, summing to rot_dim/2
+ *   num_axes      1 .. 4
+ * rot_dim: even, at most head_dim and 512, half of it whole 16-byte pieces.
+ * head_dim: row of a head a multiple of 16 bytes, at most 1024 elements.
+ */
+int pa_rope_reshape_and_cache(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
+                              const void *k_new, int64_t k_stride, const void *v_new,
+                              int64_t v_stride, void *k_cache, void *v_cache,
+                              const int64_t *slot_mapping, const int64_t *positions,
+                              const float *inv_freq, const int *sections, int num_axes,
+                              int interleaved, int64_t T, int64_t num_blocks, int Hq, int Hkv,
+                              int block_size, int head_dim, int rot_dim, int dtype,
+                              pa_stream_t stream);
+
+/*
  * pa_copy_blocks -- copy-on-write support: for each pair (src, dst), physical
  * block dst of BOTH caches becomes a byte copy of block src ("Apa itu
  * PagedAttention?", section "Cara kerja PagedAttention", item 3; nalar.dev,
@@ -131,6 +167,32 @@ int pa_swap_blocks(void *dst_k, void *dst_v, const void *src_k, const void *src_
                    const int64_t *pairs, int64_t n, int64_t src_num_blocks,
                    int64_t dst_num_blocks, int Hkv, int block_size, int head_dim, int dtype,
                    pa_stream_t stream);
+
+/*
+ * pa_compact_cache -- keep some tokens of each sequence and move them to its
+ * front: row i of (sequence b, KV head h) becomes the old row keep[b][h][i],
+ * K and V, for i < keep_lens[b].  Each KV head keeps tokens of its own; the
+ * number kept is the sequence's.  Bit exact.
+ *   src_table  int32 [B][src_blocks_per_seq]: the sequences' pages
+ *   dst_table  int32 [B][dst_blocks_per_seq]: the pages that receive the kept
+ *              tokens.  A page may stay in its place (the same page at the same
+ *              logical block of the same sequence: compaction in place); every
+ *              other page written must not be read by this call, nor may a page
+ *              be written for two sequences.  Pages that other sequences still
+ *              share are replaced by fresh ones (pa_bm_compact does this).
+ *   keep       int32 [B][Hkv][max_keep] device: strictly ascending positions
+ *              inside src_table; entries from keep_lens[b] on are not read
+ *   keep_lens  int32 [B], each in [0, max_keep]
+ * Validate mode checks every rule above.  Outside it, a position or page out of
+ * range is skipped and recorded (PA_DEVERR_BAD_BLOCK); positions that are not
+ * ascending, or pages read and written other than in place, give undefined
+ * rows.  Rows behind the last kept token keep their old bytes.
+ */
+int pa_compact_cache(void *k_cache, void *v_cache, const int32_t *src_table,
+                     int src_blocks_per_seq, const int32_t *dst_table, int dst_blocks_per_seq,
+                     const int32_t *keep, int max_keep, const int32_t *keep_lens, int B,
+                     int64_t num_blocks, int Hkv, int block_size, int head_dim, int dtype,
+                     pa_stream_t stream);
 
 /*
  * pa_decode_workspace_size -- bytes of device workspace pa_decode needs: the
@@ -372,6 +434,27 @@ int pa_decode_noalloc(void *out, const void *q, const void *k_cache, const void 
                       const int32_t *context_lens, int B, int Hq, int Hkv, int head_dim,
                       int block_size, int64_t num_blocks, float scale, int partition_tokens,
                       int dtype, pa_stream_t stream);
+
+/*
+ * pa_decode_window -- pa_decode with a sliding window and sinks: the new query
+ * of sequence b (at position L - 1, L = context_lens[b]) sees the tokens j with
+ *   j < num_sinks  or  j >= L - window,
+ * the first few of the sequence and the last `window`, the newest included.
+ *   window     at least 1; num_sinks at least 0 (both may exceed L)
+ *   block_table  entries of blocks that hold no visible token are never read:
+ *              their pages may have been freed (pa_bm_trim)
+ *   context_lens  each in [0, capacity]; a row of length 0 (padding of a batch)
+ *              gets zeros
+ * Other arguments and the error bound as for pa_decode; bit-identical under any
+ * placement of the blocks.  K and V of tokens that are not visible do not enter
+ * the result, whatever they hold.  One launch, without a workspace: a cluster
+ * of 1 to 16 CTAs (from the sizes alone) per (sequence, KV head).
+ */
+int pa_decode_window(void *out, const void *q, const void *k_cache, const void *v_cache,
+                     const int32_t *block_table, int max_blocks_per_seq,
+                     const int32_t *context_lens, int B, int Hq, int Hkv, int head_dim,
+                     int block_size, int64_t num_blocks, float scale, int window, int num_sinks,
+                     int dtype, pa_stream_t stream);
 
 /*
  * pa_check_wait_timeout -- diagnostic of the device-side failure path: one

@@ -35,6 +35,12 @@ SIGNATURES = {
                                 _c_int, _c_vp]),
     "pa_swap_blocks": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64,
                                 _c_int, _c_int, _c_int, _c_int, _c_vp]),
+    "pa_rope_reshape_and_cache": (_c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp,
+                                           _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp,
+                                           _c_int, _c_int, _c_i64, _c_i64, _c_int, _c_int, _c_int,
+                                           _c_int, _c_int, _c_int, _c_vp]),
+    "pa_compact_cache": (_c_int, [_c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_int,
+                                  _c_vp, _c_int, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_vp]),
     "pa_decode_workspace_size": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
                                           ctypes.POINTER(_c_sz)]),
     "pa_decode_kernel_for": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int,
@@ -63,6 +69,9 @@ SIGNATURES = {
     "pa_decode_noalloc_capacity": (_c_sz, []),
     "pa_decode_noalloc": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_int, _c_int,
                                    _c_int, _c_int, _c_int, _c_i64, _c_f, _c_int, _c_int, _c_vp]),
+    "pa_decode_window": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_int, _c_int,
+                                  _c_int, _c_int, _c_int, _c_i64, _c_f, _c_int, _c_int, _c_int,
+                                  _c_vp]),
     "pa_prefill_chunk": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_int,
                                   _c_int, _c_int, _c_int, _c_int, _c_int, _c_i64, _c_f, _c_int,
                                   _c_vp]),

@@ -1,6 +1,7 @@
 // reshape_and_cache and copy_blocks: the bit-exact data movement of the
 // paged KV cache.  Both are HBM-bound copies done in 16-byte vectors.
 #include <algorithm>
+#include <new>
 #include <unordered_set>
 #include <vector>
 
@@ -125,6 +126,28 @@ int grid_for(int64_t work, int threads) {
 
 }  // namespace
 
+namespace pa {
+
+int validate_slots(const int64_t *slots, int64_t T, int64_t num_blocks, int block_size,
+                   cudaStream_t stream) try {
+    std::vector<int64_t> s(T);
+    if (int rc = fetch(s.data(), slots, T * sizeof(int64_t), stream)) return rc;
+    std::unordered_set<int64_t> seen;
+    for (int64_t t = 0; t < T; ++t) {
+        if (s[t] < 0) continue;
+        if (s[t] >= num_blocks * block_size)
+            return fail(PA_ERR_INVALID, "validate: slot %lld of token %lld out of pool",
+                        (long long)s[t], (long long)t);
+        if (!seen.insert(s[t]).second)
+            return fail(PA_ERR_INVALID, "validate: duplicate slot %lld", (long long)s[t]);
+    }
+    return PA_OK;
+} catch (const std::bad_alloc &) {
+    return fail(PA_ERR_OOM, "validate: host allocation failed");
+}
+
+}  // namespace pa
+
 extern "C" {
 
 int pa_reshape_and_cache(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
@@ -145,19 +168,8 @@ int pa_reshape_and_cache(const void *k_new, const void *v_new, void *k_cache, vo
     if (!pa::aligned16(k_new) || !pa::aligned16(v_new) || !pa::aligned16(k_cache) ||
         !pa::aligned16(v_cache))
         return pa::fail(PA_ERR_INVALID, "reshape_and_cache: pointers must be 16-byte aligned");
-    if (pa::validate_on()) {
-        std::vector<int64_t> s(T);
-        if (int rc = pa::fetch(s.data(), slot_mapping, T * sizeof(int64_t), stream)) return rc;
-        std::unordered_set<int64_t> seen;
-        for (int64_t t = 0; t < T; ++t) {
-            if (s[t] < 0) continue;
-            if (s[t] >= num_blocks * block_size)
-                return pa::fail(PA_ERR_INVALID, "validate: slot %lld of token %lld out of pool",
-                                (long long)s[t], (long long)t);
-            if (!seen.insert(s[t]).second)
-                return pa::fail(PA_ERR_INVALID, "validate: duplicate slot %lld", (long long)s[t]);
-        }
-    }
+    if (pa::validate_on())
+        if (int rc = pa::validate_slots(slot_mapping, T, num_blocks, block_size, stream)) return rc;
     const int chunks = static_cast<int>(head_dim * es / 16);
     const int64_t total = T * Hkv * chunks;
     (void)cudaGetLastError();  // drop a stale error that is not ours

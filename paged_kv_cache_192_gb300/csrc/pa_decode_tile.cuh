@@ -190,10 +190,12 @@ struct WarpAttn {
         }
     }
 
-    // One staged tile: K rows at kaddr, V rows at vaddr (shared), nvalid rows valid.
+    // One staged tile: K rows at kaddr, V rows at vaddr (shared), nvalid rows
+    // valid; with WIN, only rows [first, nvalid) are (at least one).
+    template <bool WIN = false>
     __device__ __forceinline__ void tile(uint32_t kaddr, uint32_t vaddr, int nvalid, float *pbuf,
-                                         float *sbuf) {
-        const bool masked = nvalid < C::TT;
+                                         float *sbuf, int first = 0) {
+        const bool masked = nvalid < C::TT || (WIN && first > 0);
         // ---- QK: partial dots of S token rows x GQ heads -----------------
         float part_[C::V];
 #pragma unroll
@@ -219,7 +221,7 @@ struct WarpAttn {
         transpose_reduce<C::V, C::G>(part_, lane);
 
         float sc[C::VPL];
-        const bool row_valid = row_mine < nvalid;
+        const bool row_valid = row_mine < nvalid && (!WIN || row_mine >= first);
 #pragma unroll
         for (int k = 0; k < C::VPL; ++k) sc[k] = row_valid ? part_[k] : -INFINITY;
 
@@ -257,7 +259,8 @@ struct WarpAttn {
         }
 #pragma unroll
         for (int k = 0; k < C::VPL; ++k) {
-            const float pk = fast_exp2(sc[k] - mh[k]);
+            // (a head whose scores are all -inf so far takes p = 0)
+            const float pk = fast_exp2(sc[k] - (WIN && mh[k] == -INFINITY ? 0.f : mh[k]));
             lsum[k] += pk;
             pbuf[row_mine * GQ + h0 + k] = pk;
         }
@@ -290,7 +293,7 @@ struct WarpAttn {
 #pragma unroll
                 for (int j = 0; j < C::EPC / 2; ++j) vf[c * C::EPC / 2 + j] = f[j];
             }
-            if (masked && row >= nvalid) {
+            if (masked && (row >= nvalid || (WIN && row < first))) {
                 // p is 0 there, but the stale row may hold NaN: 0 * NaN = NaN
 #pragma unroll
                 for (int j = 0; j < C::P; ++j) vf[j] = make_float2(0.f, 0.f);
@@ -514,9 +517,11 @@ struct MmaAttn {
 
     // nvalid: tokens of the tile inside the context; with QH > GQ, the
     // columns from GQ on (a forked child's heads) see only the first
-    // nvalid_hi of them.
+    // nvalid_hi of them.  WIN: only tokens [first, nvalid) count (at least
+    // one).
+    template <bool WIN = false>
     __device__ __forceinline__ void tile(uint32_t kaddr, uint32_t vaddr, int nvalid, float *,
-                                         float *, int nvalid_hi = 0) {
+                                         float *, int nvalid_hi = 0, int first = 0) {
         // ---- S^T = K q^T (two accumulators: shorter dependency chains) ----
         float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -538,8 +543,19 @@ struct MmaAttn {
             }
             __syncwarp();
         }
+        if (WIN && first > 0) {
+            // and the V rows before the first token that counts
+            for (int i = lane; i < first * C::HALVES * 8; i += 32) {
+                const int r = i / (C::HALVES * 8), w = i % (C::HALVES * 8);
+                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                 vaddr + (w >> 3) * C::HALF + r * 128 + (w & 7) * 16),
+                             "r"(0u)
+                             : "memory");
+            }
+            __syncwarp();
+        }
         const int nv = (QH > GQ && 2 * t >= GQ) ? nvalid_hi : nvalid;
-        const bool v0 = g < nv, v1 = g + 8 < nv;
+        const bool v0 = g < nv && (!WIN || g >= first), v1 = g + 8 < nv && (!WIN || g + 8 >= first);
         const float x0 = v0 ? (s[0] + s2[0]) * qscale : -INFINITY;  // token g, head 2t
         const float x1 = v0 ? (s[1] + s2[1]) * qscale : -INFINITY;  // token g, head 2t+1
         const float x2 = v1 ? (s[2] + s2[2]) * qscale : -INFINITY;  // token g+8, head 2t
@@ -571,8 +587,9 @@ struct MmaAttn {
         }
         // a column that has seen no token yet (m = -inf) takes p = 0, not
         // exp2(-inf + inf): the forked child's columns past its fork point
-        const float mr0 = (QH > GQ && m_run[0] == -INFINITY) ? 0.f : m_run[0];
-        const float mr1 = (QH > GQ && m_run[1] == -INFINITY) ? 0.f : m_run[1];
+        // (WIN: columns whose scores are all -inf so far likewise)
+        const float mr0 = ((QH > GQ || WIN) && m_run[0] == -INFINITY) ? 0.f : m_run[0];
+        const float mr1 = ((QH > GQ || WIN) && m_run[1] == -INFINITY) ? 0.f : m_run[1];
         const float p0 = fast_exp2(x0 - mr0), p1 = fast_exp2(x1 - mr1);
         const float p2 = fast_exp2(x2 - mr0), p3 = fast_exp2(x3 - mr1);
         lsum[0] += p0 + p2;

@@ -1,0 +1,506 @@
+// Paged decode attention with a sliding window and sinks for sm_103a.
+//
+// The one query of sequence b sits at the newest position L - 1 and sees the
+// first S tokens (sinks) and the last W (the window, itself included):
+//   o = sum_{j < S or L - W <= j < L} softmax(scale q . k_j) v_j
+// Blocks of the table none of whose tokens is visible are never read, so
+// their pages may have been freed and their entries may be anything.
+//
+// Bound: HBM on the visible K/V (a batch), latency (a few sequences).  What
+// is read is at most S + W tokens per sequence however long it is, so a
+// (sequence, KV head) item is small and the items of a batch are nearly
+// equal.  One thread-block cluster of C CTAs computes one item in one launch
+// without a workspace: the visible tiles are split evenly over the cluster's
+// warps; each warp streams its tiles through its own ring of shared-memory
+// stages (as the persistent decode kernel does) with a running maximum and
+// sum; the warps' results meet in shared memory, the CTAs' in distributed
+// shared memory, each CTA finishing 1/C of the item's output.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "pa_decode_tile.cuh"
+#include "pa_prefill.cuh"
+
+namespace {
+
+using namespace pa::dec;
+
+constexpr int kNW = 4;  // warps per CTA
+
+struct WindowParams {
+    void *out;
+    const void *q;
+    const uint8_t *k_cache, *v_cache;
+    const int32_t *block_table, *context_lens;
+    int *err;
+    int64_t num_blocks;
+    int B, Hq, Hkv, bs, bs_log2, MB, window, sinks;
+    float qscale;  // scale * log2(e)
+};
+
+template <typename T, int D, int GQ>
+struct TileOf {  // CUDA-core tile
+    using type = WarpAttn<T, D, GQ>;
+    static constexpr bool MMA = false;
+    static constexpr int STAGE = Cfg<T, D, GQ>::STAGE;
+    static constexpr int NST = Cfg<T, D, GQ>::NST;
+    static constexpr int PBUF = 2 * Cfg<T, D, GQ>::TT * GQ * 4;  // p and score buffers, per warp
+    static constexpr int MINB = 1;
+};
+template <int D, int GQ>
+struct TileOf<__nv_bfloat16, D, GQ> {  // tensor-core tile
+    using type = MmaAttn<D, GQ>;
+    static constexpr bool MMA = true;
+    static constexpr int STAGE = 2 * MmaCfg<D, GQ>::TILE;
+    static constexpr int NST = 24 * 1024 / STAGE;  // 24 KB per warp: two CTAs per SM
+    static constexpr int PBUF = 0;
+    static constexpr int MINB = 2;
+};
+
+template <typename T, int D, int GQ>
+struct Layout {
+    using TO = TileOf<T, D, GQ>;
+    static constexpr int WARP = TO::NST * TO::STAGE;  // ring of a warp, then its result
+    static constexpr int OFF_P = kNW * WARP;
+    static constexpr int OFF_CTA = OFF_P + kNW * TO::PBUF;   // the CTA's result: acc [GQ][D]
+    static constexpr int OFF_ML = OFF_CTA + GQ * D * 4;      // its (max, sum) [GQ]
+    static constexpr int OFF_WML = OFF_ML + GQ * 8;          // the warps' (max, sum) [kNW][GQ]
+    static constexpr int OFF_BAR = OFF_WML + kNW * GQ * 8;
+    static constexpr int SMEM = OFF_BAR + kNW * TO::NST * 8 + 1024;
+    static_assert(GQ * D * 4 <= WARP, "a warp's result must fit its ring");
+    static_assert(WARP % 1024 == 0, "swizzled stages must stay aligned");
+};
+
+__device__ __forceinline__ uint32_t cluster_ctarank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void store2(T *dst, float2 v);
+template <>
+__device__ __forceinline__ void store2<__nv_bfloat16>(__nv_bfloat16 *dst, float2 v) {
+    *reinterpret_cast<__nv_bfloat162 *>(dst) = __floats2bfloat162_rn(v.x, v.y);
+}
+template <>
+__device__ __forceinline__ void store2<float>(float *dst, float2 v) {
+    *reinterpret_cast<float2 *>(dst) = v;
+}
+
+// The visible tiles of one sequence: ns sink tiles from token 0, then nw
+// window tiles from token wbase; lo is the window's first token.  With the
+// window reaching the sinks there is one range from token 0.
+struct Visible {
+    int L, lo, S, ns, nw, wbase;
+    __device__ __forceinline__ int first_token(int t, int TT) const {
+        return t < ns ? t * TT : wbase + (t - ns) * TT;
+    }
+    // visible tokens [a, b) of the TT (or fewer) tokens from tok on of tile t
+    __device__ __forceinline__ void rows(int t, int tok, int n, int *a, int *b) const {
+        *a = max(0, (t < ns ? 0 : lo) - tok);
+        *b = min(n, (t < ns ? S : L) - tok);
+    }
+};
+
+// A warp's result (max, sum per head, unnormalised acc [GQ][D]) into acc/ml.
+template <int D, int GQ>
+__device__ __forceinline__ void put_result(MmaAttn<D, GQ> &st, float *acc, float2 *ml) {
+    float lh[2];
+    st.reduce(lh);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int h = 2 * st.t + j;
+        if (h >= GQ) continue;
+#pragma unroll
+        for (int m = 0; m < D / 16; ++m) {
+            acc[h * D + 16 * m + st.g] = st.acc[m][j];
+            acc[h * D + 16 * m + st.g + 8] = st.acc[m][2 + j];
+        }
+        if (st.g == 0) ml[h] = make_float2(st.m_run[j], lh[j]);
+    }
+}
+template <typename T, int D, int GQ>
+__device__ __forceinline__ void put_result(WarpAttn<T, D, GQ> &st, float *acc, float2 *ml) {
+    float lh[GQ];
+    st.reduce(lh);
+    st.store_partial(acc, D, reinterpret_cast<float *>(ml), 2, lh);
+}
+
+// weight of a partial with maximum m under the common maximum M (0 for an
+// empty one; also when every partial is empty)
+__device__ __forceinline__ float weight(float m, float M) {
+    return m == -INFINITY ? 0.f : exp2f(m - M);
+}
+
+template <typename T, int D, int GQ>
+__global__ void __launch_bounds__(kNW * 32, (TileOf<T, D, GQ>::MINB))
+    decode_window_kernel(const WindowParams p, const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap) {
+    using TO = TileOf<T, D, GQ>;
+    using Lay = Layout<T, D, GQ>;
+    using St = typename TO::type;
+    constexpr int TT = St::C::TT;
+    constexpr int NST = TO::NST;
+    constexpr int ROW = D * int(sizeof(T));
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *ring = smem + warp * Lay::WARP;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::OFF_BAR) + warp * NST;
+    float *pbuf = reinterpret_cast<float *>(smem + Lay::OFF_P + warp * TO::PBUF);
+    float2 *wml = reinterpret_cast<float2 *>(smem + Lay::OFF_WML);
+    const int C = cluster_nctarank(), rank = cluster_ctarank();
+    const int item = blockIdx.x / C, b = item / p.Hkv, hk = item % p.Hkv;
+    if (lane == 0) {
+        for (int s = 0; s < NST; ++s) pa::mbar_init(&bars[s], 1);
+        pa::fence_barrier_init();
+    }
+    __syncwarp();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // ---- the visible tiles and this warp's share ------------------------------
+    Visible vis;
+    vis.L = p.context_lens[b];
+    const int cap = p.MB << p.bs_log2;
+    if (vis.L < 0 || vis.L > cap) {
+        if (threadIdx.x == 0) pa::record_error(p.err, PA_DEVERR_BAD_BLOCK);
+        vis.L = vis.L < 0 ? 0 : cap;
+    }
+    vis.lo = max(0, vis.L - p.window);
+    vis.S = p.sinks;
+    if (vis.lo <= vis.S) vis.lo = vis.S = 0;
+    vis.ns = (vis.S + TT - 1) / TT;
+    vis.wbase = vis.lo / TT * TT;
+    vis.nw = (vis.L - vis.wbase + TT - 1) / TT;
+    const int nt = vis.ns + vis.nw, parts = C * kNW, part = rank * kNW + warp;
+    const int t0 = static_cast<int>(int64_t(nt) * part / parts);
+    const int t1 = static_cast<int>(int64_t(nt) * (part + 1) / parts);
+
+    St st;
+    st.init(lane);
+    st.reset();
+    if (t0 < t1)
+        st.load_q(static_cast<const T *>(p.q) + (static_cast<size_t>(b) * p.Hq + hk * GQ) * D,
+                  p.qscale);
+
+    // ---- block-table entries: 32 (tile, block) slots at a time, one per lane,
+    //      the next batch loaded one batch ahead; -1: nothing to copy ----------
+    const int nb = max(1, TT >> p.bs_log2), tpb = 32 / nb;  // blocks per tile, tiles per batch
+    const int32_t *bt_row = p.block_table + static_cast<size_t>(b) * p.MB;
+    auto fetch = [&](int tb) -> int {
+        const int t = tb + lane / nb;
+        if (t >= t1) return -1;
+        const int tok0 = vis.first_token(t, TT), tok = tok0 + (lane % nb) * p.bs;
+        int a, e;
+        vis.rows(t, tok0, TT, &a, &e);
+        // the slot's block covers rows [tok - tok0, tok - tok0 + bs) of the tile
+        if (tok - tok0 >= e || (nb > 1 && tok - tok0 + p.bs <= a)) return -1;
+        int v = __ldg(bt_row + (tok >> p.bs_log2));
+        if (v < 0 || v >= p.num_blocks) {
+            pa::record_error(p.err, PA_DEVERR_BAD_BLOCK);
+            v = 0;
+        }
+        return v;
+    };
+    int ent = fetch(t0), ent_next = fetch(t0 + tpb), tb = t0;
+    // copies of tile t into its stage (t ascending, each once; whole warp)
+    auto issue = [&](int t) {
+        if (t - tb >= tpb) {
+            tb += tpb;
+            ent = ent_next;
+            ent_next = fetch(tb + tpb);
+        }
+        const int s = (t - t0) % NST, slot0 = (t - tb) * nb;
+        uint8_t *stage = ring + s * TO::STAGE;
+        const uint32_t sk = pa::smem_u32(stage), sv = sk + TO::STAGE / 2;
+        const int rows = min(TT, p.bs);  // rows of one copy
+        const unsigned live = __ballot_sync(pa::kFull, ent >= 0) >> slot0;
+        const int copies = __popc(live & ((1u << nb) - 1u));
+        const int r0 = nb > 1 ? 0 : vis.first_token(t, TT) & (p.bs - 1);
+        if (lane == 0) pa::mbar_arrive_expect_tx(&bars[s], 2u * copies * rows * ROW);
+        for (int j = 0; j < nb; ++j) {
+            const int blk = __shfl_sync(pa::kFull, ent, slot0 + j);
+            if (lane != 0 || blk < 0) continue;
+            const int64_t row = ((static_cast<int64_t>(blk) * p.Hkv + hk) << p.bs_log2) + r0;
+            if constexpr (TO::MMA) {
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) {
+                    const uint32_t off = h * TT * 128 + j * rows * 128;
+                    pa::tma_2d_g2s(sk + off, &kmap, 64 * h, static_cast<int>(row), &bars[s]);
+                    pa::tma_2d_g2s(sv + off, &vmap, 64 * h, static_cast<int>(row), &bars[s]);
+                }
+            } else {
+                const uint32_t bytes = static_cast<uint32_t>(rows) * ROW;
+                pa::bulk_g2s(stage + j * bytes, p.k_cache + row * ROW, bytes, &bars[s]);
+                pa::bulk_g2s(stage + TO::STAGE / 2 + j * bytes, p.v_cache + row * ROW, bytes,
+                             &bars[s]);
+            }
+        }
+    };
+    for (int t = t0; t < min(t1, t0 + NST); ++t) issue(t);
+
+    bool ok = true;
+    for (int t = t0; t < t1; ++t) {
+        const int i = t - t0, s = i % NST;
+        ok = __all_sync(pa::kFull, pa::mbar_wait(&bars[s], (i / NST) & 1));
+        if (!ok) {
+            // a copy never completed: record it, wait (bounded) for the others
+            // in flight, and meet the other warps with what there is
+            if (lane == 0) {
+                pa::record_error(p.err, PA_DEVERR_TIMEOUT);
+                for (int k = i + 1; k < min(i + NST, t1 - t0); ++k)
+                    (void)pa::mbar_wait(&bars[k % NST], (k / NST) & 1);
+            }
+            __syncwarp();
+            break;
+        }
+        const uint32_t kaddr = pa::smem_u32(ring + s * TO::STAGE);
+        int a, e;
+        vis.rows(t, vis.first_token(t, TT), TT, &a, &e);
+        if constexpr (TO::MMA)
+            st.template tile<true>(kaddr, kaddr + TO::STAGE / 2, e, nullptr, nullptr, 0, a);
+        else
+            st.template tile<true>(kaddr, kaddr + TO::STAGE / 2, e, pbuf, pbuf + TT * GQ, a);
+        __syncwarp();
+        if (t + NST < t1) {
+            pa::fence_proxy_async();
+            issue(t + NST);
+        }
+    }
+
+    // ---- the CTA's result -------------------------------------------------------
+    __syncwarp();
+    put_result(st, reinterpret_cast<float *>(ring), wml + warp * GQ);
+    __syncthreads();
+    float *cta_acc = reinterpret_cast<float *>(smem + Lay::OFF_CTA);
+    float2 *cta_ml = reinterpret_cast<float2 *>(smem + Lay::OFF_ML);
+    T *out = static_cast<T *>(p.out) + (static_cast<size_t>(b) * p.Hq + hk * GQ) * D;
+    for (int x = threadIdx.x * 2; x < GQ * D; x += kNW * 64) {
+        const int h = x / D;
+        float M = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kNW; ++w) M = fmaxf(M, wml[w * GQ + h].x);
+        float2 a = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kNW; ++w) {
+            const float2 ml = wml[w * GQ + h];
+            const float f = weight(ml.x, M);
+            const float2 v = *reinterpret_cast<const float2 *>(smem + w * Lay::WARP + x * 4);
+            l += f * ml.y;
+            a = pa::ffma2(make_float2(f, f), v, a);
+        }
+        if (C == 1) {
+            const float inv = vis.L > 0 ? 1.f / l : 0.f;
+            store2(out + x, make_float2(a.x * inv, a.y * inv));
+        } else {
+            *reinterpret_cast<float2 *>(cta_acc + x) = a;
+            if (x % D == 0) cta_ml[h] = make_float2(M, l);
+        }
+    }
+    if (C == 1) return;
+    // ---- the cluster's result: this CTA finishes 1/C of the item's outputs ------
+    cluster_sync();
+    const int share = GQ * D / C;  // a multiple of 2: GQ * D >= 64, C <= 16
+    for (int x = rank * share + threadIdx.x * 2; x < (rank + 1) * share; x += kNW * 64) {
+        const int h = x / D;
+        const uint32_t aa = pa::smem_u32(cta_acc + x), am = pa::smem_u32(cta_ml + h);
+        float M = -INFINITY, l = 0.f;
+        for (int c = 0; c < C; ++c) M = fmaxf(M, ld_cluster2(map_cta(am, c)).x);
+        float2 a = make_float2(0.f, 0.f);
+        for (int c = 0; c < C; ++c) {
+            const float2 ml = ld_cluster2(map_cta(am, c)), v = ld_cluster2(map_cta(aa, c));
+            const float f = weight(ml.x, M);
+            l += f * ml.y;
+            a = pa::ffma2(make_float2(f, f), v, a);
+        }
+        const float inv = vis.L > 0 ? 1.f / l : 0.f;
+        store2(out + x, make_float2(a.x * inv, a.y * inv));
+    }
+    cluster_sync();  // the others may still read this CTA's result
+}
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return sms;
+}
+
+template <typename T, int D, int GQ>
+int launch(const WindowParams &p, cudaStream_t stream) {
+    using TO = TileOf<T, D, GQ>;
+    using Lay = Layout<T, D, GQ>;
+    constexpr int TT = TO::type::C::TT;
+    CUtensorMap kmap{}, vmap{};
+    if constexpr (TO::MMA) {
+        const int64_t rows = (p.num_blocks * p.Hkv) << p.bs_log2;
+        const int box = std::min(TT, p.bs);
+        if (int rc = pa::pool_tensor_map(&kmap, p.k_cache, rows, D, box)) return rc;
+        if (int rc = pa::pool_tensor_map(&vmap, p.v_cache, rows, D, box)) return rc;
+    }
+    auto kern = decode_window_kernel<T, D, GQ>;
+    static std::atomic<uint64_t> smem_done{0};
+    if (int rc = pa::pf::set_smem_once(kern, Lay::SMEM, &smem_done)) return rc;
+    const int sms = sm_count();
+    if (sms <= 0) return pa::fail(PA_ERR_CUDA, "decode_window: no SM count");
+    // cluster size: enough CTAs for two per SM, at least two tiles per warp
+    const int64_t items = int64_t(p.B) * p.Hkv;
+    const int64_t tokens = std::min<int64_t>(int64_t(p.MB) << p.bs_log2, int64_t(p.sinks) + p.window);
+    const int64_t tiles = (tokens + TT - 1) / TT;
+    int c = 1;
+    while (c < 8 && items * c < 2 * sms && tiles >= 2 * kNW * 2 * c) c *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(items * c));
+    cfg.blockDim = dim3(kNW * 32);
+    cfg.dynamicSmemBytes = Lay::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(c), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    (void)cudaGetLastError();  // drop a stale error that is not ours
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, kmap, vmap);
+    if (e != cudaSuccess) return pa::cuda_fail(e, "decode_window launch");
+    return pa::check_launch("decode_window launch");
+}
+
+template <typename T, int D>
+int dispatch(int gq, const WindowParams &p, cudaStream_t s) {
+    switch (gq) {
+        case 1: return launch<T, D, 1>(p, s);
+        case 2: return launch<T, D, 2>(p, s);
+        case 4: return launch<T, D, 4>(p, s);
+        default: return launch<T, D, 8>(p, s);
+    }
+}
+
+}  // namespace
+
+namespace pa {
+
+// Validate mode of the windowed calls: lengths in [0, capacity] and every
+// block with a token visible to the first query (or a later one) in the pool.
+int validate_window(const int32_t *block_table, int MB, const int32_t *context_lens,
+                    const int32_t *query_start, int B, int bs, int64_t num_blocks, int window,
+                    int sinks, cudaStream_t stream) try {
+    std::vector<int32_t> lens(B), table(size_t(B) * MB), qs;
+    if (int rc = fetch(lens.data(), context_lens, lens.size() * 4, stream)) return rc;
+    if (int rc = fetch(table.data(), block_table, table.size() * 4, stream)) return rc;
+    if (query_start) {
+        qs.resize(size_t(B) + 1);
+        if (int rc = fetch(qs.data(), query_start, qs.size() * 4, stream)) return rc;
+    }
+    for (int b = 0; b < B; ++b) {
+        const int64_t L = lens[b], n = query_start ? int64_t(qs[b + 1]) - qs[b] : 1;
+        if (L < 0 || L > int64_t(MB) * bs)
+            return fail(PA_ERR_INVALID, "validate: context_lens[%d]=%lld outside [0,%lld]", b,
+                        (long long)L, (long long)MB * bs);
+        if (query_start && (n < 0 || n > L))
+            return fail(PA_ERR_INVALID, "validate: request %d has %lld new tokens of %lld", b,
+                        (long long)n, (long long)L);
+        if (L == 0 || n == 0) continue;
+        const int64_t lo = std::max<int64_t>(0, L - n - window + 1);
+        for (int64_t i = 0; i < (L + bs - 1) / bs; ++i) {
+            if (i * bs >= sinks && std::min<int64_t>((i + 1) * bs, L) <= lo) continue;
+            const int32_t v = table[size_t(b) * MB + i];
+            if (v < 0 || v >= num_blocks)
+                return fail(PA_ERR_INVALID, "validate: block_table[%d][%lld]=%d outside pool", b,
+                            (long long)i, v);
+        }
+    }
+    return PA_OK;
+} catch (const std::bad_alloc &) {
+    return fail(PA_ERR_OOM, "validate: host allocation failed");
+}
+
+}  // namespace pa
+
+extern "C" int pa_decode_window(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *block_table, int max_blocks_per_seq,
+                                const int32_t *context_lens, int B, int Hq, int Hkv, int head_dim,
+                                int block_size, int64_t num_blocks, float scale, int window,
+                                int num_sinks, int dtype, pa_stream_t stream) {
+    pa::clear_error();
+    if (dtype != PA_BF16 && dtype != PA_F32)
+        return pa::fail(PA_ERR_INVALID, "decode_window: bad dtype");
+    if (B < 0 || B > 65535 || Hq <= 0 || Hkv <= 0 || Hkv > 1024 || Hq % Hkv || num_blocks <= 0 ||
+        max_blocks_per_seq <= 0)
+        return pa::fail(PA_ERR_INVALID, "decode_window: bad sizes");
+    if (head_dim != 64 && head_dim != 128)
+        return pa::fail(PA_ERR_UNSUPPORTED, "decode_window: head_dim %d unsupported", head_dim);
+    const int gq = Hq / Hkv;
+    if (gq != 1 && gq != 2 && gq != 4 && gq != 8)
+        return pa::fail(PA_ERR_UNSUPPORTED, "decode_window: Hq/Hkv=%d unsupported", gq);
+    if (!pa::pow2_in(block_size, 8, 128))
+        return pa::fail(PA_ERR_UNSUPPORTED, "decode_window: block_size %d unsupported", block_size);
+    if (int64_t(max_blocks_per_seq) * block_size > (int64_t(1) << 30))
+        return pa::fail(PA_ERR_INVALID, "decode_window: table capacity too large");
+    if (num_blocks > INT32_MAX || num_blocks * Hkv * block_size > int64_t(INT32_MAX))
+        return pa::fail(PA_ERR_UNSUPPORTED, "decode_window: pools of 2^31 rows or more");
+    if (window < 1 || num_sinks < 0)
+        return pa::fail(PA_ERR_INVALID, "decode_window: window %d must be positive, num_sinks %d "
+                                        "not negative", window, num_sinks);
+    if (!(scale > 0.f) || !std::isfinite(scale))
+        return pa::fail(PA_ERR_INVALID, "decode_window: scale must be positive and finite");
+    if (B == 0) return PA_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_table || !context_lens)
+        return pa::fail(PA_ERR_INVALID, "decode_window: NULL pointer");
+    if (!pa::aligned16(q) || !pa::aligned16(out) || !pa::aligned16(k_cache) ||
+        !pa::aligned16(v_cache))
+        return pa::fail(PA_ERR_INVALID, "decode_window: q, out and pools must be 16-byte aligned");
+    if (pa::validate_on())
+        if (int rc = pa::validate_window(block_table, max_blocks_per_seq, context_lens, nullptr, B,
+                                         block_size, num_blocks, window, num_sinks, stream))
+            return rc;
+    WindowParams p{};
+    p.out = out;
+    p.q = q;
+    p.k_cache = static_cast<const uint8_t *>(k_cache);
+    p.v_cache = static_cast<const uint8_t *>(v_cache);
+    p.block_table = block_table;
+    p.context_lens = context_lens;
+    p.err = pa::device_error_word();
+    p.num_blocks = num_blocks;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.bs = block_size;
+    while ((1 << p.bs_log2) < block_size) ++p.bs_log2;
+    p.MB = max_blocks_per_seq;
+    p.window = window;
+    p.sinks = num_sinks;
+    p.qscale = scale * kLog2e;
+    if (dtype == PA_BF16)
+        return head_dim == 128 ? dispatch<__nv_bfloat16, 128>(gq, p, stream)
+                               : dispatch<__nv_bfloat16, 64>(gq, p, stream);
+    return head_dim == 128 ? dispatch<float, 128>(gq, p, stream)
+                           : dispatch<float, 64>(gq, p, stream);
+}

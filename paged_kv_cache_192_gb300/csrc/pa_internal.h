@@ -74,4 +74,14 @@ int launch_prefix_tc(const PrefixTcArgs &a, cudaStream_t stream);
 // (validate mode only).
 int fetch(void *host, const void *dev, size_t bytes, cudaStream_t stream);
 
+// Validate mode: slots inside the pool (or negative) and no slot twice.
+int validate_slots(const int64_t *slots, int64_t T, int64_t num_blocks, int block_size,
+                   cudaStream_t stream);
+
+// Validate mode of the windowed calls (pa_decode_window.cu); query_start is
+// NULL for a decode (one query per sequence).
+int validate_window(const int32_t *block_table, int MB, const int32_t *context_lens,
+                    const int32_t *query_start, int B, int bs, int64_t num_blocks, int window,
+                    int sinks, cudaStream_t stream);
+
 }  // namespace pa

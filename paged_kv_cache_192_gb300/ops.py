@@ -9,6 +9,7 @@ allocates).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -42,6 +43,14 @@ def _require(cond: bool, msg: str):
         raise ValueError(msg)
 
 
+def _int32(x, name) -> int:
+    """A host integer of the C ABI (ctypes would wrap a larger one)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name}={x} does not fit 32 bits")
+    return x
+
+
 def _pairs_ok(pairs) -> bool:
     return pairs.numel() == 0 or (pairs.dim() == 2 and pairs.shape[1] == 2)
 
@@ -49,6 +58,27 @@ def _pairs_ok(pairs) -> bool:
 def _stream(stream=None) -> int:
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
+
+
+def _on_current_device(*tensors, stream=None):
+    """The library launches on the current device: the tensors of the call
+    (and its stream) must belong to it."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t.get_device() != cur:
+            raise ValueError(f"tensors must be on the current device cuda:{cur}, "
+                             f"got cuda:{t.get_device()}")
+    if stream is not None and stream.device.index != cur:
+        raise ValueError(f"stream must belong to the current device cuda:{cur}")
+
+
+def _new(shape, like, stream):
+    """An output tensor, allocated on the stream that will write it (memory
+    that earlier work of that stream freed is then reused in its order)."""
+    if stream is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
 
 
 def set_validate(on: bool):
@@ -92,6 +122,72 @@ def reshape_and_cache(k_new, v_new, k_cache, v_cache, slot_mapping, stream=None)
         _stream(stream)))
 
 
+def _token_rows(t, name, T, H, d):
+    """Elements between tokens of [T][H][d] whose heads are contiguous."""
+    _require(t.dim() == 3 and t.shape == (T, H, d), f"{name} must be [{T}][{H}][{d}]")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return s0 if T > 1 else H * d
+
+
+def _cuda_rows(t, name, dtype):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=64)
+def _int_array(values):
+    return (ctypes.c_int * len(values))(*values)
+
+
+def rope_reshape_and_cache(q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, inv_freq,
+                           sections=None, interleaved=False, q_out=None, stream=None):
+    """Rotary positions and the store of the new rows in one launch
+    (pa_rope_reshape_and_cache).
+
+    q: [T][Hq][d]; k_new, v_new: [T][Hkv][d], the pools' dtype, the heads of a
+    token contiguous (slices of a fused projection are fine).  q and k_new are
+    rotated by their positions; k_new and v_new go to their slots (int64 [T],
+    negative: not stored).  positions: int64 [T], or [axes][T] with the number
+    of frequencies of each axis in `sections`.  inv_freq: float32 [rot/2];
+    elements from rot on are copied.  Pairs are (i, i + rot/2), or (2i, 2i + 1)
+    if interleaved.  Returns the rotated queries (q_out, which may be q)."""
+    _require(q.dim() == 3 and k_new.dim() == 3 and k_cache.dim() == 4,
+             "q must be [T][Hq][d], k_new and v_new [T][Hkv][d], pools [NB][Hkv][bs][d]")
+    NB, Hkv, bs, d = k_cache.shape
+    T, Hq = q.shape[0], q.shape[1]
+    _require(v_cache.shape == k_cache.shape, "k_cache and v_cache must have the same shape")
+    _require(slot_mapping.shape == (T,), f"slot_mapping must be [{T}]")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    _require(positions.dim() in (1, 2) and positions.shape[-1] == T,
+             f"positions must be [{T}] or [axes][{T}]")
+    _require(inv_freq.dim() == 1, "inv_freq must be [rot/2]")
+    half = inv_freq.shape[0]
+    sections = (half,) if sections is None else tuple(int(x) for x in sections)
+    _require(len(sections) == axes, f"sections must name the frequencies of each of {axes} axes")
+    qs = _token_rows(q, "q", T, Hq, d)
+    ks = _token_rows(k_new, "k_new", T, Hkv, d)
+    vs = _token_rows(v_new, "v_new", T, Hkv, d)
+    os_ = Hq * d if q_out is None else _token_rows(q_out, "q_out", T, Hq, d)
+    dt = k_cache.dtype
+    args = (_cuda_rows(q, "q", dt), qs, _cuda_rows(k_new, "k_new", dt), ks,
+            _cuda_rows(v_new, "v_new", dt), vs, _cuda(k_cache, "k_cache"),
+            _cuda(v_cache, "v_cache", dt), _cuda(slot_mapping, "slot_mapping", torch.int64),
+            _cuda(positions, "positions", torch.int64), _cuda(inv_freq, "inv_freq", torch.float32))
+    _on_current_device(q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, inv_freq,
+                       *(() if q_out is None else (q_out,)), stream=stream)
+    if q_out is None:
+        q_out = _new((T, Hq, d), q, stream)
+    check(lib().pa_rope_reshape_and_cache(
+        _cuda_rows(q_out, "q_out", dt), os_, *args, _int_array(sections), axes, bool(interleaved),
+        T, NB, Hq, Hkv, bs, d, 2 * half, _dt(k_cache), _stream(stream)))
+    return q_out
+
+
 def copy_blocks(k_cache, v_cache, pairs, stream=None):
     """Copy-on-write copies (pa_copy_blocks): for each row (src, dst) of the
     int64 [n][2] device tensor `pairs`, block dst of both pools becomes a byte
@@ -130,6 +226,34 @@ def swap_blocks(dst_k, dst_v, src_k, src_v, pairs, stream=None):
     check(lib().pa_swap_blocks(dst_k.data_ptr(), dst_v.data_ptr(), src_k.data_ptr(),
                                src_v.data_ptr(), pairs.data_ptr() if n else None, n, NBs, NBd,
                                Hkv, bs, d, _dt(src_k), _stream(stream)))
+
+
+def compact_cache(k_cache, v_cache, src_table, dst_table, keep, keep_lens, stream=None):
+    """Keep some tokens of each sequence and move them to its front
+    (pa_compact_cache), in place or into other pages.
+
+    src_table, dst_table: int32 [B][blocks], the pages before and after (the
+    same page at the same logical block is compacted in place; other pages
+    written must not be read by the call).  keep: int32 [B][Hkv][max_keep],
+    for each KV head the kept positions in ascending order; keep_lens: int32
+    [B], how many of them count.  The pools are written in place, bit exact."""
+    _require(k_cache.dim() == 4, "pools must be [NB][Hkv][bs][d]")
+    NB, Hkv, bs, d = k_cache.shape
+    _require(v_cache.shape == k_cache.shape, "k_cache and v_cache must have the same shape")
+    _require(keep.dim() == 3 and keep.shape[1] == Hkv, f"keep must be [B][{Hkv}][max_keep]")
+    B, max_keep = keep.shape[0], keep.shape[2]
+    _require(src_table.dim() == 2 and src_table.shape[0] == B and src_table.shape[1] > 0,
+             f"src_table must be [{B}][blocks]")
+    _require(dst_table.dim() == 2 and dst_table.shape[0] == B and dst_table.shape[1] > 0,
+             f"dst_table must be [{B}][blocks]")
+    _require(keep_lens.shape == (B,), f"keep_lens must be [{B}]")
+    args = (_cuda(k_cache, "k_cache"), _cuda(v_cache, "v_cache", k_cache.dtype),
+            _cuda(src_table, "src_table", torch.int32), src_table.shape[1],
+            _cuda(dst_table, "dst_table", torch.int32), dst_table.shape[1],
+            _cuda(keep, "keep", torch.int32), max_keep,
+            _cuda(keep_lens, "keep_lens", torch.int32))
+    _on_current_device(k_cache, v_cache, src_table, dst_table, keep, keep_lens, stream=stream)
+    check(lib().pa_compact_cache(*args, B, NB, Hkv, bs, d, _dt(k_cache), _stream(stream)))
 
 
 def decode_workspace_size(B, Hq, head_dim, max_blocks_per_seq, block_size, partition_tokens=0):
@@ -363,6 +487,33 @@ def decode_noalloc(q, k_cache, v_cache, block_table, context_lens, scale=None,
         _cuda(v_cache, "v_cache", k_cache.dtype), _cuda(block_table, "block_table", torch.int32),
         block_table.shape[1], _cuda(context_lens, "context_lens", torch.int32), B, Hq, Hkv, d,
         bs, NB, scale, partition_tokens, _dt(q), _stream(stream)))
+    return out
+
+
+def decode_window(q, k_cache, v_cache, block_table, context_lens, window, num_sinks=0, scale=None,
+                  out=None, stream=None):
+    """Paged decode attention with a sliding window and sinks (pa_decode_window).
+
+    As decode, but the query of a sequence of length L sees only its first
+    num_sinks tokens and its last `window` (the newest included).  Entries of
+    block_table whose block holds no visible token are not read (the page may
+    have been freed); a row of length 0 gets zeros.  No workspace.  Returns
+    out [B][Hq][d]."""
+    _check_decode_shapes(q, k_cache, v_cache, block_table, context_lens, out)
+    B, Hq, d = q.shape
+    NB, Hkv, bs, _ = k_cache.shape
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    args = (_cuda(q, "q", k_cache.dtype), _cuda(k_cache, "k_cache"),
+            _cuda(v_cache, "v_cache", k_cache.dtype),
+            _cuda(block_table, "block_table", torch.int32), block_table.shape[1],
+            _cuda(context_lens, "context_lens", torch.int32))
+    _on_current_device(q, k_cache, v_cache, block_table, context_lens,
+                       *(() if out is None else (out,)), stream=stream)
+    if out is None:
+        out = _new(q.shape, q, stream)
+    check(lib().pa_decode_window(
+        _cuda(out, "out", q.dtype), *args, B, Hq, Hkv, d, bs, NB, scale, _int32(window, "window"),
+        _int32(num_sinks, "num_sinks"), _dt(q), _stream(stream)))
     return out
 
 
