@@ -485,6 +485,36 @@ int pa_prefill_chunk(void *out, const void *q, const void *k_cache, const void *
                      int max_query_len, int Hq, int Hkv, int head_dim, int block_size,
                      int64_t num_blocks, float scale, int dtype, pa_stream_t stream);
 
+/*
+ * pa_prefill_window -- pa_prefill_chunk with a sliding window and sinks: new
+ * token i of request r, at position p = P_r + i, sees the tokens j <= p with
+ *   j < num_sinks  or  j > p - window.
+ *   out, q        [total_tokens][Hq][head_dim]  (bf16 only); rows outside every
+ *                 request are left as they are
+ *   query_start   int32 [R+1] prefix sum of new-token counts, inside
+ *                 [0, total_tokens]; a request may have no new tokens
+ *   total_tokens  rows of q and out
+ *   max_query_len host int >= every request's new tokens (sizes the grid)
+ *   window        at least 1; num_sinks at least 0 (both may exceed the context)
+ *   block_table   entries of blocks that no new token of the request sees are
+ *                 never read: their pages may have been freed (pa_bm_trim)
+ * Any block size and table length that pa_decode_window takes.  K and V of
+ * tokens that no new token of a request sees (slots never written, tokens
+ * before the first query's window) do not enter its rows, whatever they hold;
+ * a NaN or infinity in a token that one of them sees may also reach the rows
+ * of the same request that do not.
+ * Other arguments and the error bound as for pa_prefill_chunk.  A request whose
+ * lengths do not fit (context outside [new tokens, capacity], rows outside
+ * [0, total_tokens]) is left out and PA_DEVERR_BAD_BLOCK recorded.  One launch
+ * per 1024 requests.
+ */
+int pa_prefill_window(void *out, const void *q, const void *k_cache, const void *v_cache,
+                      const int32_t *block_table, int max_blocks_per_seq,
+                      const int32_t *query_start, const int32_t *context_lens, int R,
+                      int total_tokens, int max_query_len, int Hq, int Hkv, int head_dim,
+                      int block_size, int64_t num_blocks, float scale, int window, int num_sinks,
+                      int dtype, pa_stream_t stream);
+
 /* kernels pa_prefill_chunk can launch (pa_prefill_kernel_for) */
 enum { PA_PREFILL_PERSISTENT_GRID = 1, PA_PREFILL_ITEM_GRID = 2, PA_PREFILL_SIMPLE = 3 };
 

@@ -75,6 +75,9 @@ SIGNATURES = {
     "pa_prefill_chunk": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_int,
                                   _c_int, _c_int, _c_int, _c_int, _c_int, _c_i64, _c_f, _c_int,
                                   _c_vp]),
+    "pa_prefill_window": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_int,
+                                   _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_i64, _c_f,
+                                   _c_int, _c_int, _c_int, _c_vp]),
     "pa_prefill_kernel_for": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_i64,
                                        _c_int, ctypes.POINTER(_c_int)]),
     "pa_bm_create": (_c_int, [_c_i64, _c_int, ctypes.c_uint64, ctypes.POINTER(_c_vp)]),

@@ -1,5 +1,5 @@
 """Refusals of the bounded-cache calls (rotary store, compaction, windowed
-decode): mismatched shapes by the binding before any pointer reaches the
+decode and prefill): mismatched shapes by the binding before any pointer reaches the
 library, bad sizes by the library before it touches CUDA.  CPU only."""
 import ctypes
 
@@ -107,6 +107,31 @@ def test_decode_window_then_device_check():
         ops.decode_window(**window_args())
 
 
+def prefill_args(R=3, T=10):
+    k, v = pools()
+    return dict(q=torch.zeros(T, 4, 64, dtype=bf16), k_cache=k, v_cache=v,
+                block_table=torch.zeros(R, 4, dtype=i32), query_start=torch.zeros(R + 1, dtype=i32),
+                context_lens=torch.ones(R, dtype=i32), max_query_len=10, window=16)
+
+
+@pytest.mark.parametrize("bad,msg", [
+    (dict(out=torch.zeros(9, 4, 64, dtype=bf16)), "out must have the shape of q"),
+    (dict(block_table=torch.zeros(2, 4, dtype=i32)), "block_table must be"),
+    (dict(query_start=torch.zeros(3, dtype=i32)), "query_start must be"),
+    (dict(context_lens=torch.ones(3, 1, dtype=i32)), "context_lens"),
+    (dict(q=torch.zeros(10, 4, 128, dtype=bf16)), "head_dim"),
+    (dict(v_cache=torch.zeros(8, 2, 8, 64, dtype=bf16)), "same shape"),
+])
+def test_prefill_window_rejects_mismatched_tensors(bad, msg):
+    with pytest.raises(ValueError, match=msg):
+        ops.prefill_window(**{**prefill_args(), **bad})
+
+
+def test_prefill_window_then_device_check():
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        ops.prefill_window(**prefill_args())
+
+
 # ---- the C ABI ------------------------------------------------------------------
 P = ctypes.c_void_p
 
@@ -182,6 +207,25 @@ WINDOW_REFUSALS = [
 @pytest.mark.parametrize("kw,code", WINDOW_REFUSALS)
 def test_decode_window_c_refusals(lib, kw, code):
     assert c_window(lib, **kw) == code
+    assert bool(lib.pa_last_error_string()) == (code != 0)
+
+
+def c_prefill(lib, **kw):
+    a = dict(MB=4, R=2, T=10, mq=5, Hq=4, Hkv=4, d=64, bs=16, NB=8, scale=0.125, window=8, sinks=0,
+             dtype=0, ptr=None)
+    a.update(kw)
+    p = a["ptr"]
+    return lib.pa_prefill_window(p, p, p, p, p, a["MB"], p, p, a["R"], a["T"], a["mq"], a["Hq"],
+                                 a["Hkv"], a["d"], a["bs"], a["NB"], a["scale"], a["window"],
+                                 a["sinks"], a["dtype"], None)
+
+
+@pytest.mark.parametrize("kw,code", [x for x in WINDOW_REFUSALS if "B" not in x[0]] + [
+    (dict(dtype=1), 4), (dict(R=-1), 1), (dict(T=-1), 1), (dict(mq=-1), 1), (dict(R=0), 0),
+    (dict(T=0), 0), (dict(mq=0), 0), (dict(T=2 ** 31 - 1, Hq=1024, Hkv=1024), 4),
+])
+def test_prefill_window_c_refusals(lib, kw, code):
+    assert c_prefill(lib, **kw) == code
     assert bool(lib.pa_last_error_string()) == (code != 0)
 
 
