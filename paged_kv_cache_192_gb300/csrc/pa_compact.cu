@@ -7,11 +7,15 @@
 // head with K and V).
 //
 // In place, a row that is read may lie where an earlier row is written.  The
-// positions are ascending, so row i comes from position keep[i] >= i: one CTA
-// walks the rows of its (sequence, head, cache, column slice) in order, reads
-// a chunk of rows [i0, i1) into registers, and writes it after a barrier.
-// Later chunks read positions >= i1 only, which this chunk does not write,
-// and what it overwrites was read by this chunk or an earlier one.
+// positions are ascending, so row i comes from position keep[i] >= i: the rows
+// of a (sequence, head, cache) are walked in order, a chunk of rows [i0, i1) is
+// read into registers and written after a barrier.  Later chunks read
+// positions >= i1 only, which this chunk does not write, and what it
+// overwrites was read by this chunk or an earlier one.  So only reads wait for
+// one another, and the next chunk's positions and pages are fetched while this
+// chunk's rows are on their way: one memory latency per chunk.  One CTA walks a
+// list when there are many; a cluster of CTAs takes larger chunks together
+// (its barrier in the CTA barrier's place) when there are few.
 #include <new>
 #include <unordered_map>
 #include <unordered_set>
@@ -23,67 +27,98 @@
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 8;  // 16-byte pieces in flight per thread
+constexpr int kRows = 4;  // 16-byte pieces in flight per thread
 
 struct CompactParams {
     uint8_t *k_cache, *v_cache;
     const int32_t *src_table, *dst_table, *keep, *keep_lens;
     int64_t num_blocks;
-    int Hkv, bs, bs_log2, MBs, MBd, max_keep, row, slice;  // row, slice: 16-byte pieces
+    int Hkv, bs, bs_log2, MBs, MBd, max_keep;
+    int row, row_log2;  // 16-byte pieces of a row; lanes of a row: the next power of two
     int *err;
 };
 
-// grid: x = (sequence, KV head), y = cache (0: K, 1: V), z = column slice
+__device__ __forceinline__ void sync_readers(bool cluster) {
+    if (cluster) {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+        __syncthreads();
+    }
+}
+
+// grid: x = (sequence, KV head) x CTA of the cluster, y = cache (0: K, 1: V)
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p) {
+    uint32_t C = 1, rank = 0;
+    if (CLUSTER) {
+        asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
+        asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
+    const int list = blockIdx.x / C, b = list / p.Hkv, h = list % p.Hkv;
     uint4 *pool = reinterpret_cast<uint4 *>(blockIdx.y ? p.v_cache : p.k_cache);
     int n = p.keep_lens[b];
-    const int cap = min(p.max_keep, p.MBd << p.bs_log2);
+    const int cap = min(p.max_keep, p.MBd << p.bs_log2), src_cap = p.MBs << p.bs_log2;
     if (n < 0 || n > cap) {
         if (threadIdx.x == 0) pa::record_error(p.err, PA_DEVERR_BAD_BLOCK);
         n = n < 0 ? 0 : cap;
     }
-    const int32_t *keep = p.keep + static_cast<int64_t>(blockIdx.x) * p.max_keep;
+    const int32_t *keep = p.keep + static_cast<int64_t>(list) * p.max_keep;
     const int32_t *src_row = p.src_table + static_cast<int64_t>(b) * p.MBs;
     const int32_t *dst_row = p.dst_table + static_cast<int64_t>(b) * p.MBd;
-    const int col = blockIdx.z * p.slice + threadIdx.x % p.slice;
-    const int rpp = kThreads / p.slice;  // rows of one pass of the CTA
-    // piece of token j of this head under table row `t`; -1: no such page
-    auto piece = [&](const int32_t *t, int j) -> int64_t {
-        const int blk = t[j >> p.bs_log2];
+    const int col = threadIdx.x & ((1 << p.row_log2) - 1);
+    const int rpp = kThreads >> p.row_log2;  // rows of one pass of the CTA
+    const int chunk = C * kRows * rpp;       // rows of a chunk
+    const int first = rank * kRows * rpp + (threadIdx.x >> p.row_log2);  // this thread's first
+    const bool idle = col >= p.row;
+    // pool row of token j of this head under a table row; -1: no such page
+    auto row_of = [&](const int32_t *table, int j) -> int {
+        const int blk = __ldg(table + (j >> p.bs_log2));
         if (blk < 0 || blk >= p.num_blocks) return -1;
-        const int64_t r = ((static_cast<int64_t>(blk) * p.Hkv + h) << p.bs_log2) + (j & (p.bs - 1));
-        return r * p.row + col;
+        return ((blk * p.Hkv + h) << p.bs_log2) + (j & (p.bs - 1));
     };
-    for (int i0 = 0; i0 < n; i0 += kRows * rpp) {
-        uint4 v[kRows];
-        int64_t to[kRows];
+    int kept[kRows], from[kRows], to[kRows];  // of the chunk after the next, of the next
+    auto load_kept = [&](int i0) {
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
-            const int i = i0 + k * rpp + threadIdx.x / p.slice;
-            to[k] = -1;
-            if (i >= n || col >= p.row) continue;
-            const int j = keep[i];
-            if (j < 0 || j >= p.MBs << p.bs_log2) {
+            const int i = i0 + first + k * rpp;
+            kept[k] = i < n && !idle ? __ldg(keep + i) : -1;
+        }
+    };
+    auto load_rows = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const int i = i0 + first + k * rpp, j = kept[k];
+            from[k] = to[k] = -1;
+            if (i >= n || idle) continue;
+            if (j >= 0 && j < src_cap) from[k] = row_of(src_row, j);
+            to[k] = row_of(dst_row, i);
+            if (from[k] < 0 || to[k] < 0) {
                 pa::record_error(p.err, PA_DEVERR_BAD_BLOCK);
-                continue;
-            }
-            const int64_t from = piece(src_row, j);
-            to[k] = piece(dst_row, i);
-            if (from < 0 || to[k] < 0) {
-                pa::record_error(p.err, PA_DEVERR_BAD_BLOCK);
-                to[k] = -1;
-            } else if (from == to[k]) {
-                to[k] = -1;  // stays where it is
-            } else {
-                v[k] = pool[from];
+                from[k] = -1;
+            } else if (from[k] == to[k]) {
+                from[k] = -1;  // stays where it is
             }
         }
-        __syncthreads();
+    };
+    load_kept(0);
+    load_rows(0);
+    load_kept(chunk);
+    for (int i0 = 0; i0 < n; i0 += chunk) {
+        uint4 v[kRows];
+        int dst[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            dst[k] = from[k] >= 0 ? to[k] : -1;
+            if (from[k] >= 0) v[k] = pool[static_cast<int64_t>(from[k]) * p.row + col];
+        }
+        load_rows(i0 + chunk);
+        load_kept(i0 + 2 * chunk);
+        sync_readers(CLUSTER);
 #pragma unroll
         for (int k = 0; k < kRows; ++k)
-            if (to[k] >= 0) pool[to[k]] = v[k];
+            if (dst[k] >= 0) pool[static_cast<int64_t>(dst[k]) * p.row + col] = v[k];
     }
 }
 
@@ -154,6 +189,8 @@ extern "C" int pa_compact_cache(void *k_cache, void *v_cache, const int32_t *src
     if (int64_t(src_blocks_per_seq) * block_size > (int64_t(1) << 30) ||
         int64_t(dst_blocks_per_seq) * block_size > (int64_t(1) << 30) || max_keep > (1 << 30))
         return pa::fail(PA_ERR_INVALID, "compact_cache: table capacity too large");
+    if (num_blocks > INT32_MAX || num_blocks * Hkv * block_size > int64_t(INT32_MAX))
+        return pa::fail(PA_ERR_UNSUPPORTED, "compact_cache: pools of 2^31 rows or more");
     if ((head_dim * es) % 16)
         return pa::fail(PA_ERR_INVALID, "compact_cache: row bytes must be a multiple of 16");
     if (B == 0 || max_keep == 0) return PA_OK;
@@ -182,23 +219,31 @@ extern "C" int pa_compact_cache(void *k_cache, void *v_cache, const int32_t *src
     p.max_keep = max_keep;
     p.row = head_dim * es / 16;
     p.err = pa::device_error_word();
-    // columns: the whole row when there are enough (sequence, head) pairs to
-    // fill the GPU, else slices of at least four pieces (64 bytes)
-    p.slice = 1;
-    while (p.slice < p.row && p.slice < kThreads) p.slice *= 2;
-    auto slices = [&] { return (p.row + p.slice - 1) / p.slice; };
-    while (p.slice > 4 && int64_t(B) * Hkv * 2 * slices() < 2 * 152) p.slice /= 2;
+    while ((1 << p.row_log2) < p.row) ++p.row_log2;
+    // clusters while there are too few lists for two CTAs per SM and a chunk of
+    // the cluster is no longer than the longest list
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return pa::cuda_fail(cudaGetLastError(), "compact_cache: SM count");
+    const int64_t lists = int64_t(B) * Hkv;
+    const int rows = kRows * (kThreads >> p.row_log2);
+    unsigned c = 1;
+    while (c < 8 && lists * 2 * c < 2 * sms && int64_t(rows) * c < max_keep) c *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(B * Hkv), 2, static_cast<unsigned>(slices()));
+    cfg.gridDim = dim3(static_cast<unsigned>(lists) * c, 2);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {c, 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = c > 1 ? 2 : 1;
     (void)cudaGetLastError();  // drop a stale error that is not ours
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, compact_kernel, p);
+    const cudaError_t e = c > 1 ? cudaLaunchKernelEx(&cfg, compact_kernel<true>, p)
+                                : cudaLaunchKernelEx(&cfg, compact_kernel<false>, p);
     if (e != cudaSuccess) return pa::cuda_fail(e, "compact_cache launch");
     return pa::check_launch("compact_cache launch");
 }

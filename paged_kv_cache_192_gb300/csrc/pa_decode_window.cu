@@ -360,8 +360,8 @@ int launch(const WindowParams &p, cudaStream_t stream) {
     if constexpr (TO::MMA) {
         const int64_t rows = (p.num_blocks * p.Hkv) << p.bs_log2;
         const int box = std::min(TT, p.bs);
-        if (int rc = pa::pool_tensor_map(&kmap, p.k_cache, rows, D, box)) return rc;
-        if (int rc = pa::pool_tensor_map(&vmap, p.v_cache, rows, D, box)) return rc;
+        if (int rc = pa::encode_pool_map(&kmap, p.k_cache, rows, D, box)) return rc;
+        if (int rc = pa::encode_pool_map(&vmap, p.v_cache, rows, D, box)) return rc;
     }
     auto kern = decode_window_kernel<T, D, GQ>;
     static std::atomic<uint64_t> smem_done{0};

@@ -40,6 +40,12 @@ int pool_tensor_map(CUtensorMap *map, const void *pool, int64_t rows, int D, int
 int q_tensor_map(CUtensorMap *map, const void *q, int64_t tokens, int Hq, int D, int gq,
                  int box_tokens);
 
+// The same maps encoded anew: 0.03 us each, so a call pays nothing for keeping
+// none (the windowed calls).
+int encode_pool_map(CUtensorMap *map, const void *pool, int64_t rows, int D, int box_rows);
+int encode_q_map(CUtensorMap *map, const void *q, int64_t tokens, int Hq, int D, int gq,
+                 int box_tokens);
+
 inline size_t dtype_size(int dtype) { return dtype == PA_BF16 ? 2 : (dtype == PA_F32 ? 4 : 0); }
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

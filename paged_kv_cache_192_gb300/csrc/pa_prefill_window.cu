@@ -548,9 +548,9 @@ int launch(const WinParams &p0, const void *q, const void *k_cache, const void *
     const int64_t rows = (p0.num_blocks * p0.Hkv) << p0.bs_log2;
     CUtensorMap kmap, vmap, qmap;
     const int box = std::min(p0.bs, kT2KT);
-    if (int rc = pa::pool_tensor_map(&kmap, k_cache, rows, D, box)) return rc;
-    if (int rc = pa::pool_tensor_map(&vmap, v_cache, rows, D, box)) return rc;
-    if (int rc = pa::q_tensor_map(&qmap, q, p0.T, p0.Hq, D, GQ, 128 / GQ)) return rc;
+    if (int rc = pa::encode_pool_map(&kmap, k_cache, rows, D, box)) return rc;
+    if (int rc = pa::encode_pool_map(&vmap, v_cache, rows, D, box)) return rc;
+    if (int rc = pa::encode_q_map(&qmap, q, p0.T, p0.Hq, D, GQ, 128 / GQ)) return rc;
     using Lay = WLayout<D>;
     auto kern = prefill_window_kernel<D, GQ>;
     static std::atomic<uint64_t> attr_done{0};

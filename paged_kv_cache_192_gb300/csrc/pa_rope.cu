@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxHalf = 256;  // frequencies (rot_dim / 2)
+constexpr int kBatch = 4;      // units in flight per thread
 
 struct RopeParams {
     uint8_t *q_out;
@@ -31,6 +32,7 @@ struct RopeParams {
     int64_t T, num_blocks;
     int64_t q_out_stride, q_stride, k_stride, v_stride;  // bytes between tokens
     int Hq, Hkv, bs_log2, row, half;                     // row: bytes of one head
+    int lanes_log2, vlanes_log2;  // lanes per rotated head, per V head (powers of two)
     int sec_end[4];                                      // first frequency past each axis
     int *err;
 };
@@ -60,7 +62,8 @@ __device__ __forceinline__ void st16(uint8_t *p, const uint4 &v) { *reinterpret_
 // A unit of a rotated head is one 16-byte chunk of the first half of its
 // rotated elements with the matching chunk of the second half (INTER = 0), or
 // one chunk, whose pairs are adjacent (INTER = 1); chunks past the rotated
-// elements are copied.
+// elements are copied.  A thread requests four units at a time, the first four
+// before the token's angles are computed.
 template <typename T, int INTER>
 __global__ void __launch_bounds__(kThreads) rope_store_kernel(const RopeParams p) {
     constexpr int EPC = 16 / sizeof(T);
@@ -69,6 +72,57 @@ __global__ void __launch_bounds__(kThreads) rope_store_kernel(const RopeParams p
     const int64_t t = blockIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t slot = p.slots[t];
+    const int64_t blk = slot >> p.bs_log2;
+    const int off = static_cast<int>(slot & ((1ll << p.bs_log2) - 1));
+    const bool stored = slot >= 0 && blk < p.num_blocks;
+    if (slot >= 0 && !stored && threadIdx.x == 0) pa::record_error(p.err, PA_DEVERR_BAD_BLOCK);
+
+    const int chunks = p.row / 16;             // per head
+    const int hc = p.half / EPC;               // chunks of half the rotated elements
+    const int per_head = INTER ? chunks : chunks - hc;
+    const int nq = p.Hq << p.lanes_log2, nqk = nq + (p.Hkv << p.lanes_log2);
+    const int total = stored ? nqk + (p.Hkv << p.vlanes_log2) : nq;
+    // unit u: its source and destination rows and chunk; V chunks and chunks
+    // past the rotated ones (turn = false) are copied
+    struct Unit {
+        const uint8_t *src;
+        uint8_t *dst;
+        int c;
+        bool live, turn;
+    };
+    auto locate = [&](int u) {
+        Unit x;
+        const bool v = u >= nqk;
+        const int lg = v ? p.vlanes_log2 : p.lanes_log2;
+        const int w = v ? u - nqk : u, hh = w >> lg;
+        x.c = w & ((1 << lg) - 1);
+        x.live = u < total && x.c < (v ? chunks : per_head);
+        x.turn = !v && x.c < (INTER ? 2 * hc : hc);
+        if (!INTER && !v && !x.turn) x.c += hc;
+        if (u < nq) {
+            x.src = p.q + t * p.q_stride + hh * p.row;
+            x.dst = p.q_out + t * p.q_out_stride + hh * p.row;
+        } else {
+            const int h = v ? hh : hh - p.Hq;
+            const int64_t r = ((blk * p.Hkv + h) << p.bs_log2) + off;
+            x.src = v ? p.v_new + t * p.v_stride + h * p.row : p.k_new + t * p.k_stride + h * p.row;
+            x.dst = (v ? p.v_cache : p.k_cache) + r * p.row;
+        }
+        return x;
+    };
+    uint4 a[kBatch], b[INTER ? 1 : kBatch];
+    auto request = [&](int u0) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const Unit x = locate(u0 + k * kThreads);
+            if (!x.live) continue;
+            a[k] = ld16(x.src + x.c * 16);
+            if (!INTER && x.turn) b[INTER ? 0 : k] = ld16(x.src + (x.c + hc) * 16);
+        }
+    };
+    request(threadIdx.x);
+
     for (int i = threadIdx.x; i < p.half; i += kThreads) {
         const int axis = (i >= p.sec_end[0]) + (i >= p.sec_end[1]) + (i >= p.sec_end[2]);
         const double pos = static_cast<double>(p.positions[axis * p.T + t]);
@@ -79,67 +133,39 @@ __global__ void __launch_bounds__(kThreads) rope_store_kernel(const RopeParams p
         sincospif(static_cast<float>(2.0 * turns), &s, &c);
         cs[i] = make_float2(c, s);
     }
-    const int64_t slot = p.slots[t];
-    const int64_t blk = slot >> p.bs_log2;
-    const bool stored = slot >= 0 && blk < p.num_blocks;
-    if (slot >= 0 && !stored && threadIdx.x == 0) pa::record_error(p.err, PA_DEVERR_BAD_BLOCK);
     __syncthreads();
 
-    const int chunks = p.row / 16;             // per head
-    const int hc = p.half / EPC;               // chunks of half the rotated elements
-    const int per_head = INTER ? chunks : chunks - hc;
-    const int nq = p.Hq * per_head, nk = p.Hkv * per_head, nv = p.Hkv * chunks;
-    const int total = nq + (stored ? nk + nv : 0);
-    for (int u = threadIdx.x; u < total; u += kThreads) {
-        if (u >= nq + nk) {  // a chunk of V
-            const int h = (u - nq - nk) / chunks, c = (u - nq - nk) % chunks;
-            const int64_t row = ((blk * p.Hkv + h) << p.bs_log2) + (slot & ((1ll << p.bs_log2) - 1));
-            st16(p.v_cache + row * p.row + c * 16, ld16(p.v_new + t * p.v_stride + h * p.row + c * 16));
-            continue;
-        }
-        const uint8_t *src;
-        uint8_t *dst;
-        int c;
-        if (u < nq) {
-            const int h = u / per_head;
-            c = u % per_head;
-            src = p.q + t * p.q_stride + h * p.row;
-            dst = p.q_out + t * p.q_out_stride + h * p.row;
-        } else {
-            const int h = (u - nq) / per_head;
-            c = (u - nq) % per_head;
-            const int64_t row = ((blk * p.Hkv + h) << p.bs_log2) + (slot & ((1ll << p.bs_log2) - 1));
-            src = p.k_new + t * p.k_stride + h * p.row;
-            dst = p.k_cache + row * p.row;
-        }
-        float2 a[NP], b[NP];
-        if (INTER) {
-            uint4 x = ld16(src + c * 16);
-            if (c < 2 * hc) {
-                pa::Elem<T>::unpack(x, a);
+    for (int u0 = threadIdx.x; u0 < total; u0 += kBatch * kThreads) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const Unit x = locate(u0 + k * kThreads);
+            if (!x.live) continue;
+            if (!x.turn) {
+                st16(x.dst + x.c * 16, a[k]);
+                continue;
+            }
+            float2 f[NP], g[NP];
+            pa::Elem<T>::unpack(a[k], f);
+            if (INTER) {
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
-                    const float2 w = cs[c * NP + i];
-                    a[i] = make_float2(a[i].x * w.x - a[i].y * w.y, a[i].x * w.y + a[i].y * w.x);
+                    const float2 w = cs[x.c * NP + i];
+                    f[i] = make_float2(f[i].x * w.x - f[i].y * w.y, f[i].x * w.y + f[i].y * w.x);
                 }
-                x = pack_chunk<T>(a);
-            }
-            st16(dst + c * 16, x);
-        } else if (c < hc) {
-            pa::Elem<T>::unpack(ld16(src + c * 16), a);
-            pa::Elem<T>::unpack(ld16(src + (c + hc) * 16), b);
+            } else {
+                pa::Elem<T>::unpack(b[INTER ? 0 : k], g);
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const float2 w0 = cs[c * EPC + 2 * i], w1 = cs[c * EPC + 2 * i + 1];
-                const float2 x = a[i], y = b[i];
-                a[i] = make_float2(x.x * w0.x - y.x * w0.y, x.y * w1.x - y.y * w1.y);
-                b[i] = make_float2(x.x * w0.y + y.x * w0.x, x.y * w1.y + y.y * w1.x);
+                for (int i = 0; i < NP; ++i) {
+                    const float2 w0 = cs[x.c * EPC + 2 * i], w1 = cs[x.c * EPC + 2 * i + 1];
+                    const float2 m = f[i], n = g[i];
+                    f[i] = make_float2(m.x * w0.x - n.x * w0.y, m.y * w1.x - n.y * w1.y);
+                    g[i] = make_float2(m.x * w0.y + n.x * w0.x, m.y * w1.y + n.y * w1.x);
+                }
+                st16(x.dst + (x.c + hc) * 16, pack_chunk<T>(g));
             }
-            st16(dst + c * 16, pack_chunk<T>(a));
-            st16(dst + (c + hc) * 16, pack_chunk<T>(b));
-        } else {
-            st16(dst + (c + hc) * 16, ld16(src + (c + hc) * 16));
+            st16(x.dst + x.c * 16, pack_chunk<T>(f));
         }
+        if (u0 + kBatch * kThreads < total) request(u0 + kBatch * kThreads);
     }
 }
 
@@ -226,6 +252,9 @@ extern "C" int pa_rope_reshape_and_cache(
     while ((1 << p.bs_log2) < block_size) ++p.bs_log2;
     p.row = row;
     p.half = rot_dim / 2;
+    const int chunks = row / 16, per_head = interleaved ? chunks : chunks - p.half * es / 16;
+    while ((1 << p.lanes_log2) < per_head) ++p.lanes_log2;
+    while ((1 << p.vlanes_log2) < chunks) ++p.vlanes_log2;
     p.err = pa::device_error_word();
     (void)cudaGetLastError();  // drop a stale error that is not ours
     cudaLaunchConfig_t cfg = {};

@@ -27,6 +27,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     return fn;
 }
 
+}  // namespace
+
 int encode_pool_map(CUtensorMap *map, const void *pool, int64_t rows, int D, int box_rows) {
     auto enc = tensor_map_encoder();
     if (!enc) return fail(PA_ERR_UNSUPPORTED, "no cuTensorMapEncodeTiled");
@@ -57,8 +59,6 @@ int encode_q_map(CUtensorMap *map, const void *q, int64_t tokens, int Hq, int D,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? PA_OK : fail(PA_ERR_CUDA, "tensor map encode failed (%d)", (int)r);
 }
-
-}  // namespace
 
 // Query rows [tokens][Hq][D] (bf16) viewed as a 3D tensor, read in boxes of
 // 64 columns x gq heads x box_tokens tokens (rows of 128 bytes, the 128-byte

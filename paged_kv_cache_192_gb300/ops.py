@@ -146,7 +146,8 @@ def reshape_and_cache(k_new, v_new, k_cache, v_cache, slot_mapping, stream=None)
 
 def _token_rows(t, name, T, H, d):
     """Elements between tokens of [T][H][d] whose heads are contiguous."""
-    _require(t.dim() == 3 and t.shape == (T, H, d), f"{name} must be [{T}][{H}][{d}]")
+    if t.shape != (T, H, d):
+        raise ValueError(f"{name} must be [{T}][{H}][{d}]")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != d and H > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
@@ -175,14 +176,16 @@ def rope_reshape_and_cache(q, k_new, v_new, k_cache, v_cache, slot_mapping, posi
     NB, Hkv, bs, d = k_cache.shape
     T, Hq = q.shape[0], q.shape[1]
     _require(v_cache.shape == k_cache.shape, "k_cache and v_cache must have the same shape")
-    _require(slot_mapping.shape == (T,), f"slot_mapping must be [{T}]")
+    if slot_mapping.shape != (T,):
+        raise ValueError(f"slot_mapping must be [{T}]")
     axes = positions.shape[0] if positions.dim() == 2 else 1
-    _require(positions.dim() in (1, 2) and positions.shape[-1] == T,
-             f"positions must be [{T}] or [axes][{T}]")
+    if positions.shape != (T,) and positions.shape != (axes, T):
+        raise ValueError(f"positions must be [{T}] or [axes][{T}]")
     _require(inv_freq.dim() == 1, "inv_freq must be [rot/2]")
     half = inv_freq.shape[0]
-    sections = (half,) if sections is None else tuple(int(x) for x in sections)
-    _require(len(sections) == axes, f"sections must name the frequencies of each of {axes} axes")
+    sections = (half,) if sections is None else tuple(sections)
+    if len(sections) != axes:
+        raise ValueError(f"sections must name the frequencies of each of {axes} axes")
     qs = _token_rows(q, "q", T, Hq, d)
     ks = _token_rows(k_new, "k_new", T, Hkv, d)
     vs = _token_rows(v_new, "v_new", T, Hkv, d)
@@ -254,13 +257,14 @@ def compact_cache(k_cache, v_cache, src_table, dst_table, keep, keep_lens, strea
     _require(k_cache.dim() == 4, "pools must be [NB][Hkv][bs][d]")
     NB, Hkv, bs, d = k_cache.shape
     _require(v_cache.shape == k_cache.shape, "k_cache and v_cache must have the same shape")
-    _require(keep.dim() == 3 and keep.shape[1] == Hkv, f"keep must be [B][{Hkv}][max_keep]")
+    if keep.dim() != 3 or keep.shape[1] != Hkv:
+        raise ValueError(f"keep must be [B][{Hkv}][max_keep]")
     B, max_keep = keep.shape[0], keep.shape[2]
-    _require(src_table.dim() == 2 and src_table.shape[0] == B and src_table.shape[1] > 0,
-             f"src_table must be [{B}][blocks]")
-    _require(dst_table.dim() == 2 and dst_table.shape[0] == B and dst_table.shape[1] > 0,
-             f"dst_table must be [{B}][blocks]")
-    _require(keep_lens.shape == (B,), f"keep_lens must be [{B}]")
+    for name, t in (("src_table", src_table), ("dst_table", dst_table)):
+        if t.dim() != 2 or t.shape[0] != B or t.shape[1] == 0:
+            raise ValueError(f"{name} must be [{B}][blocks]")
+    if keep_lens.shape != (B,):
+        raise ValueError(f"keep_lens must be [{B}]")
     dev, dt = _device_of(k_cache, "k_cache", stream), k_cache.dtype
     args = (_ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
             _ptr(src_table, "src_table", torch.int32, dev), src_table.shape[1],
@@ -309,13 +313,16 @@ def decode_tile_for(Hq, Hkv, head_dim, block_size, num_blocks, dtype=torch.bfloa
 
 
 def _check_decode_shapes(q, k_cache, v_cache, block_table, context_lens, out):
+    # (messages are formatted only when raised: this runs in front of every call)
     _require(q.dim() == 3 and k_cache.dim() == 4, "q must be [B][Hq][d], pools [NB][Hkv][bs][d]")
     B, Hq, d = q.shape
-    _require(k_cache.shape[3] == d, f"pools must have head_dim {d} like q")
+    if k_cache.shape[3] != d:
+        raise ValueError(f"pools must have head_dim {d} like q")
     _require(v_cache.shape == k_cache.shape, "k_cache and v_cache must have the same shape")
-    _require(block_table.dim() == 2 and block_table.shape[0] == B,
-             f"block_table must be [{B}][max_blocks_per_seq]")
-    _require(context_lens.shape == (B,), f"context_lens must be [{B}]")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}][max_blocks_per_seq]")
+    if context_lens.shape != (B,):
+        raise ValueError(f"context_lens must be [{B}]")
     _require(out is None or out.shape == q.shape, "out must have the shape of q")
 
 
@@ -576,11 +583,13 @@ def prefill_window(q, k_cache, v_cache, block_table, query_start, context_lens, 
     Tq, Hq, d = q.shape
     NB, Hkv, bs, _ = k_cache.shape
     R = context_lens.shape[0]
-    _require(k_cache.shape[3] == d, f"pools must have head_dim {d} like q")
+    if k_cache.shape[3] != d:
+        raise ValueError(f"pools must have head_dim {d} like q")
     _require(v_cache.shape == k_cache.shape, "k_cache and v_cache must have the same shape")
-    _require(query_start.shape == (R + 1,), f"query_start must be [{R + 1}]")
-    _require(block_table.dim() == 2 and block_table.shape[0] == R,
-             f"block_table must be [{R}][max_blocks_per_seq]")
+    if query_start.shape != (R + 1,):
+        raise ValueError(f"query_start must be [{R + 1}]")
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError(f"block_table must be [{R}][max_blocks_per_seq]")
     _require(out is None or out.shape == q.shape, "out must have the shape of q")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     dev, dt = _device_of(q, "q", stream), k_cache.dtype

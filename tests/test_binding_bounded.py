@@ -177,7 +177,8 @@ def c_compact(lib, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=5), 1), (dict(B=-1), 1), (dict(B=65536), 1), (dict(NB=0), 1), (dict(Hkv=0), 1),
     (dict(bs=12), 1), (dict(d=60), 1), (dict(MBs=0), 1), (dict(MBd=0), 1), (dict(mk=-1), 1),
-    (dict(MBs=2 ** 27), 1), (dict(), 1), (dict(ptr=P(8)), 1), (dict(B=0), 0), (dict(mk=0), 0),
+    (dict(MBs=2 ** 27), 1), (dict(NB=2 ** 26), 4), (dict(), 1), (dict(ptr=P(8)), 1), (dict(B=0), 0),
+    (dict(mk=0), 0),
 ])
 def test_compact_c_refusals(lib, kw, code):
     assert c_compact(lib, **kw) == code
