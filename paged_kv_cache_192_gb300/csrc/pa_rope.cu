@@ -19,9 +19,9 @@
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxHalf = 256;  // frequencies (rot_dim / 2)
-constexpr int kBatch = 4;      // units in flight per thread
+constexpr int kBatch = 2;      // units in flight per thread
 
 struct RopeParams {
     uint8_t *q_out;
@@ -62,10 +62,10 @@ __device__ __forceinline__ void st16(uint8_t *p, const uint4 &v) { *reinterpret_
 // A unit of a rotated head is one 16-byte chunk of the first half of its
 // rotated elements with the matching chunk of the second half (INTER = 0), or
 // one chunk, whose pairs are adjacent (INTER = 1); chunks past the rotated
-// elements are copied.  A thread requests four units at a time, the first four
+// elements are copied.  A thread requests two units at a time, the first two
 // before the token's angles are computed.
 template <typename T, int INTER>
-__global__ void __launch_bounds__(kThreads) rope_store_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 12) rope_store_kernel(const RopeParams p) {
     constexpr int EPC = 16 / sizeof(T);
     constexpr int NP = EPC / 2;
     __shared__ float2 cs[kMaxHalf];
