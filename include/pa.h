@@ -506,7 +506,7 @@ int pa_prefill_chunk(void *out, const void *q, const void *k_cache, const void *
  * Other arguments and the error bound as for pa_prefill_chunk.  A request whose
  * lengths do not fit (context outside [new tokens, capacity], rows outside
  * [0, total_tokens]) is left out and PA_DEVERR_BAD_BLOCK recorded.  One launch
- * per 1024 requests.
+ * per 256 requests.
  */
 int pa_prefill_window(void *out, const void *q, const void *k_cache, const void *v_cache,
                       const int32_t *block_table, int max_blocks_per_seq,

@@ -18,11 +18,16 @@
 // of 64 tokens arrive by TMA, through table entries that the loader warp
 // fetches 32 at a time, one batch ahead, so a table may have any length.
 //
-// Warps: 0-3 and 4-7 softmax of the item's query tiles A and B (128 rows
-// each); 8 and 11 issue the tcgen05.mma of A and of B; 9 loads K/V; 10 loads
-// the query tiles.  TMEM (512 columns): O_A [0,128), O_B [128,256), then per
-// query tile 64 columns of S and 64 of P (bf16 hi, lo: ~2^-16 of a weight).
-// Every wait is bounded.
+// Warps: 0-3 and 4-7 softmax of groups A and B; 8 and 11 issue the
+// tcgen05.mma of A and of B; 9 loads K/V; 10 loads the query tiles.  TMEM (512
+// columns): O_A [0,128), O_B [128,256), then per group 64 columns of S and 64
+// of P (bf16 hi, lo: ~2^-16 of a weight).  Every wait is bounded.
+//
+// The groups share an item in one of two ways.  With many items, A and B are
+// its two query tiles of 128 rows and both use every K/V tile.  With few
+// (SPLIT), an item is one query tile: A takes the even K/V tiles and B the odd
+// ones, and the two results meet through shared memory by log-sum-exp, so that
+// an item takes half as long and twice as many SMs have one.
 #include <cuda.h>
 
 #include <algorithm>
@@ -35,7 +40,7 @@ namespace {
 
 using namespace pa::pf;
 
-constexpr int kMaxR = 1024;  // requests per launch (the tables in shared memory)
+constexpr int kMaxR = 256;  // requests per launch (the tables in shared memory)
 
 struct WinParams {
     __nv_bfloat16 *out;
@@ -54,17 +59,22 @@ struct WLayout {
     static constexpr int TMEM_COLS = 512;
     static constexpr int QT_BYTES = 128 * D * 2;   // one query tile
     static constexpr int T_BYTES = kT2KT * D * 2;  // one K or V tile
+    static constexpr int OFF_X = QT_BYTES;         // second query tile; SPLIT: exchange of O
     static constexpr int OFF_KV = 2 * QT_BYTES;    // [stage][K|V]
     static constexpr int OFF_BAR = OFF_KV + NST * 2 * T_BYTES;
-    // kv_full, kv_empty [NST]; s_full, s_free, p_full, o_done, o_free [2];
-    // q_full, q_empty, drain
-    static constexpr int N_BAR = 2 * NST + 10 + 3;
+    // kv_full, kv_empty [NST]; s_full, s_free, p_full, o_done, o_free, x_full
+    // [2]; q_full, q_empty, drain
+    static constexpr int N_BAR = 2 * NST + 12 + 3;
     static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;   // TMEM slot, fail flag, scan scratch
-    static constexpr int OFF_PRE = OFF_MISC + 64;          // [kMaxR + 1] query tiles before request r
+    static constexpr int OFF_ML = OFF_MISC + 64;           // SPLIT: (max, sum) [2][128]
+    static constexpr int OFF_PRE = OFF_ML + 2 * 128 * 8;   // [kMaxR + 1] query tiles before request r
     static constexpr int OFF_QS = OFF_PRE + 4 * (kMaxR + 1);
     static constexpr int OFF_N = OFF_QS + 4 * kMaxR;
     static constexpr int OFF_L = OFF_N + 4 * kMaxR;
-    static constexpr int SMEM = OFF_L + 4 * kMaxR + 1024;
+    static constexpr int OFF_OUT = (OFF_L + 4 * kMaxR + 15) / 16 * 16;  // staged output, 2 KB per warp
+    static constexpr int SMEM = OFF_OUT + 8 * 2048 + 1024;
+    static_assert(OFF_BAR % 8 == 0 && OFF_ML % 8 == 0 && OFF_X % 16 == 0, "alignment");
+    static_assert(QT_BYTES >= 128 * (D / 2) * 4, "half of O must fit the exchange");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -87,7 +97,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-template <int D, int GQ>
+template <int D, int GQ, bool SPLIT>
 __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
     prefill_window_kernel(const WinParams p, const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap vmap,
@@ -95,7 +105,9 @@ __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
     using Lay = WLayout<D>;
     constexpr int NST = Lay::NST;
     constexpr int CH = D * 2 / 16;  // 16-byte chunks per row
-    constexpr int QTOK = 256 / GQ;  // query tokens per item
+    constexpr int QTILES = SPLIT ? 1 : 2;     // query tiles per item
+    constexpr int STEP = SPLIT ? 2 : 1;       // K/V tiles from one of a group to its next
+    constexpr int QTOK = QTILES * 128 / GQ;   // query tokens per item
     constexpr int TILE_TX = 2 * kT2KT * D * 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -105,7 +117,8 @@ __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
     uint64_t *kv_full = bars, *kv_empty = bars + NST;
     uint64_t *s_full = bars + 2 * NST, *s_free = s_full + 2;  // [group]
     uint64_t *p_full = s_free + 2, *o_done = p_full + 2, *o_free = o_done + 2;
-    uint64_t *q_full = o_free + 2, *q_empty = q_full + 1, *drain = q_empty + 1;
+    uint64_t *x_full = o_free + 2;  // [group that wrote]
+    uint64_t *q_full = x_full + 2, *q_empty = q_full + 1, *drain = q_empty + 1;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + Lay::OFF_MISC);
     volatile int *fail = reinterpret_cast<volatile int *>(smem + Lay::OFF_MISC + 4);
     int *scan = reinterpret_cast<int *>(smem + Lay::OFF_MISC + 8);  // [12]
@@ -117,9 +130,11 @@ __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // ---- set-up: barriers, TMEM ------------------------------------------------
     if (tid == 0) {
+        for (const CUtensorMap *map : {&kmap, &vmap, &qmap})
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
         for (int i = 0; i < NST; ++i) {
             pa::mbar_init(&kv_full[i], 1);
-            pa::mbar_init(&kv_empty[i], 2);  // both query tiles' PV
+            pa::mbar_init(&kv_empty[i], SPLIT ? 1 : 2);  // the PV of the groups that use it
         }
         for (int i = 0; i < 2; ++i) {
             pa::mbar_init(&s_full[i], 1);
@@ -127,9 +142,10 @@ __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
             pa::mbar_init(&p_full[i], 4);
             pa::mbar_init(&o_done[i], 1);
             pa::mbar_init(&o_free[i], 4);
+            pa::mbar_init(&x_full[i], 4);
         }
         pa::mbar_init(q_full, 1);
-        pa::mbar_init(q_empty, 2);  // both query tiles' last S
+        pa::mbar_init(q_empty, 2);  // both groups' last S
         pa::mbar_init(drain, 2);
         *fail = 0;
         pa::fence_barrier_init();
@@ -224,8 +240,8 @@ __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
                 break;
             }
             if (lane == 0) {
-                pa::mbar_arrive_expect_tx(q_full, 2 * Lay::QT_BYTES);
-                for (int qt = 0; qt < 2; ++qt)
+                pa::mbar_arrive_expect_tx(q_full, QTILES * Lay::QT_BYTES);
+                for (int qt = 0; qt < QTILES; ++qt)
 #pragma unroll
                     for (int h = 0; h < D / 64; ++h)
                         tma_load_3d(sq + qt * Lay::QT_BYTES + h * (128 * 128), &qmap, h * 64,
@@ -290,13 +306,13 @@ __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
             if (!ok) *fail = 1;
         }
     } else if (warp == Lay::MMA_WARP || warp == Lay::MMA_WARP_B) {
-        // ---------------- MMA issuers, one per query tile ----------------
+        // ---------------- MMA issuers, one per group ----------------
         const int wg = warp == Lay::MMA_WARP ? 0 : 1;
         constexpr uint32_t kIdS = pa::tc::idesc_bf16(128, kT2KT, 0, 0);
         constexpr uint32_t kIdO = pa::tc::idesc_bf16(128, D, 0, 1);
         constexpr uint32_t kStage = (2 * Lay::T_BYTES) >> 4;
         const uint64_t dq = pa::tc::sdesc(sq, 16, 1024) +
-                            static_cast<uint32_t>(wg * (Lay::QT_BYTES >> 4));
+                            static_cast<uint32_t>(SPLIT ? 0 : wg * (Lay::QT_BYTES >> 4));
         const uint64_t dk = pa::tc::sdesc(skv, 16, 1024);
         const uint64_t dv = pa::tc::sdesc(skv + Lay::T_BYTES, kT2KT * 128, 1024);
         const uint32_t sc = tmem + 256 + wg * 128, ph = sc + 64, pl = ph + 32;
@@ -304,9 +320,9 @@ __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
         auto wait_all = [&](uint64_t *bar, uint32_t parity) {
             return __all_sync(pa::kFull, pa::mbar_wait(bar, parity));
         };
-        // S of CTA tile g, once the group has loaded S of tile g - 1
-        auto issue_s = [&](int g) {
-            if (g > 0 && !wait_all(&s_free[wg], (g - 1) & 1)) return false;
+        // S of CTA tile g, the group's l-th, once the group has loaded the last
+        auto issue_s = [&](int g, int l) {
+            if (l > 0 && !wait_all(&s_free[wg], (l - 1) & 1)) return false;
             pa::tc::fence_after();
             const uint64_t b0 = dk + static_cast<uint32_t>((g % NST) * kStage);
             if (pa::tc::elect_one()) {
@@ -336,50 +352,58 @@ __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
             __syncwarp();
         };
         bool ok = true;
-        int g = 0, it = 0;
+        int g0 = 0, l = 0, it = 0;  // CTA tiles before the item, tiles of the group so far
         for (int x = blockIdx.x; ok && x < nitems; x += gridDim.x, ++it) {
             const int nt = item_of(x).ntiles;
-            ok = wait_all(q_full, it & 1) && wait_all(&kv_full[g % NST], (g / NST) & 1);
-            if (!ok) break;
-            pa::tc::fence_after();
-            ok = issue_s(g);
-            for (int j = 0; j < nt && ok; ++j, ++g) {
-                if (j + 1 < nt) {
-                    ok = wait_all(&kv_full[(g + 1) % NST], ((g + 1) / NST) & 1);
-                    if (!ok) break;
-                    pa::tc::fence_after();
-                    ok = issue_s(g + 1);
+            ok = wait_all(q_full, it & 1);
+            const int first = SPLIT ? wg : 0;
+            auto start = [&](int j, int lj) {  // S of the item's tile j once its K has landed
+                const int g = g0 + j;
+                if (!wait_all(&kv_full[g % NST], (g / NST) & 1)) return false;
+                pa::tc::fence_after();
+                return issue_s(g, lj);
+            };
+            if (ok && first < nt) ok = start(first, l);
+            for (int j = first; j < nt && ok; j += STEP, ++l) {
+                if (j + STEP < nt) {
+                    ok = start(j + STEP, l + 1);
                     if (!ok) break;
                 } else {
                     if (pa::tc::elect_one()) pa::tc::commit(q_empty);
                     __syncwarp();
                 }
                 // the item's first PV overwrites O once the group has read the last item's
-                if (j == 0 && it > 0) ok = wait_all(&o_free[wg], (it - 1) & 1);
-                if (ok) ok = wait_all(&p_full[wg], g & 1);
+                if (j == first && it > 0) ok = wait_all(&o_free[wg], (it - 1) & 1);
+                if (ok) ok = wait_all(&p_full[wg], l & 1);
                 if (!ok) break;
                 pa::tc::fence_after();
-                issue_pv(g, j > 0);
+                issue_pv(g0 + j, j > first);
             }
+            if (first >= nt) {  // no tile for this group: the query tile is free for its part
+                if (pa::tc::elect_one()) pa::tc::commit(q_empty);
+                __syncwarp();
+            }
+            g0 += nt;
         }
         if (!ok) *fail = 1;
     } else {
         // ---------------- softmax warp groups ----------------
-        const int wg = warp >> 2;   // query tile A or B
+        const int wg = warp >> 2;   // group A or B
         const int row = tid & 127;  // TMEM lane
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t o_col = wg * 128, s_col = 256 + wg * 128, p_col = s_col + 64;
-        const int m = wg * 128 + row;
+        const int m = (SPLIT ? 0 : wg * 128) + row;
         const float qs2 = p.qscale;  // softmax scale in log2 units
-        auto pv_done = [&](int gg) { return pa::mbar_wait(&o_done[wg], gg & 1); };
+        auto pv_done = [&](int l) { return pa::mbar_wait(&o_done[wg], l & 1); };
         bool ok = true;
-        int g = 0;
-        for (int x = blockIdx.x; ok && x < nitems; x += gridDim.x) {
-            const Item I = item_of(x);
+        int g0 = 0, l = 0, it = 0;  // CTA tiles before the item, tiles of the group so far
+        Item I = item_of(min(static_cast<int>(blockIdx.x), nitems - 1)), next_item = I;
+        for (int x = blockIdx.x; ok && x < nitems; x += gridDim.x, ++it, I = next_item) {
             const int pos = I.P + min(I.t0 + m / GQ, I.n - 1);  // this row's own key
             float m_used = -INFINITY, lsum = 0.f;
-            for (int j = 0; j < I.ntiles; ++j, ++g) {
-                ok = pa::mbar_wait(&s_full[wg], g & 1);
+            const int first = SPLIT ? wg : 0;
+            for (int j = first; j < I.ntiles; j += STEP, ++l) {
+                ok = pa::mbar_wait(&s_full[wg], l & 1);
                 if (!ok) break;
                 pa::tc::fence_after();
                 uint32_t sr[2][32];
@@ -397,9 +421,14 @@ __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
                 // hidden: keys past the row's own, and keys [S, pos - W]
                 const int hi = pos - j0, wl = pos - p.window - j0, s0 = p.sinks - j0;
                 if (hi < kT2KT - 1 || (wl >= 0 && s0 < kT2KT)) {
+                    // bit c: key j0 + c is hidden; up(n): the bits from n on
+                    auto up = [](int n) { return n >= 64 ? 0ull : ~0ull << max(n, 0); };
+                    const uint64_t hidden = up(hi + 1) | (up(s0) & ~up(wl + 1));
+                    const uint32_t hl = static_cast<uint32_t>(hidden),
+                                   hh = static_cast<uint32_t>(hidden >> 32);
 #pragma unroll
                     for (int c = 0; c < 64; ++c)
-                        if (c > hi || (c <= wl && c >= s0)) s[c] = -INFINITY;
+                        if ((c < 32 ? hl : hh) & (1u << (c & 31))) s[c] = -INFINITY;
                 }
                 float mx[8];
 #pragma unroll
@@ -436,12 +465,12 @@ __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
                 const float rs = ((rs2[0].x + rs2[0].y) + (rs2[1].x + rs2[1].y)) +
                                  ((rs2[2].x + rs2[2].y) + (rs2[3].x + rs2[3].y));
                 lsum = lsum * alpha + rs;
-                if (j > 0) {  // PV of the previous tile must be done before O is rescaled
-                    ok = pv_done(g - 1);
+                if (j > first) {  // PV of the previous tile must be done before O is rescaled
+                    ok = pv_done(l - 1);
                     if (!ok) break;
                     pa::tc::fence_after();
                     if (__any_sync(pa::kFull, alpha != 1.f)) {
-#pragma unroll
+#pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 32) {
                             uint32_t o[32];
                             pa::tc::ld32(lane_base + o_col + c0, o);
@@ -458,7 +487,7 @@ __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
                 // 0 * NaN is NaN, so they are zeroed.  Each group does so before
                 // its own P arrival; both write zeros.
                 {
-                    const uint32_t vst = skv + (g % NST) * 2 * Lay::T_BYTES + Lay::T_BYTES;
+                    const uint32_t vst = skv + ((g0 + j) % NST) * 2 * Lay::T_BYTES + Lay::T_BYTES;
                     auto zero_rows = [&](int a, int b) {
                         for (int idx = row; idx < (b - a) * CH; idx += 128)
                             asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
@@ -479,32 +508,117 @@ __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[wg]);
             }
+            g0 += I.ntiles;
             if (!ok) break;
-            ok = pv_done(g - 1);  // PV of the item's last tile
+            const bool any = first < I.ntiles;  // SPLIT: an item of one tile leaves B none
+            // (while the last PV runs:) where this lane writes its part of four
+            // rows, NULL for rows past the request, and the group's next item
+            __nv_bfloat16 *dst[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int mr = m - lane + k * 8 + lane / 4, t = I.t0 + mr / GQ;
+                dst[k] = t < I.n ? p.out +
+                                       (static_cast<size_t>(I.qs + t) * p.Hq + I.hk * GQ + mr % GQ) * D +
+                                       (lane & 3) * 8
+                                 : nullptr;
+            }
+            next_item = item_of(min(x + static_cast<int>(gridDim.x), nitems - 1));
+            if (any) ok = pv_done(l - 1);       // PV of the item's last tile
             if (!ok) break;
             pa::tc::fence_after();
-            const int t = I.t0 + m / GQ;
-            const float inv = 1.f / lsum;
-            __nv_bfloat16 *dst =
-                p.out + (static_cast<size_t>(I.qs + min(t, I.n - 1)) * p.Hq + I.hk * GQ + m % GQ) * D;
-#pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 64) {  // two TMEM loads per wait
-                uint32_t o[2][32];
-                pa::tc::ld32(lane_base + o_col + c0, o[0]);
-                pa::tc::ld32(lane_base + o_col + c0 + 32, o[1]);
+            // 32 columns of O from column c0, times f
+            auto load_o = [&](int c0, float f, float (&o)[32]) {
+                uint32_t u[32];
+                pa::tc::ld32(lane_base + o_col + c0, u);
                 pa::tc::wait_ld();
-                if (t < I.n) {
 #pragma unroll
-                    for (int c = 0; c < 64; c += 8) {
-                        const uint32_t *oc = &o[c >> 5][c & 31];
-                        uint4 w4;
-                        w4.x = pack_bf16(__uint_as_float(oc[0]) * inv, __uint_as_float(oc[1]) * inv);
-                        w4.y = pack_bf16(__uint_as_float(oc[2]) * inv, __uint_as_float(oc[3]) * inv);
-                        w4.z = pack_bf16(__uint_as_float(oc[4]) * inv, __uint_as_float(oc[5]) * inv);
-                        w4.w = pack_bf16(__uint_as_float(oc[6]) * inv, __uint_as_float(oc[7]) * inv);
-                        *reinterpret_cast<uint4 *>(dst + c0 + c) = w4;
-                    }
+                for (int c = 0; c < 32; ++c) o[c] = any ? __uint_as_float(u[c]) * f : 0.f;
+            };
+            // Rounded, through this warp's 2 KB of shared memory, so that four
+            // lanes write 64 bytes of a row (a lane writing its own row in
+            // 16-byte pieces took 5,000 cycles per item and held up the next
+            // item's products)
+            uint8_t *stage = smem + Lay::OFF_OUT + warp * 2048;
+            auto swz = [](int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); };
+            auto store_o = [&](int c0, const float (&o)[32]) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint4 w4;
+                    w4.x = pack_bf16(o[8 * c], o[8 * c + 1]);
+                    w4.y = pack_bf16(o[8 * c + 2], o[8 * c + 3]);
+                    w4.z = pack_bf16(o[8 * c + 4], o[8 * c + 5]);
+                    w4.w = pack_bf16(o[8 * c + 6], o[8 * c + 7]);
+                    *reinterpret_cast<uint4 *>(stage + swz(lane, c)) = w4;
                 }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint4 w4 = *reinterpret_cast<const uint4 *>(
+                        stage + swz(k * 8 + lane / 4, lane & 3));
+                    if (dst[k]) *reinterpret_cast<uint4 *>(dst[k] + c0) = w4;
+                }
+                __syncwarp();
+            };
+            if constexpr (!SPLIT) {
+                const float inv = 1.f / lsum;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    float o[32];
+                    load_o(c0, inv, o);
+                    store_o(c0, o);
+                }
+            } else {
+                // Each group finishes half of the columns: it takes the other's
+                // part of them and gives its own part of the other half.  B
+                // gives first; a row's slots are used by one thread of each.
+                float4 *xs = reinterpret_cast<float4 *>(smem + Lay::OFF_X);  // [D / 8][128]
+                float2 *xml = reinterpret_cast<float2 *>(smem + Lay::OFF_ML);  // [group][128]
+                auto give = [&](int half) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D / 2; c0 += 32) {
+                        float o[32];
+                        load_o(half * (D / 2) + c0, 1.f, o);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            xs[((c0 + c) / 4) * 128 + row] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                    }
+                    xml[wg * 128 + row] = make_float2(m_used, lsum);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&x_full[wg]);
+                };
+                auto take = [&](int half) {
+                    if (!__all_sync(pa::kFull, pa::mbar_wait(&x_full[wg ^ 1], it & 1))) return false;
+                    const float2 other = xml[(wg ^ 1) * 128 + row];
+                    const float M = fmaxf(m_used, other.x);
+                    const float fo = other.x == -INFINITY ? 0.f : exp2f(other.x - M);
+                    const float fm = m_used == -INFINITY ? 0.f : exp2f(m_used - M);
+                    const float inv = 1.f / (lsum * fm + other.y * fo);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D / 2; c0 += 32) {
+                        float o[32];
+                        load_o(half * (D / 2) + c0, fm * inv, o);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 v = xs[((c0 + c) / 4) * 128 + row];
+                            o[c] = fmaf(v.x, fo * inv, o[c]);
+                            o[c + 1] = fmaf(v.y, fo * inv, o[c + 1]);
+                            o[c + 2] = fmaf(v.z, fo * inv, o[c + 2]);
+                            o[c + 3] = fmaf(v.w, fo * inv, o[c + 3]);
+                        }
+                        store_o(half * (D / 2) + c0, o);
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                if (wg == 1) {
+                    give(0);
+                    ok = take(1);
+                } else {
+                    ok = take(0);
+                    if (ok) give(1);
+                }
+                ok = __all_sync(pa::kFull, ok);
+                if (!ok) break;
             }
             // O of this group may be overwritten once every warp has read it
             pa::tc::fence_before();
@@ -542,9 +656,16 @@ __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
     }
 }
 
-template <int D, int GQ>
-int launch(const WinParams &p0, const void *q, const void *k_cache, const void *v_cache,
-           int max_query_len, cudaStream_t stream) {
+// Upper bound of the query tiles of qtok tokens: at most one per request is
+// partly filled.
+int64_t query_tiles(const WinParams &p, int max_query_len, int qtok) {
+    return std::min<int64_t>(int64_t(p.R) * ((max_query_len + qtok - 1) / qtok),
+                             int64_t(p.T) / qtok + p.R);
+}
+
+template <int D, int GQ, bool SPLIT>
+int launch_t(const WinParams &p0, const void *q, const void *k_cache, const void *v_cache,
+             int max_query_len, int sms, cudaStream_t stream) {
     const int64_t rows = (p0.num_blocks * p0.Hkv) << p0.bs_log2;
     CUtensorMap kmap, vmap, qmap;
     const int box = std::min(p0.bs, kT2KT);
@@ -552,14 +673,10 @@ int launch(const WinParams &p0, const void *q, const void *k_cache, const void *
     if (int rc = pa::encode_pool_map(&vmap, v_cache, rows, D, box)) return rc;
     if (int rc = pa::encode_q_map(&qmap, q, p0.T, p0.Hq, D, GQ, 128 / GQ)) return rc;
     using Lay = WLayout<D>;
-    auto kern = prefill_window_kernel<D, GQ>;
+    auto kern = prefill_window_kernel<D, GQ, SPLIT>;
     static std::atomic<uint64_t> attr_done{0};
     if (int rc = set_smem_once(kern, Lay::SMEM, &attr_done)) return rc;
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return pa::cuda_fail(cudaGetLastError(), "prefill_window: SM count");
-    constexpr int qtok = 256 / GQ;
+    constexpr int qtok = (SPLIT ? 128 : 256) / GQ;
     // more requests than the kernel's tables hold: several launches
     for (int r0 = 0; r0 < p0.R; r0 += kMaxR) {
         WinParams p = p0;
@@ -567,9 +684,7 @@ int launch(const WinParams &p0, const void *q, const void *k_cache, const void *
         p.block_table += int64_t(r0) * p.MB;
         p.query_start += r0;
         p.context_lens += r0;
-        // at most one query tile per request is partly filled
-        const int64_t tiles = std::min<int64_t>(int64_t(p.R) * ((max_query_len + qtok - 1) / qtok),
-                                                int64_t(p.T) / qtok + p.R);
+        const int64_t tiles = query_tiles(p, max_query_len, qtok);
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(
             std::max<int64_t>(1, std::min<int64_t>(sms, tiles * p.Hkv))));
@@ -587,6 +702,18 @@ int launch(const WinParams &p0, const void *q, const void *k_cache, const void *
         if (int rc = pa::check_launch("prefill_window launch")) return rc;
     }
     return PA_OK;
+}
+
+template <int D, int GQ>
+int launch(const WinParams &p, const void *q, const void *k_cache, const void *v_cache,
+           int max_query_len, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return pa::cuda_fail(cudaGetLastError(), "prefill_window: SM count");
+    if (query_tiles(p, max_query_len, 256 / GQ) * p.Hkv * 2 <= sms)
+        return launch_t<D, GQ, true>(p, q, k_cache, v_cache, max_query_len, sms, stream);
+    return launch_t<D, GQ, false>(p, q, k_cache, v_cache, max_query_len, sms, stream);
 }
 
 }  // namespace
@@ -616,8 +743,8 @@ extern "C" int pa_prefill_window(void *out, const void *q, const void *k_cache,
         return pa::fail(PA_ERR_INVALID, "prefill_window: table capacity too large");
     if (num_blocks > INT32_MAX || num_blocks * Hkv * block_size > int64_t(INT32_MAX) - 256)
         return pa::fail(PA_ERR_UNSUPPORTED, "prefill_window: pools of 2^31 rows or more");
-    // items are counted in 32 bits: (tokens / 32 + requests) * KV heads
-    if ((int64_t(total_tokens) / 32 + std::min(R, kMaxR)) * Hkv > INT32_MAX / 2)
+    // items are counted in 32 bits: (tokens / 16 + requests) * KV heads
+    if ((int64_t(total_tokens) / 16 + std::min(R, kMaxR)) * Hkv > INT32_MAX / 2)
         return pa::fail(PA_ERR_UNSUPPORTED, "prefill_window: too many query tokens");
     if (window < 1 || num_sinks < 0)
         return pa::fail(PA_ERR_INVALID, "prefill_window: window %d must be positive, num_sinks %d "

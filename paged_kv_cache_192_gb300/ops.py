@@ -18,6 +18,8 @@ from . import _lib
 from ._lib import PA_BF16, PA_F32, check, lib
 
 _DTYPES = {torch.bfloat16: PA_BF16, torch.float32: PA_F32}
+_CONTIGUOUS = torch.contiguous_format
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -46,7 +48,7 @@ def _require(cond: bool, msg: str):
 def _int32(x, name) -> int:
     """A host integer of the C ABI (ctypes would wrap a larger one)."""
     x = int(x)
-    if not -2 ** 31 <= x < 2 ** 31:
+    if not -2147483648 <= x <= 2147483647:
         raise ValueError(f"{name}={x} does not fit 32 bits")
     return x
 
@@ -82,25 +84,33 @@ def _device_of(t, name, stream=None) -> int:
     return dev
 
 
-def _ptr(t, name, dtype, dev, contiguous=True) -> int:
-    """Address of a tensor of a call that runs on device `dev`."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+def _refuse(dev, *specs):
+    """Raise for the first tensor at fault of a call that runs on device `dev`:
+    specs are (tensor, name, dtype, whether it must be contiguous).  A call
+    asks all its tensors in one expression first and comes here only when one
+    of them fails (small calls are bound by the host)."""
+    for t, name, dtype, contiguous in specs:
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if contiguous and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _check_out(out, dtype, dev):
+    if out.get_device() != dev or out.dtype is not dtype or not out.is_contiguous():
+        _refuse(dev, (out, "out", dtype, True))
 
 
 def _new_like(t, stream):
-    """An output shaped like the contiguous t, allocated on the stream that
+    """A contiguous output shaped like t, allocated on the stream that
     will write it (memory that earlier work of that stream freed is then
     reused in its order)."""
     if stream is None:
-        return torch.empty_like(t, memory_format=torch.contiguous_format)
+        return torch.empty_like(t, memory_format=_CONTIGUOUS)
     with torch.cuda.stream(stream):
-        return torch.empty_like(t, memory_format=torch.contiguous_format)
+        return torch.empty_like(t, memory_format=_CONTIGUOUS)
 
 
 def set_validate(on: bool):
@@ -191,17 +201,24 @@ def rope_reshape_and_cache(q, k_new, v_new, k_cache, v_cache, slot_mapping, posi
     vs = _token_rows(v_new, "v_new", T, Hkv, d)
     os_ = Hq * d if q_out is None else _token_rows(q_out, "q_out", T, Hq, d)
     dev, dt = _device_of(q, "q", stream), k_cache.dtype
-    args = (_ptr(q, "q", dt, dev, False), qs, _ptr(k_new, "k_new", dt, dev, False), ks,
-            _ptr(v_new, "v_new", dt, dev, False), vs, _ptr(k_cache, "k_cache", dt, dev),
-            _ptr(v_cache, "v_cache", dt, dev),
-            _ptr(slot_mapping, "slot_mapping", torch.int64, dev),
-            _ptr(positions, "positions", torch.int64, dev),
-            _ptr(inv_freq, "inv_freq", torch.float32, dev))
     if q_out is None:
         q_out = _new_like(q, stream)
+    if not (q.dtype is dt and k_new.dtype is dt and v_new.dtype is dt and v_cache.dtype is dt
+            and q_out.dtype is dt and slot_mapping.dtype is _I64 and positions.dtype is _I64
+            and inv_freq.dtype is _F32 and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and slot_mapping.is_contiguous() and positions.is_contiguous()
+            and inv_freq.is_contiguous() and k_new.get_device() == v_new.get_device()
+            == k_cache.get_device() == v_cache.get_device() == slot_mapping.get_device()
+            == positions.get_device() == inv_freq.get_device() == q_out.get_device() == dev):
+        _refuse(dev, (q, "q", dt, False), (k_new, "k_new", dt, False), (v_new, "v_new", dt, False),
+                (k_cache, "k_cache", dt, True), (v_cache, "v_cache", dt, True),
+                (slot_mapping, "slot_mapping", _I64, True), (positions, "positions", _I64, True),
+                (inv_freq, "inv_freq", _F32, True), (q_out, "q_out", dt, False))
     check(lib().pa_rope_reshape_and_cache(
-        _ptr(q_out, "q_out", dt, dev, False), os_, *args, _int_array(sections), axes,
-        bool(interleaved), T, NB, Hq, Hkv, bs, d, 2 * half, _dt(k_cache), _stream(stream)))
+        q_out.data_ptr(), os_, q.data_ptr(), qs, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+        k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
+        inv_freq.data_ptr(), _int_array(sections), axes, 1 if interleaved else 0, T, NB, Hq, Hkv, bs,
+        d, 2 * half, _dt(k_cache), _stream(stream)))
     return q_out
 
 
@@ -266,12 +283,19 @@ def compact_cache(k_cache, v_cache, src_table, dst_table, keep, keep_lens, strea
     if keep_lens.shape != (B,):
         raise ValueError(f"keep_lens must be [{B}]")
     dev, dt = _device_of(k_cache, "k_cache", stream), k_cache.dtype
-    args = (_ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
-            _ptr(src_table, "src_table", torch.int32, dev), src_table.shape[1],
-            _ptr(dst_table, "dst_table", torch.int32, dev), dst_table.shape[1],
-            _ptr(keep, "keep", torch.int32, dev), max_keep,
-            _ptr(keep_lens, "keep_lens", torch.int32, dev))
-    check(lib().pa_compact_cache(*args, B, NB, Hkv, bs, d, _dt(k_cache), _stream(stream)))
+    if not (v_cache.dtype is dt and src_table.dtype is _I32 and dst_table.dtype is _I32
+            and keep.dtype is _I32 and keep_lens.dtype is _I32 and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and src_table.is_contiguous()
+            and dst_table.is_contiguous() and keep.is_contiguous() and keep_lens.is_contiguous()
+            and v_cache.get_device() == src_table.get_device() == dst_table.get_device()
+            == keep.get_device() == keep_lens.get_device() == dev):
+        _refuse(dev, (k_cache, "k_cache", dt, True), (v_cache, "v_cache", dt, True),
+                (src_table, "src_table", _I32, True), (dst_table, "dst_table", _I32, True),
+                (keep, "keep", _I32, True), (keep_lens, "keep_lens", _I32, True))
+    check(lib().pa_compact_cache(
+        k_cache.data_ptr(), v_cache.data_ptr(), src_table.data_ptr(), src_table.shape[1],
+        dst_table.data_ptr(), dst_table.shape[1], keep.data_ptr(), max_keep, keep_lens.data_ptr(), B,
+        NB, Hkv, bs, d, _dt(k_cache), _stream(stream)))
 
 
 def decode_workspace_size(B, Hq, head_dim, max_blocks_per_seq, block_size, partition_tokens=0):
@@ -525,14 +549,22 @@ def decode_window(q, k_cache, v_cache, block_table, context_lens, window, num_si
     NB, Hkv, bs, _ = k_cache.shape
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     dev, dt = _device_of(q, "q", stream), k_cache.dtype
-    args = (_ptr(q, "q", dt, dev), _ptr(k_cache, "k_cache", dt, dev),
-            _ptr(v_cache, "v_cache", dt, dev), _ptr(block_table, "block_table", torch.int32, dev),
-            block_table.shape[1], _ptr(context_lens, "context_lens", torch.int32, dev))
+    if not (q.dtype is dt and v_cache.dtype is dt and block_table.dtype is _I32
+            and context_lens.dtype is _I32 and q.is_contiguous() and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and block_table.is_contiguous()
+            and context_lens.is_contiguous() and k_cache.get_device() == v_cache.get_device()
+            == block_table.get_device() == context_lens.get_device() == dev):
+        _refuse(dev, (q, "q", dt, True), (k_cache, "k_cache", dt, True),
+                (v_cache, "v_cache", dt, True), (block_table, "block_table", _I32, True),
+                (context_lens, "context_lens", _I32, True))
     if out is None:
         out = _new_like(q, stream)
+    else:
+        _check_out(out, dt, dev)
     check(lib().pa_decode_window(
-        _ptr(out, "out", dt, dev), *args, B, Hq, Hkv, d, bs, NB, scale, _int32(window, "window"),
-        _int32(num_sinks, "num_sinks"), _dt(q), _stream(stream)))
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+        block_table.shape[1], context_lens.data_ptr(), B, Hq, Hkv, d, bs, NB, scale,
+        _int32(window, "window"), _int32(num_sinks, "num_sinks"), _dt(q), _stream(stream)))
     return out
 
 
@@ -593,14 +625,23 @@ def prefill_window(q, k_cache, v_cache, block_table, query_start, context_lens, 
     _require(out is None or out.shape == q.shape, "out must have the shape of q")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     dev, dt = _device_of(q, "q", stream), k_cache.dtype
-    args = (_ptr(q, "q", dt, dev), _ptr(k_cache, "k_cache", dt, dev),
-            _ptr(v_cache, "v_cache", dt, dev), _ptr(block_table, "block_table", torch.int32, dev),
-            block_table.shape[1], _ptr(query_start, "query_start", torch.int32, dev),
-            _ptr(context_lens, "context_lens", torch.int32, dev))
+    if not (q.dtype is dt and v_cache.dtype is dt and block_table.dtype is _I32
+            and query_start.dtype is _I32 and context_lens.dtype is _I32 and q.is_contiguous()
+            and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_table.is_contiguous() and query_start.is_contiguous()
+            and context_lens.is_contiguous() and k_cache.get_device() == v_cache.get_device()
+            == block_table.get_device() == query_start.get_device()
+            == context_lens.get_device() == dev):
+        _refuse(dev, (q, "q", dt, True), (k_cache, "k_cache", dt, True),
+                (v_cache, "v_cache", dt, True), (block_table, "block_table", _I32, True),
+                (query_start, "query_start", _I32, True), (context_lens, "context_lens", _I32, True))
     if out is None:
         out = _new_like(q, stream)
+    else:
+        _check_out(out, dt, dev)
     check(lib().pa_prefill_window(
-        _ptr(out, "out", dt, dev), *args, R, Tq, _int32(max_query_len, "max_query_len"), Hq, Hkv, d,
-        bs, NB, scale, _int32(window, "window"), _int32(num_sinks, "num_sinks"), _dt(q),
-        _stream(stream)))
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+        block_table.shape[1], query_start.data_ptr(), context_lens.data_ptr(), R, Tq,
+        _int32(max_query_len, "max_query_len"), Hq, Hkv, d, bs, NB, scale, _int32(window, "window"),
+        _int32(num_sinks, "num_sinks"), _dt(q), _stream(stream)))
     return out
