@@ -582,8 +582,27 @@ int pa_bm_append_n(pa_bm *bm, int64_t seq, int64_t n, int64_t *slots, int64_t *c
 /* Drop seq; blocks whose refcount reaches 0 return to the free list. */
 int pa_bm_free_seq(pa_bm *bm, int64_t seq);
 
+/* Free the blocks of seq that a sliding window has left: those whose tokens
+ * are all in [num_sinks, len - window), which neither the newest token nor any
+ * later one sees (pa_decode_window, pa_prefill_window).  Their places in the
+ * block list and table become -1; *freed (may be NULL) receives how many the
+ * sequence gave up (a shared block returns to the free list with its last
+ * holder).  Calls that read the whole context (pa_decode and the like) no longer
+ * work on the sequence. */
+int pa_bm_trim(pa_bm *bm, int64_t seq, int64_t window, int64_t num_sinks, int64_t *freed);
+
+/* Block lists for a compaction (pa_compact_cache) of n sequences to n_tokens[i]
+ * tokens each (at most their length): a block that the sequence alone holds
+ * stays at its logical place, a shared one, or the place of one that pa_bm_trim
+ * gave up, gets a fresh block, and the blocks past the kept tokens are dropped.  Take the sequences'
+ * block tables before (src_table) and after (dst_table), and launch the
+ * compaction before anything else writes into blocks given out later.  All or
+ * nothing; PA_ERR_OOM when there are too few free blocks. */
+int pa_bm_compact(pa_bm *bm, const int64_t *seqs, int n, const int64_t *n_tokens);
+
 /* Host int32 out[n][max_blocks]: the block table rows of seqs[0..n), padded
- * with 0.  PA_ERR_INVALID if a sequence is unknown or has more blocks. */
+ * with 0 (-1 where pa_bm_trim freed a block).  PA_ERR_INVALID if a sequence is
+ * unknown or has more blocks. */
 int pa_bm_block_table(const pa_bm *bm, const int64_t *seqs, int n, int32_t *out,
                       int max_blocks);
 

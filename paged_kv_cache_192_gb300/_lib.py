@@ -87,6 +87,8 @@ SIGNATURES = {
     "pa_bm_append": (_c_int, [_c_vp, _c_i64, _p_i64, _p_i64, _p_i64]),
     "pa_bm_append_n": (_c_int, [_c_vp, _c_i64, _c_i64, _p_i64, _p_i64, _p_i64]),
     "pa_bm_free_seq": (_c_int, [_c_vp, _c_i64]),
+    "pa_bm_trim": (_c_int, [_c_vp, _c_i64, _c_i64, _c_i64, _p_i64]),
+    "pa_bm_compact": (_c_int, [_c_vp, _p_i64, _c_int, _p_i64]),
     "pa_bm_block_table": (_c_int, [_c_vp, _p_i64, _c_int, _p_i32, _c_int]),
     "pa_bm_seq_len": (_c_int, [_c_vp, _c_i64, _p_i64]),
     "pa_bm_seq_blocks": (_c_int, [_c_vp, _c_i64, _p_i32, _c_i64, _p_i64]),

@@ -68,6 +68,26 @@ class BlockManager:
     def free_seq(self, seq: int):
         check(lib().pa_bm_free_seq(self._h, int(seq)))
 
+    def trim(self, seq: int, window: int, num_sinks: int = 0) -> int:
+        """Free the blocks that a sliding window has left (pa_bm_trim): those
+        whose tokens are all past the sinks and before len - window; their
+        table entries become -1.  -> how many the sequence gave up."""
+        v = ctypes.c_int64()
+        check(lib().pa_bm_trim(self._h, int(seq), int(window), int(num_sinks), ctypes.byref(v)))
+        return v.value
+
+    def compact(self, seqs, n_tokens):
+        """Block lists for ops.compact_cache of seqs to n_tokens tokens each
+        (pa_bm_compact).  Take block_table(seqs) before (src_table) and after
+        (dst_table) the call."""
+        seqs = np.ascontiguousarray(seqs, dtype=np.int64)
+        n_tokens = np.ascontiguousarray(n_tokens, dtype=np.int64)
+        if seqs.ndim != 1 or n_tokens.shape != seqs.shape:
+            raise ValueError("seqs and n_tokens must be one-dimensional and of one length")
+        check(lib().pa_bm_compact(self._h, seqs.ctypes.data_as(ctypes.POINTER(ctypes.c_int64)),
+                                  len(seqs),
+                                  n_tokens.ctypes.data_as(ctypes.POINTER(ctypes.c_int64))))
+
     def block_table(self, seqs, max_blocks: int) -> np.ndarray:
         seqs = np.ascontiguousarray(seqs, dtype=np.int64)
         out = np.zeros((len(seqs), int(max_blocks)), dtype=np.int32)

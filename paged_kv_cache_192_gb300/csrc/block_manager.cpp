@@ -20,6 +20,9 @@
 // reused first) whose initial order is 0..n-1 or a SplitMix64-driven
 // Fisher-Yates shuffle; the first branch that appends into a shared, partly
 // filled last block takes the copy; a full shared block is never copied.
+// A sequence may give up blocks that a sliding window has left (pa_bm_trim;
+// their places stay in its list as -1) and take a shorter list for the tokens
+// it keeps (pa_bm_compact).
 // Every failing call leaves the state unchanged, host allocation failures
 // included: every call allocates what it needs (vector capacity, map nodes)
 // before it changes anything, and no exception leaves the C ABI.
@@ -57,9 +60,10 @@ struct pa_bm {
         return b;
     }
     // never allocates: the stack holds each block at most once and keeps the
-    // capacity of num_blocks it was created with
+    // capacity of num_blocks it was created with.  -1 is the place of a block
+    // that the sequence gave up (pa_bm_trim).
     void release(int32_t b) {
-        if (--ref[b] == 0) free_stack.push_back(b);
+        if (b >= 0 && --ref[b] == 0) free_stack.push_back(b);
     }
     // Blocks an append of n tokens to s would take (new blocks + a CoW copy).
     int64_t needed(const Seq &s, int64_t n) const {
@@ -207,7 +211,8 @@ int pa_bm_fork(pa_bm *bm, int64_t parent, int64_t child) {
         alloc_point();
         // (the insertion may rehash: `it` is not used after it)
         const pa_bm::Seq &cs = bm->seqs.emplace(child, std::move(c)).first->second;
-        for (int32_t b : cs.blocks) ++bm->ref[b];
+        for (int32_t b : cs.blocks)
+            if (b >= 0) ++bm->ref[b];
         return int(PA_OK);
     });
 }
@@ -262,6 +267,75 @@ int pa_bm_free_seq(pa_bm *bm, int64_t seq) {
     for (int32_t b : it->second.blocks) bm->release(b);
     bm->seqs.erase(it);
     return PA_OK;
+}
+
+int pa_bm_trim(pa_bm *bm, int64_t seq, int64_t window, int64_t num_sinks, int64_t *freed) {
+    pa::clear_error();
+    if (!bm || window < 1 || num_sinks < 0)
+        return pa::fail(PA_ERR_INVALID, "bm_trim: bad arguments");
+    auto it = bm->seqs.find(seq);
+    if (it == bm->seqs.end()) return pa::fail(PA_ERR_INVALID, "bm_trim: unknown sequence");
+    pa_bm::Seq &s = it->second;
+    int64_t n = 0;
+    // tokens [num_sinks, lo) are hidden from the newest token and all later ones
+    const int64_t lo = s.len - std::min(window, s.len);
+    const int64_t i0 = std::min(num_sinks, s.len) / bm->bs + (std::min(num_sinks, s.len) % bm->bs != 0);
+    for (int64_t i = i0; (i + 1) * bm->bs <= lo; ++i) {
+        if (s.blocks[i] < 0) continue;
+        bm->release(s.blocks[i]);
+        s.blocks[i] = -1;
+        ++n;
+    }
+    if (freed) *freed = n;
+    return PA_OK;
+}
+
+int pa_bm_compact(pa_bm *bm, const int64_t *seqs, int n, const int64_t *n_tokens) {
+    pa::clear_error();
+    if (!bm || n < 0 || (n > 0 && (!seqs || !n_tokens)))
+        return pa::fail(PA_ERR_INVALID, "bm_compact: bad arguments");
+    return guarded("bm_compact", [&] {
+        // the new block lists first (-1: a fresh block), so that nothing has
+        // changed when a sequence is refused or memory runs out
+        alloc_point();
+        std::vector<std::vector<int32_t>> lists(n);
+        alloc_point();
+        std::unordered_map<int64_t, int> once;
+        int64_t fresh = 0;
+        for (int k = 0; k < n; ++k) {
+            auto it = bm->seqs.find(seqs[k]);
+            if (it == bm->seqs.end() || n_tokens[k] < 0 || n_tokens[k] > it->second.len)
+                return pa::fail(PA_ERR_INVALID, "bm_compact: sequence %lld, %lld tokens",
+                                (long long)seqs[k], (long long)n_tokens[k]);
+            alloc_point();
+            if (!once.emplace(seqs[k], k).second)
+                return pa::fail(PA_ERR_INVALID, "bm_compact: sequence %lld twice",
+                                (long long)seqs[k]);
+            const int64_t nblk = (n_tokens[k] + bm->bs - 1) / bm->bs;
+            ensure_capacity(lists[k], size_t(nblk));
+            for (int64_t i = 0; i < nblk; ++i) {
+                const int32_t b = it->second.blocks[i];
+                lists[k].push_back(b >= 0 && bm->ref[b] == 1 ? b : -1);
+                fresh += lists[k].back() < 0;
+            }
+        }
+        if (fresh > int64_t(bm->free_stack.size()))
+            return pa::fail(PA_ERR_OOM, "bm_compact: %lld blocks needed, %zu free",
+                            (long long)fresh, bm->free_stack.size());
+        // nothing below allocates.  All fresh blocks are taken before any old
+        // one is given back: none of them is read by the same compaction.
+        for (auto &l : lists)
+            for (int32_t &b : l)
+                if (b < 0) b = bm->take();
+        for (int k = 0; k < n; ++k) {
+            pa_bm::Seq &s = bm->seqs.find(seqs[k])->second;
+            for (size_t i = 0; i < s.blocks.size(); ++i)
+                if (i >= lists[k].size() || s.blocks[i] != lists[k][i]) bm->release(s.blocks[i]);
+            s.blocks = std::move(lists[k]);
+            s.len = n_tokens[k];
+        }
+        return int(PA_OK);
+    });
 }
 
 int pa_bm_block_table(const pa_bm *bm, const int64_t *seqs, int n, int32_t *out,

@@ -1,0 +1,204 @@
+"""The bounded-cache operators together, as a serving loop uses them: rotary
+store, windowed prefill of a prompt in chunks, windowed decode steps, pages
+freed behind the window and given to other sequences, a fork with
+copy-on-write, and a compaction after which plain decode reads the cache."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV, bf16 = "cuda", torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from paged_kv_cache_192_gb300 import build
+    build.build()
+
+
+class Loop:
+    W, S, Hq, Hkv, d, bs = 48, 5, 8, 2, 64, 8
+
+    def __init__(self, num_blocks, dtype=bf16):
+        from paged_kv_cache_192_gb300 import layout
+        from paged_kv_cache_192_gb300.block_manager import BlockManager
+        self.bm = BlockManager(num_blocks, self.bs, seed=5)
+        self.k, self.v = layout.alloc_pools(num_blocks, self.Hkv, self.bs, self.d, dtype, DEV)
+        self.hist = {}  # sequence -> rows stored so far (K as stored, V)
+        self.g = torch.Generator().manual_seed(11)
+        self.inv = (10000.0 ** (-torch.arange(self.d // 2).double() / (self.d // 2))).float().to(DEV)
+        self.dtype = dtype
+
+    def rand(self, *shape):
+        return torch.randn(*shape, generator=self.g).to(self.dtype).to(DEV)
+
+    def store(self, tokens):
+        """tokens: {seq: n} appended and stored; returns the rotated queries."""
+        from paged_kv_cache_192_gb300 import ops
+        slots, pos, pairs = [], [], []
+        for s, n in tokens.items():
+            L = self.bm.seq_len(s)
+            sl, cow = self.bm.append_n(s, n)
+            slots += list(sl)
+            pos += list(range(L, L + n))
+            pairs += cow
+        if pairs:
+            ops.copy_blocks(self.k, self.v, torch.tensor(pairs, dtype=torch.int64, device=DEV))
+        T = len(slots)
+        q, k, v = self.rand(T, self.Hq, self.d), self.rand(T, self.Hkv, self.d), self.rand(T, self.Hkv, self.d)
+        slots = torch.tensor(slots, dtype=torch.int64, device=DEV)
+        q = ops.rope_reshape_and_cache(q, k, v, self.k, self.v, slots,
+                                       torch.tensor(pos, dtype=torch.int64, device=DEV), self.inv)
+        kr = self.k[slots // self.bs, :, slots % self.bs].double().cpu()
+        at = 0
+        for s, n in tokens.items():
+            old = self.hist.get(s, (kr[:0], kr[:0]))
+            self.hist[s] = (torch.cat([old[0], kr[at:at + n]]),
+                            torch.cat([old[1], v[at:at + n].double().cpu()]))
+            at += n
+        return q
+
+    def tables(self, seqs):
+        mb = max(len(self.bm.seq_blocks(s)) for s in seqs)
+        return (torch.from_numpy(self.bm.block_table(seqs, mb)).to(DEV),
+                torch.tensor([self.bm.seq_len(s) for s in seqs], dtype=torch.int32, device=DEV))
+
+    def check(self, out, q, tokens):
+        """Half a step of the output plus 2^-13 of the largest value (the bound
+        of the windowed tests)."""
+        gq, at = self.Hq // self.Hkv, 0
+        for s, n in tokens.items():
+            k, v = (x.repeat_interleave(gq, 1) for x in self.hist[s])
+            L = k.shape[0]
+            j, p = torch.arange(L), torch.arange(L - n, L)[:, None]
+            sees = (j <= p) & ((j < self.S) | (j > p - self.W))
+            w = torch.einsum("nhd,jhd->hnj", q[at:at + n].double().cpu(), k) * self.d ** -0.5
+            ref = torch.einsum("hnj,jhd->nhd", w.masked_fill(~sees, -float("inf")).softmax(-1), v)
+            err = (out[at:at + n].double().cpu() - ref).abs()
+            assert bool((err <= 2.0 ** -8 * ref.abs() + 2.0 ** -13 * v.abs().max()).all()), float(err.max())
+            at += n
+
+    def prefill(self, tokens):
+        from paged_kv_cache_192_gb300 import ops
+        q = self.store(tokens)
+        table, lens = self.tables(list(tokens))
+        start = torch.tensor([0] + list(np.cumsum(list(tokens.values()))), dtype=torch.int32, device=DEV)
+        out = ops.prefill_window(q, self.k, self.v, table, start, lens, max(tokens.values()), self.W, self.S)
+        self.check(out, q, tokens)
+        self.trim(tokens)
+
+    def decode(self, seqs):
+        from paged_kv_cache_192_gb300 import ops
+        q = self.store({s: 1 for s in seqs})
+        table, lens = self.tables(seqs)
+        out = ops.decode_window(q, self.k, self.v, table, lens, self.W, self.S)
+        self.check(out, q, {s: 1 for s in seqs})
+        self.trim(seqs)
+        return q, out
+
+    def trim(self, seqs):
+        for s in seqs:
+            self.bm.trim(s, self.W, self.S)
+
+
+def test_serving_loop_in_a_pool_that_only_holds_the_windows():
+    from paged_kv_cache_192_gb300 import ops
+    # three sequences of about 200 tokens need 75 pages whole; sinks, window and
+    # a chunk of up to 41 tokens fit in 14 each
+    lp = Loop(num_blocks=42)
+    lens = {0: 200, 1: 173, 2: 90}
+    for s in lens:
+        lp.bm.add_seq(s, 0)
+    done = {s: 0 for s in lens}
+    while any(done[s] < n for s, n in lens.items()):
+        chunk = {s: min(n - done[s], 41 - 7 * s) for s, n in lens.items() if done[s] < n}
+        lp.prefill(chunk)
+        for s, n in chunk.items():
+            done[s] += n
+    for _ in range(20):
+        lp.decode([0, 1, 2])
+    # a branch of sequence 1 shares its pages and writes its own copy of the last
+    lp.bm.fork(1, 7)
+    lp.hist[7] = lp.hist[1]
+    for _ in range(11):
+        lp.decode([0, 7, 1, 2])
+    assert ops.device_error() == 0
+    # every sequence keeps its sinks and window: plain decode then sees the same
+    seqs = [0, 1, 2, 7]
+    table, L = lp.tables(seqs)
+    q = lp.rand(4, lp.Hq, lp.d)
+    want = ops.decode_window(q, lp.k, lp.v, table, L, lp.W, lp.S)
+    n = lp.S + lp.W
+    keep = np.stack([np.concatenate([np.arange(lp.S), np.arange(int(x) - lp.W, int(x))]) for x in L.cpu()])
+    keep = torch.from_numpy(np.repeat(keep[:, None], lp.Hkv, 1).astype(np.int32)).to(DEV)
+    ops.set_validate(True)
+    try:
+        for i, s in enumerate(seqs):  # one at a time: the pool has no room for all the fresh pages
+            src = table[i:i + 1].contiguous()
+            lp.bm.compact([s], [n])
+            ops.compact_cache(lp.k, lp.v, src, lp.tables([s])[0], keep[i:i + 1].contiguous(),
+                              torch.tensor([n], dtype=torch.int32, device=DEV))
+    finally:
+        ops.set_validate(False)
+    dst, new_lens = lp.tables(seqs)
+    assert new_lens.tolist() == [n] * 4 and (dst >= 0).all()
+    got = ops.decode(q, lp.k, lp.v, dst, new_lens)
+    # both are within the bound of the exact result: twice it from each other
+    vmax = max(float(v.abs().max()) for _, v in lp.hist.values())
+    assert bool(((got.double() - want.double()).abs() <= 2.0 ** -7 * want.double().abs() + 2.0 ** -12 * vmax).all())
+    assert lp.bm.num_free() == 42 - 4 * 7 and ops.device_error() == 0
+    # and the sequences go on from there, through the plain calls
+    slots = torch.tensor([lp.bm.append(s)[0] for s in seqs], dtype=torch.int64, device=DEV)
+    kn, vn = lp.rand(4, lp.Hkv, lp.d), lp.rand(4, lp.Hkv, lp.d)
+    ops.reshape_and_cache(kn, vn, lp.k, lp.v, slots)
+    table, L = lp.tables(seqs)
+    a = ops.decode(q, lp.k, lp.v, table, L)
+    b = ops.decode_window(q, lp.k, lp.v, table, L, n + 1)
+    assert bool(((a.double() - b.double()).abs() <= 2.0 ** -7 * b.double().abs() + 2.0 ** -12 * max(vmax, float(vn.abs().max()))).all())
+    assert ops.device_error() == 0
+
+
+def test_decode_step_captured_as_one_graph():
+    """Store and windowed decode of a batch with two padding rows, captured
+    once and replayed with new tokens in the same buffers."""
+    from paged_kv_cache_192_gb300 import ops
+    lp = Loop(num_blocks=64)
+    for s in (0, 1, 2):
+        lp.bm.add_seq(s, 0)
+    lp.prefill({0: 90, 1: 33, 2: 61})
+    B = 5
+    MB = 24
+    q, k, v = (torch.zeros(B, h, lp.d, dtype=bf16, device=DEV) for h in (lp.Hq, lp.Hkv, lp.Hkv))
+    slots = torch.full((B,), -1, dtype=torch.int64, device=DEV)
+    pos = torch.zeros(B, dtype=torch.int64, device=DEV)
+    table = torch.zeros(B, MB, dtype=torch.int32, device=DEV)
+    lens = torch.zeros(B, dtype=torch.int32, device=DEV)
+
+    def step():
+        r = ops.rope_reshape_and_cache(q, k, v, lp.k, lp.v, slots, pos, lp.inv)
+        return r, ops.decode_window(r, lp.k, lp.v, table, lens, lp.W, lp.S)
+
+    step()  # with padding only
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        rot, out = step()
+    for _ in range(12):
+        rows = [0, 2, 4]  # rows 1 and 3 are padding
+        for r, s in zip(rows, (0, 1, 2)):
+            slot, _, _ = lp.bm.append(s)
+            slots[r], pos[r] = slot, lp.bm.seq_len(s) - 1
+            lens[r] = lp.bm.seq_len(s)
+            row = lp.bm.block_table([s], MB)
+            table[r] = torch.from_numpy(row[0]).to(DEV)
+        for t in (q, k, v):
+            t.copy_(lp.rand(*t.shape))
+        g.replay()
+        torch.cuda.synchronize()
+        for r, s in zip(rows, (0, 1, 2)):
+            kr = lp.k[slots[r] // lp.bs, :, slots[r] % lp.bs].double().cpu()[None]
+            lp.hist[s] = (torch.cat([lp.hist[s][0], kr]), torch.cat([lp.hist[s][1], v[r:r + 1].double().cpu()]))
+            lp.check(out[r:r + 1], rot[r:r + 1], {s: 1})
+        assert not out[[1, 3]].any()
+        lp.trim([0, 1, 2])
+    assert ops.device_error() == 0
