@@ -23,9 +23,10 @@ _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 
 def _dt(t: torch.Tensor) -> int:
-    if t.dtype not in _DTYPES:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return _DTYPES[t.dtype]
+    return code
 
 
 def _cuda(t: torch.Tensor, name: str, dtype=None):
@@ -62,12 +63,14 @@ def _pairs_ok(pairs) -> bool:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream=None) -> int:
+def _stream(stream=None, dev=None) -> int:
+    """Handle of `stream`, or of the current stream of device `dev` (default:
+    the current device)."""
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return _raw_stream(torch.cuda.current_device())
+        return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(torch.cuda.current_device() if dev is None else dev)
 
 
 def _device_of(t, name, stream=None) -> int:
@@ -76,9 +79,9 @@ def _device_of(t, name, stream=None) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{dev}, not on the current device "
-                         f"cuda:{torch.cuda.current_device()}")
+    cur = torch.cuda.current_device()
+    if dev != cur:
+        raise ValueError(f"{name} is on cuda:{dev}, not on the current device cuda:{cur}")
     if stream is not None and stream.device.index != dev:
         raise ValueError(f"stream must belong to the current device cuda:{dev}")
     return dev
@@ -184,7 +187,7 @@ def rope_reshape_and_cache(q, k_new, v_new, k_cache, v_cache, slot_mapping, posi
     _require(q.dim() == 3 and k_new.dim() == 3 and k_cache.dim() == 4,
              "q must be [T][Hq][d], k_new and v_new [T][Hkv][d], pools [NB][Hkv][bs][d]")
     NB, Hkv, bs, d = k_cache.shape
-    T, Hq = q.shape[0], q.shape[1]
+    T, Hq, _ = q.shape
     _require(v_cache.shape == k_cache.shape, "k_cache and v_cache must have the same shape")
     if slot_mapping.shape != (T,):
         raise ValueError(f"slot_mapping must be [{T}]")
@@ -218,7 +221,7 @@ def rope_reshape_and_cache(q, k_new, v_new, k_cache, v_cache, slot_mapping, posi
         q_out.data_ptr(), os_, q.data_ptr(), qs, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
         k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
         inv_freq.data_ptr(), _int_array(sections), axes, 1 if interleaved else 0, T, NB, Hq, Hkv, bs,
-        d, 2 * half, _dt(k_cache), _stream(stream)))
+        d, 2 * half, _dt(k_cache), _stream(stream, dev)))
     return q_out
 
 
@@ -295,7 +298,7 @@ def compact_cache(k_cache, v_cache, src_table, dst_table, keep, keep_lens, strea
     check(lib().pa_compact_cache(
         k_cache.data_ptr(), v_cache.data_ptr(), src_table.data_ptr(), src_table.shape[1],
         dst_table.data_ptr(), dst_table.shape[1], keep.data_ptr(), max_keep, keep_lens.data_ptr(), B,
-        NB, Hkv, bs, d, _dt(k_cache), _stream(stream)))
+        NB, Hkv, bs, d, _dt(k_cache), _stream(stream, dev)))
 
 
 def decode_workspace_size(B, Hq, head_dim, max_blocks_per_seq, block_size, partition_tokens=0):
@@ -564,7 +567,7 @@ def decode_window(q, k_cache, v_cache, block_table, context_lens, window, num_si
     check(lib().pa_decode_window(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
         block_table.shape[1], context_lens.data_ptr(), B, Hq, Hkv, d, bs, NB, scale,
-        _int32(window, "window"), _int32(num_sinks, "num_sinks"), _dt(q), _stream(stream)))
+        _int32(window, "window"), _int32(num_sinks, "num_sinks"), _dt(q), _stream(stream, dev)))
     return out
 
 
@@ -643,5 +646,5 @@ def prefill_window(q, k_cache, v_cache, block_table, query_start, context_lens, 
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
         block_table.shape[1], query_start.data_ptr(), context_lens.data_ptr(), R, Tq,
         _int32(max_query_len, "max_query_len"), Hq, Hkv, d, bs, NB, scale, _int32(window, "window"),
-        _int32(num_sinks, "num_sinks"), _dt(q), _stream(stream)))
+        _int32(num_sinks, "num_sinks"), _dt(q), _stream(stream, dev)))
     return out
