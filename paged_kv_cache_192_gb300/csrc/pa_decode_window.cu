@@ -41,7 +41,8 @@ struct WindowParams {
     float qscale;  // scale * log2(e)
 };
 
-template <typename T, int D, int GQ>
+// DEEP: the deeper ring with fewer CTAs per SM (tensor-core tile only)
+template <typename T, int D, int GQ, bool DEEP = false>
 struct TileOf {  // CUDA-core tile
     using type = WarpAttn<T, D, GQ>;
     static constexpr bool MMA = false;
@@ -50,19 +51,24 @@ struct TileOf {  // CUDA-core tile
     static constexpr int PBUF = 2 * Cfg<T, D, GQ>::TT * GQ * 4;  // p and score buffers, per warp
     static constexpr int MINB = 1;
 };
-template <int D, int GQ>
-struct TileOf<__nv_bfloat16, D, GQ> {  // tensor-core tile
+template <int D, int GQ, bool DEEP>
+struct TileOf<__nv_bfloat16, D, GQ, DEEP> {  // tensor-core tile
     using type = MmaAttn<D, GQ>;
     static constexpr bool MMA = true;
     static constexpr int STAGE = 2 * MmaCfg<D, GQ>::TILE;
-    static constexpr int NST = 24 * 1024 / STAGE;  // 24 KB per warp: two CTAs per SM
+    // Two stages per warp, and as many CTAs per SM as then fit: other CTAs fill
+    // the time in which one starts or merges.  32 sequences, window 4096, d 128:
+    // 80.5 us with 2 stages and 3 CTAs per SM, 83.4 with 3 and 2, 104.5 with 6
+    // and 1; 64 sequences, window 2048, d 64: 43.2 us with 2 stages, 45.6 with
+    // 3, 60.2 with 4 (4 KB stages).  DEEP: for the batches of launch().
+    static constexpr int NST = DEEP ? (D == 128 ? 3 : 4) : 2;
     static constexpr int PBUF = 0;
-    static constexpr int MINB = 2;
+    static constexpr int MINB = (D == 128 ? 3 : 4) - (DEEP ? 1 : 0);
 };
 
-template <typename T, int D, int GQ>
+template <typename T, int D, int GQ, bool DEEP>
 struct Layout {
-    using TO = TileOf<T, D, GQ>;
+    using TO = TileOf<T, D, GQ, DEEP>;
     static constexpr int WARP = TO::NST * TO::STAGE;  // ring of a warp, then its result
     static constexpr int OFF_P = kNW * WARP;
     static constexpr int OFF_CTA = OFF_P + kNW * TO::PBUF;   // the CTA's result: acc [GQ][D]
@@ -155,12 +161,12 @@ __device__ __forceinline__ float weight(float m, float M) {
     return m == -INFINITY ? 0.f : exp2f(m - M);
 }
 
-template <typename T, int D, int GQ>
-__global__ void __launch_bounds__(kNW * 32, (TileOf<T, D, GQ>::MINB))
+template <typename T, int D, int GQ, bool DEEP>
+__global__ void __launch_bounds__(kNW * 32, (TileOf<T, D, GQ, DEEP>::MINB))
     decode_window_kernel(const WindowParams p, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap) {
-    using TO = TileOf<T, D, GQ>;
-    using Lay = Layout<T, D, GQ>;
+    using TO = TileOf<T, D, GQ, DEEP>;
+    using Lay = Layout<T, D, GQ, DEEP>;
     using St = typename TO::type;
     constexpr int TT = St::C::TT;
     constexpr int NST = TO::NST;
@@ -351,29 +357,48 @@ int sm_count() {
     return sms;
 }
 
-template <typename T, int D, int GQ>
-int launch(const WindowParams &p, cudaStream_t stream) {
-    using TO = TileOf<T, D, GQ>;
-    using Lay = Layout<T, D, GQ>;
-    constexpr int TT = TO::type::C::TT;
+// CTAs of a kernel that run at once on the current device (0: unknown); looked
+// up once per kernel and device, where clusters of 16 CTAs, past the portable
+// size of 8, are also allowed.
+template <typename K>
+int concurrent_ctas(K kern, size_t smem, std::atomic<int> (&cache)[64]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < 64)
+        if (const int n = cache[dev].load(std::memory_order_relaxed)) return n;
+    int per_sm = 0;
+    const int sms = sm_count();
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kNW * 32, smem) != cudaSuccess)
+        return 0;
+    if (dev < 64) cache[dev].store(per_sm * sms, std::memory_order_relaxed);
+    return per_sm * sms;
+}
+
+// CTAs of decode_window_kernel that run at once, with its attributes set;
+// 0: a CUDA call failed.
+template <typename T, int D, int GQ, bool DEEP>
+int prepare_kernel() {
+    using Lay = Layout<T, D, GQ, DEEP>;
+    static std::atomic<uint64_t> smem_done{0};
+    static std::atomic<int> slots[64];
+    auto kern = decode_window_kernel<T, D, GQ, DEEP>;
+    if (pa::pf::set_smem_once(kern, Lay::SMEM, &smem_done)) return 0;
+    return concurrent_ctas(kern, Lay::SMEM, slots);
+}
+
+template <typename T, int D, int GQ, bool DEEP>
+int launch_t(const WindowParams &p, int c, cudaStream_t stream) {
+    using TO = TileOf<T, D, GQ, DEEP>;
+    using Lay = Layout<T, D, GQ, DEEP>;
     CUtensorMap kmap{}, vmap{};
     if constexpr (TO::MMA) {
         const int64_t rows = (p.num_blocks * p.Hkv) << p.bs_log2;
-        const int box = std::min(TT, p.bs);
+        const int box = std::min(TO::type::C::TT, p.bs);
         if (int rc = pa::encode_pool_map(&kmap, p.k_cache, rows, D, box)) return rc;
         if (int rc = pa::encode_pool_map(&vmap, p.v_cache, rows, D, box)) return rc;
     }
-    auto kern = decode_window_kernel<T, D, GQ>;
-    static std::atomic<uint64_t> smem_done{0};
-    if (int rc = pa::pf::set_smem_once(kern, Lay::SMEM, &smem_done)) return rc;
-    const int sms = sm_count();
-    if (sms <= 0) return pa::fail(PA_ERR_CUDA, "decode_window: no SM count");
-    // cluster size: enough CTAs for two per SM, at least two tiles per warp
     const int64_t items = int64_t(p.B) * p.Hkv;
-    const int64_t tokens = std::min<int64_t>(int64_t(p.MB) << p.bs_log2, int64_t(p.sinks) + p.window);
-    const int64_t tiles = (tokens + TT - 1) / TT;
-    int c = 1;
-    while (c < 8 && items * c < 2 * sms && tiles >= 2 * kNW * 2 * c) c *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(items * c));
     cfg.blockDim = dim3(kNW * 32);
@@ -387,9 +412,49 @@ int launch(const WindowParams &p, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     (void)cudaGetLastError();  // drop a stale error that is not ours
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, kmap, vmap);
+    const cudaError_t e =
+        cudaLaunchKernelEx(&cfg, decode_window_kernel<T, D, GQ, DEEP>, p, kmap, vmap);
     if (e != cudaSuccess) return pa::cuda_fail(e, "decode_window launch");
     return pa::check_launch("decode_window launch");
+}
+
+template <typename T, int D, int GQ>
+int launch(const WindowParams &p, cudaStream_t stream) {
+    using TO = TileOf<T, D, GQ>;
+    constexpr int TT = TO::type::C::TT;
+    const int slots = prepare_kernel<T, D, GQ, false>(), sms = sm_count();
+    if (slots <= 0 || sms <= 0)
+        return pa::cuda_fail(cudaGetLastError(), "decode_window: kernel attributes");
+    // Cluster size: the largest that leaves every warp two tiles and all
+    // clusters running at once (clusters of 16 sit two to a GPC).  A second
+    // wave of clusters costs more than the split gains: window 4096, 8 KV heads,
+    // 4 sequences: 16.0 us with clusters of 8, 30.4 with 16; 16 sequences of
+    // window 1024: 15.9 us with clusters of 2, 21.4 with 4.  One sequence: window
+    // 8192 13.4 us with clusters of 16, 18.5 with 8.
+    const int64_t items = int64_t(p.B) * p.Hkv;
+    const int64_t tokens = std::min<int64_t>(int64_t(p.MB) << p.bs_log2, int64_t(p.sinks) + p.window);
+    const int64_t tiles = (tokens + TT - 1) / TT;
+    auto fits = [&](int c) {
+        return tiles >= 2 * kNW * c && items * c <= slots && (c < 16 || items <= 16);
+    };
+    int c = 1;
+    while (c < 16 && fits(2 * c)) c *= 2;
+    if constexpr (TO::MMA) {
+        // A last wave of fewer CTAs than SMs leaves memory idle, each CTA alone
+        // on its SM: the time lost, as a part of the whole.  The deeper ring has
+        // fewer CTAs at once, so that another number of items ends badly: 512
+        // items of window 4096 175 us with two stages (a last wave of 56 CTAs),
+        // 150 with the deeper ring (208); 384 items of window 2048 64.6 and 75.2.
+        auto lost = [&](int64_t at_once) {
+            const int64_t last = items % at_once;
+            return items <= at_once || last == 0 || last >= sms ? 0.0 : double(sms - last) / items;
+        };
+        const int deep = prepare_kernel<T, D, GQ, true>();
+        if (deep <= 0) return pa::cuda_fail(cudaGetLastError(), "decode_window: kernel attributes");
+        if (c == 1 && lost(slots) > lost(deep) + 0.05)
+            return launch_t<T, D, GQ, true>(p, c, stream);
+    }
+    return launch_t<T, D, GQ, false>(p, c, stream);
 }
 
 template <typename T, int D>

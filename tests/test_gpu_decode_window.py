@@ -62,6 +62,16 @@ def test_cluster_sizes(B, L, W, dtype, gq):
     bt.check(run(bt))
 
 
+@pytest.mark.parametrize("d,B", [(128, 230), (64, 310)])
+@pytest.mark.parametrize("gq", [1, 8])
+def test_batches_that_end_in_a_short_wave(d, B, gq):
+    """A few more items than run at once: the kernel with the deeper ring."""
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(1, 150, size=B)]
+    bt = batch(lens, 70, 3, Hq=2 * gq, Hkv=2, d=d, bs=8, seed=B)
+    bt.check(run(bt))
+
+
 def test_window_beyond_the_context_matches_decode():
     from paged_kv_cache_192_gb300 import ops
     bt = batch([5, 100, 333, 1000], 1000, 0)
