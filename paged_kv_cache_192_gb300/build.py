@@ -2,8 +2,11 @@
 
 Each translation unit under csrc/ is compiled by nvcc in parallel, then the
 objects are linked into ``paged_kv_cache_192_gb300/libpa_gb300.so`` (static
-CUDA runtime, no torch dependency).  Objects are cached in ``_build/`` keyed
-by a hash of the sources and flags, so an unchanged tree rebuilds in no time.
+CUDA runtime, no torch dependency).  Beside it, ``binding/bounded_calls.cpp``
+(the torch-facing binding of the calls whose time on the host counts) becomes
+the extension module ``_bounded_calls.so``, linked to the library and to the
+installed torch.  Objects are cached in ``_build/`` keyed by a hash of the
+sources and flags, so an unchanged tree rebuilds in no time.
 """
 from __future__ import annotations
 
@@ -14,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpa_gb300.so")
+BINDING_SRC = os.path.join(PKG, "binding", "bounded_calls.cpp")
+BINDING = os.path.join(PKG, "_bounded_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -43,6 +49,40 @@ def _digest(paths, extra) -> str:
     return h.hexdigest()[:16]
 
 
+def _torch_flags():
+    """(compile flags, link flags) of an extension module of the running
+    Python against the installed torch (found without importing it)."""
+    import importlib.util
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch not found")
+    root = os.path.dirname(spec.origin)
+    with open(os.path.join(root, "version.py")) as f:
+        version = f.read()
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include/torch/csrc/api/include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    comp = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden"] + [x for i in inc for x in ("-I", i)]
+    lib = os.path.join(root, "lib")
+    link = ["-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10",
+            f"-Wl,-rpath,{lib}", "-Wl,-rpath,$ORIGIN"]
+    return comp, link, version
+
+
+def _compile_binding(src: str, obj: str, flags) -> str:
+    if os.path.exists(obj):
+        return obj
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("g++ not found")
+    tmp = obj + ".tmp.o"
+    r = subprocess.run([cxx] + flags + ["-c", src, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, obj)
+    return obj
+
+
 def _compile(src: str, obj: str, headers) -> str:
     if os.path.exists(obj):
         return obj
@@ -53,6 +93,20 @@ def _compile(src: str, obj: str, headers) -> str:
         raise RuntimeError(f"nvcc failed for {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, obj)
     return obj
+
+
+def _link(out: str, cmd, objs, libs, stamp_name: str):
+    key = _digest(objs, cmd + libs)
+    stamp = os.path.join(BUILD, stamp_name)
+    if os.path.exists(out) and os.path.exists(stamp) and open(stamp).read() == key:
+        return
+    tmp = out + ".tmp"
+    r = subprocess.run(cmd + ["-o", tmp] + objs + libs, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of {os.path.basename(out)} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+    with open(stamp, "w") as f:
+        f.write(key)
 
 
 def build(verbose: bool = False) -> str:
@@ -70,25 +124,21 @@ def build(verbose: bool = False) -> str:
             obj = os.path.join(BUILD, f"{os.path.basename(src)}.{key}.o")
             objs.append(obj)
             futs.append(ex.submit(_compile, src, obj, headers))
+        comp, link, torch_version = _torch_flags()
+        key = _digest([BINDING_SRC] + headers, comp + [torch_version])
+        binding_obj = os.path.join(BUILD, f"bounded_calls.cpp.{key}.o")
+        futs.append(ex.submit(_compile_binding, BINDING_SRC, binding_obj, comp))
         for f in futs:
             f.result()
     # objects of earlier sources or flags are not reused: drop them
-    keep = {os.path.basename(o) for o in objs}
+    keep = {os.path.basename(o) for o in objs + [binding_obj]}
     for old in glob.glob(os.path.join(BUILD, "*.o")):
         if os.path.basename(old) not in keep:
             os.remove(old)
-    link_key = _digest(objs, ["link"])
-    stamp = os.path.join(BUILD, "lib.stamp")
-    if os.path.exists(LIB) and os.path.exists(stamp) and open(stamp).read() == link_key:
-        return LIB
-    tmp = LIB + ".tmp"
-    cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lpthread"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    with open(stamp, "w") as f:
-        f.write(link_key)
+    _link(LIB, [nvcc()] + ARCH + ["-shared"], objs, ["-lpthread"], "lib.stamp")
+    # (the library is found beside the module; its name is what the loader sees)
+    _link(BINDING, [shutil.which("g++") or "c++", "-shared"], [binding_obj],
+          ["-L", PKG, "-l:" + os.path.basename(LIB)] + link, "binding.stamp")
     if verbose:
         print("built", LIB)
     return LIB

@@ -9,7 +9,6 @@ allocates).
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 
 import torch
@@ -18,15 +17,12 @@ from . import _lib
 from ._lib import PA_BF16, PA_F32, check, lib
 
 _DTYPES = {torch.bfloat16: PA_BF16, torch.float32: PA_F32}
-_CONTIGUOUS = torch.contiguous_format
-_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 
 def _dt(t: torch.Tensor) -> int:
-    code = _DTYPES.get(t.dtype)
-    if code is None:
+    if t.dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return code
+    return _DTYPES[t.dtype]
 
 
 def _cuda(t: torch.Tensor, name: str, dtype=None):
@@ -46,74 +42,30 @@ def _require(cond: bool, msg: str):
         raise ValueError(msg)
 
 
-def _int32(x, name) -> int:
-    """A host integer of the C ABI (ctypes would wrap a larger one)."""
-    x = int(x)
-    if not -2147483648 <= x <= 2147483647:
-        raise ValueError(f"{name}={x} does not fit 32 bits")
-    return x
-
-
 def _pairs_ok(pairs) -> bool:
     return pairs.numel() == 0 or (pairs.dim() == 2 and pairs.shape[1] == 2)
 
 
-# the current stream's handle without building a Stream object (2.9 us of a
-# small call's time on the host, against 0.1)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+def _stream(stream=None) -> int:
+    s = stream if stream is not None else torch.cuda.current_stream()
+    return s.cuda_stream
 
 
-def _stream(stream=None, dev=None) -> int:
-    """Handle of `stream`, or of the current stream of device `dev` (default:
-    the current device)."""
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
-    return _raw_stream(torch.cuda.current_device() if dev is None else dev)
+_bounded = None
 
 
-def _device_of(t, name, stream=None) -> int:
-    """The device a call runs on: that of its first tensor, which must be the
-    current one (the library launches there), as must be a stream's."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    cur = torch.cuda.current_device()
-    if dev != cur:
-        raise ValueError(f"{name} is on cuda:{dev}, not on the current device cuda:{cur}")
-    if stream is not None and stream.device.index != dev:
-        raise ValueError(f"stream must belong to the current device cuda:{dev}")
-    return dev
-
-
-def _refuse(dev, *specs):
-    """Raise for the first tensor at fault of a call that runs on device `dev`:
-    specs are (tensor, name, dtype, whether it must be contiguous).  A call
-    asks all its tensors in one expression first and comes here only when one
-    of them fails (small calls are bound by the host)."""
-    for t, name, dtype, contiguous in specs:
-        if t.get_device() != dev:
-            raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if contiguous and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-
-
-def _check_out(out, dtype, dev):
-    if out.get_device() != dev or out.dtype is not dtype or not out.is_contiguous():
-        _refuse(dev, (out, "out", dtype, True))
-
-
-def _new_like(t, stream):
-    """A contiguous output shaped like t, allocated on the stream that
-    will write it (memory that earlier work of that stream freed is then
-    reused in its order)."""
-    if stream is None:
-        return torch.empty_like(t, memory_format=_CONTIGUOUS)
-    with torch.cuda.stream(stream):
-        return torch.empty_like(t, memory_format=_CONTIGUOUS)
+def _calls():
+    """The extension module that binds the bounded-cache calls (rotary store,
+    compaction, windowed decode and prefill): the same checks and marshalling
+    as here, in C++, because small calls are bound by their time on the host.
+    They run on the device of their tensors."""
+    global _bounded
+    if _bounded is None:
+        lib()  # the library, or its error if it has not been built
+        from . import _bounded_calls
+        _bounded_calls.set_check(check)
+        _bounded = _bounded_calls
+    return _bounded
 
 
 def set_validate(on: bool):
@@ -157,21 +109,6 @@ def reshape_and_cache(k_new, v_new, k_cache, v_cache, slot_mapping, stream=None)
         _stream(stream)))
 
 
-def _token_rows(t, name, T, H, d):
-    """Elements between tokens of [T][H][d] whose heads are contiguous."""
-    if t.shape != (T, H, d):
-        raise ValueError(f"{name} must be [{T}][{H}][{d}]")
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != d and H > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s0 if T > 1 else H * d
-
-
-@functools.lru_cache(maxsize=64)
-def _int_array(values):
-    return (ctypes.c_int * len(values))(*values)
-
-
 def rope_reshape_and_cache(q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, inv_freq,
                            sections=None, interleaved=False, q_out=None, stream=None):
     """Rotary positions and the store of the new rows in one launch
@@ -184,45 +121,8 @@ def rope_reshape_and_cache(q, k_new, v_new, k_cache, v_cache, slot_mapping, posi
     of frequencies of each axis in `sections`.  inv_freq: float32 [rot/2];
     elements from rot on are copied.  Pairs are (i, i + rot/2), or (2i, 2i + 1)
     if interleaved.  Returns the rotated queries (q_out, which may be q)."""
-    _require(q.dim() == 3 and k_new.dim() == 3 and k_cache.dim() == 4,
-             "q must be [T][Hq][d], k_new and v_new [T][Hkv][d], pools [NB][Hkv][bs][d]")
-    NB, Hkv, bs, d = k_cache.shape
-    T, Hq, _ = q.shape
-    _require(v_cache.shape == k_cache.shape, "k_cache and v_cache must have the same shape")
-    if slot_mapping.shape != (T,):
-        raise ValueError(f"slot_mapping must be [{T}]")
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    if positions.shape != (T,) and positions.shape != (axes, T):
-        raise ValueError(f"positions must be [{T}] or [axes][{T}]")
-    _require(inv_freq.dim() == 1, "inv_freq must be [rot/2]")
-    half = inv_freq.shape[0]
-    sections = (half,) if sections is None else tuple(sections)
-    if len(sections) != axes:
-        raise ValueError(f"sections must name the frequencies of each of {axes} axes")
-    qs = _token_rows(q, "q", T, Hq, d)
-    ks = _token_rows(k_new, "k_new", T, Hkv, d)
-    vs = _token_rows(v_new, "v_new", T, Hkv, d)
-    os_ = Hq * d if q_out is None else _token_rows(q_out, "q_out", T, Hq, d)
-    dev, dt = _device_of(q, "q", stream), k_cache.dtype
-    if q_out is None:
-        q_out = _new_like(q, stream)
-    if not (q.dtype is dt and k_new.dtype is dt and v_new.dtype is dt and v_cache.dtype is dt
-            and q_out.dtype is dt and slot_mapping.dtype is _I64 and positions.dtype is _I64
-            and inv_freq.dtype is _F32 and k_cache.is_contiguous() and v_cache.is_contiguous()
-            and slot_mapping.is_contiguous() and positions.is_contiguous()
-            and inv_freq.is_contiguous() and k_new.get_device() == v_new.get_device()
-            == k_cache.get_device() == v_cache.get_device() == slot_mapping.get_device()
-            == positions.get_device() == inv_freq.get_device() == q_out.get_device() == dev):
-        _refuse(dev, (q, "q", dt, False), (k_new, "k_new", dt, False), (v_new, "v_new", dt, False),
-                (k_cache, "k_cache", dt, True), (v_cache, "v_cache", dt, True),
-                (slot_mapping, "slot_mapping", _I64, True), (positions, "positions", _I64, True),
-                (inv_freq, "inv_freq", _F32, True), (q_out, "q_out", dt, False))
-    check(lib().pa_rope_reshape_and_cache(
-        q_out.data_ptr(), os_, q.data_ptr(), qs, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
-        k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
-        inv_freq.data_ptr(), _int_array(sections), axes, 1 if interleaved else 0, T, NB, Hq, Hkv, bs,
-        d, 2 * half, _dt(k_cache), _stream(stream, dev)))
-    return q_out
+    return _calls().rope_reshape_and_cache(q, k_new, v_new, k_cache, v_cache, slot_mapping, positions,
+                                           inv_freq, sections, interleaved, q_out, stream)
 
 
 def copy_blocks(k_cache, v_cache, pairs, stream=None):
@@ -274,31 +174,7 @@ def compact_cache(k_cache, v_cache, src_table, dst_table, keep, keep_lens, strea
     written must not be read by the call).  keep: int32 [B][Hkv][max_keep],
     for each KV head the kept positions in ascending order; keep_lens: int32
     [B], how many of them count.  The pools are written in place, bit exact."""
-    _require(k_cache.dim() == 4, "pools must be [NB][Hkv][bs][d]")
-    NB, Hkv, bs, d = k_cache.shape
-    _require(v_cache.shape == k_cache.shape, "k_cache and v_cache must have the same shape")
-    if keep.dim() != 3 or keep.shape[1] != Hkv:
-        raise ValueError(f"keep must be [B][{Hkv}][max_keep]")
-    B, max_keep = keep.shape[0], keep.shape[2]
-    for name, t in (("src_table", src_table), ("dst_table", dst_table)):
-        if t.dim() != 2 or t.shape[0] != B or t.shape[1] == 0:
-            raise ValueError(f"{name} must be [{B}][blocks]")
-    if keep_lens.shape != (B,):
-        raise ValueError(f"keep_lens must be [{B}]")
-    dev, dt = _device_of(k_cache, "k_cache", stream), k_cache.dtype
-    if not (v_cache.dtype is dt and src_table.dtype is _I32 and dst_table.dtype is _I32
-            and keep.dtype is _I32 and keep_lens.dtype is _I32 and k_cache.is_contiguous()
-            and v_cache.is_contiguous() and src_table.is_contiguous()
-            and dst_table.is_contiguous() and keep.is_contiguous() and keep_lens.is_contiguous()
-            and v_cache.get_device() == src_table.get_device() == dst_table.get_device()
-            == keep.get_device() == keep_lens.get_device() == dev):
-        _refuse(dev, (k_cache, "k_cache", dt, True), (v_cache, "v_cache", dt, True),
-                (src_table, "src_table", _I32, True), (dst_table, "dst_table", _I32, True),
-                (keep, "keep", _I32, True), (keep_lens, "keep_lens", _I32, True))
-    check(lib().pa_compact_cache(
-        k_cache.data_ptr(), v_cache.data_ptr(), src_table.data_ptr(), src_table.shape[1],
-        dst_table.data_ptr(), dst_table.shape[1], keep.data_ptr(), max_keep, keep_lens.data_ptr(), B,
-        NB, Hkv, bs, d, _dt(k_cache), _stream(stream, dev)))
+    _calls().compact_cache(k_cache, v_cache, src_table, dst_table, keep, keep_lens, stream)
 
 
 def decode_workspace_size(B, Hq, head_dim, max_blocks_per_seq, block_size, partition_tokens=0):
@@ -340,16 +216,13 @@ def decode_tile_for(Hq, Hkv, head_dim, block_size, num_blocks, dtype=torch.bfloa
 
 
 def _check_decode_shapes(q, k_cache, v_cache, block_table, context_lens, out):
-    # (messages are formatted only when raised: this runs in front of every call)
     _require(q.dim() == 3 and k_cache.dim() == 4, "q must be [B][Hq][d], pools [NB][Hkv][bs][d]")
     B, Hq, d = q.shape
-    if k_cache.shape[3] != d:
-        raise ValueError(f"pools must have head_dim {d} like q")
+    _require(k_cache.shape[3] == d, f"pools must have head_dim {d} like q")
     _require(v_cache.shape == k_cache.shape, "k_cache and v_cache must have the same shape")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must be [{B}][max_blocks_per_seq]")
-    if context_lens.shape != (B,):
-        raise ValueError(f"context_lens must be [{B}]")
+    _require(block_table.dim() == 2 and block_table.shape[0] == B,
+             f"block_table must be [{B}][max_blocks_per_seq]")
+    _require(context_lens.shape == (B,), f"context_lens must be [{B}]")
     _require(out is None or out.shape == q.shape, "out must have the shape of q")
 
 
@@ -547,28 +420,8 @@ def decode_window(q, k_cache, v_cache, block_table, context_lens, window, num_si
     block_table whose block holds no visible token are not read (the page may
     have been freed); a row of length 0 gets zeros.  No workspace.  Returns
     out [B][Hq][d]."""
-    _check_decode_shapes(q, k_cache, v_cache, block_table, context_lens, out)
-    B, Hq, d = q.shape
-    NB, Hkv, bs, _ = k_cache.shape
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    dev, dt = _device_of(q, "q", stream), k_cache.dtype
-    if not (q.dtype is dt and v_cache.dtype is dt and block_table.dtype is _I32
-            and context_lens.dtype is _I32 and q.is_contiguous() and k_cache.is_contiguous()
-            and v_cache.is_contiguous() and block_table.is_contiguous()
-            and context_lens.is_contiguous() and k_cache.get_device() == v_cache.get_device()
-            == block_table.get_device() == context_lens.get_device() == dev):
-        _refuse(dev, (q, "q", dt, True), (k_cache, "k_cache", dt, True),
-                (v_cache, "v_cache", dt, True), (block_table, "block_table", _I32, True),
-                (context_lens, "context_lens", _I32, True))
-    if out is None:
-        out = _new_like(q, stream)
-    else:
-        _check_out(out, dt, dev)
-    check(lib().pa_decode_window(
-        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-        block_table.shape[1], context_lens.data_ptr(), B, Hq, Hkv, d, bs, NB, scale,
-        _int32(window, "window"), _int32(num_sinks, "num_sinks"), _dt(q), _stream(stream, dev)))
-    return out
+    return _calls().decode_window(q, k_cache, v_cache, block_table, context_lens, window, num_sinks,
+                                  scale, out, stream)
 
 
 def prefill_chunk(q, k_cache, v_cache, block_table, query_start, context_lens, max_query_len,
@@ -613,38 +466,5 @@ def prefill_window(q, k_cache, v_cache, block_table, query_start, context_lens, 
     block_table whose block no query of the request sees are not read (the
     page may have been freed).  Rows of q outside every request get no
     result.  Returns out [tokens][Hq][d]."""
-    _require(q.dim() == 3 and k_cache.dim() == 4 and context_lens.dim() == 1,
-             "q must be [tokens][Hq][d], pools [NB][Hkv][bs][d], context_lens [R]")
-    Tq, Hq, d = q.shape
-    NB, Hkv, bs, _ = k_cache.shape
-    R = context_lens.shape[0]
-    if k_cache.shape[3] != d:
-        raise ValueError(f"pools must have head_dim {d} like q")
-    _require(v_cache.shape == k_cache.shape, "k_cache and v_cache must have the same shape")
-    if query_start.shape != (R + 1,):
-        raise ValueError(f"query_start must be [{R + 1}]")
-    if block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError(f"block_table must be [{R}][max_blocks_per_seq]")
-    _require(out is None or out.shape == q.shape, "out must have the shape of q")
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    dev, dt = _device_of(q, "q", stream), k_cache.dtype
-    if not (q.dtype is dt and v_cache.dtype is dt and block_table.dtype is _I32
-            and query_start.dtype is _I32 and context_lens.dtype is _I32 and q.is_contiguous()
-            and k_cache.is_contiguous() and v_cache.is_contiguous()
-            and block_table.is_contiguous() and query_start.is_contiguous()
-            and context_lens.is_contiguous() and k_cache.get_device() == v_cache.get_device()
-            == block_table.get_device() == query_start.get_device()
-            == context_lens.get_device() == dev):
-        _refuse(dev, (q, "q", dt, True), (k_cache, "k_cache", dt, True),
-                (v_cache, "v_cache", dt, True), (block_table, "block_table", _I32, True),
-                (query_start, "query_start", _I32, True), (context_lens, "context_lens", _I32, True))
-    if out is None:
-        out = _new_like(q, stream)
-    else:
-        _check_out(out, dt, dev)
-    check(lib().pa_prefill_window(
-        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-        block_table.shape[1], query_start.data_ptr(), context_lens.data_ptr(), R, Tq,
-        _int32(max_query_len, "max_query_len"), Hq, Hkv, d, bs, NB, scale, _int32(window, "window"),
-        _int32(num_sinks, "num_sinks"), _dt(q), _stream(stream, dev)))
-    return out
+    return _calls().prefill_window(q, k_cache, v_cache, block_table, query_start, context_lens,
+                                   max_query_len, window, num_sinks, scale, out, stream)

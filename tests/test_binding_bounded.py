@@ -230,8 +230,25 @@ def test_prefill_window_c_refusals(lib, kw, code):
     assert bool(lib.pa_last_error_string()) == (code != 0)
 
 
-@pytest.mark.parametrize("x", [2 ** 31, -2 ** 31 - 1, 2 ** 40 + 5])
-def test_host_integers_that_would_wrap(x):
+@pytest.mark.parametrize("x", [2 ** 31, -2 ** 31 - 1, 2 ** 70])
+@pytest.mark.parametrize("name", ["window", "num_sinks"])
+def test_host_integers_that_would_wrap(x, name):
     with pytest.raises(ValueError, match="32 bits"):
-        ops._int32(x, "window")
-    assert ops._int32(2 ** 31 - 1, "window") == 2 ** 31 - 1
+        ops.decode_window(**{**window_args(), name: x})
+    with pytest.raises(ValueError, match="32 bits"):
+        ops.prefill_window(**{**prefill_args(), name: x})
+
+
+@pytest.mark.parametrize("bad", [dict(window=3.5), dict(window=None), dict(scale="x")])
+def test_host_arguments_of_other_types(bad):
+    with pytest.raises(TypeError):
+        ops.decode_window(**{**window_args(), **bad})
+
+
+def test_things_that_are_no_tensors():
+    with pytest.raises(ValueError, match="v_cache must be a CUDA tensor"):
+        ops.decode_window(**{**window_args(), "v_cache": None})
+    with pytest.raises(TypeError):
+        ops.rope_reshape_and_cache(**{**rope_args(), "sections": 64})
+    with pytest.raises(ValueError, match="1 to 4 axes"):
+        ops.rope_reshape_and_cache(**{**rope_args(), "sections": (1, 1, 1, 1, 60)})

@@ -193,12 +193,29 @@ def test_streams_and_graphs():
     assert torch.equal(o1, half) and not torch.equal(o1, ra)
 
 
-def test_other_current_device_is_refused(monkeypatch):
+def test_tensors_elsewhere_and_of_other_types_are_refused():
     from paged_kv_cache_192_gb300 import ops
     bt = batch([30], 16, 0)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
-    with pytest.raises(ValueError, match="current device"):
-        ops.decode_window(bt.q_t, bt.k_cache, bt.v_cache, bt.table_t, bt.lens_t, 16)
+    args = dict(q=bt.q_t, k_cache=bt.k_cache, v_cache=bt.v_cache, block_table=bt.table_t,
+                context_lens=bt.lens_t, window=16)
+    for name in ("k_cache", "v_cache", "block_table", "context_lens"):
+        with pytest.raises(ValueError, match=f"{name} must be a CUDA tensor on cuda:0"):
+            ops.decode_window(**{**args, name: args[name].cpu()})
+    for name, other in (("q", f32), ("v_cache", f32), ("block_table", torch.int64),
+                        ("context_lens", torch.int64)):
+        with pytest.raises(TypeError, match=f"{name} must be"):
+            ops.decode_window(**{**args, name: args[name].to(other)})
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        ops.decode_window(**{**args, **{n: args[n].half() for n in ("q", "k_cache", "v_cache")}})
+    wide = torch.zeros(1, 8, 256, dtype=bf16, device=DEV)
+    with pytest.raises(ValueError, match="q must be contiguous"):
+        ops.decode_window(**{**args, "q": wide[..., ::2]})
+    with pytest.raises(ValueError, match="out must be contiguous"):
+        ops.decode_window(**{**args, "out": wide[..., ::2]})
+    with pytest.raises(TypeError, match="out must be"):
+        ops.decode_window(**{**args, "out": torch.zeros(1, 8, 128, device=DEV)})
+    with pytest.raises(AttributeError):
+        ops.decode_window(**args, stream=7)
 
 
 def test_empty_batch():
