@@ -11,7 +11,8 @@
 // for a status of the library.
 #include <Python.h>
 
-#include <ATen/ops/empty_like.h>
+#include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -124,7 +125,7 @@ struct Place {
         return t.data_ptr();
     }
     at::Tensor new_like(const at::Tensor &t) const {
-        return at::empty_like(t, t.options(), at::MemoryFormat::Contiguous);
+        return at::Tensor(at::detail::empty_cuda(t.sizes(), t.scalar_type(), t.device(), std::nullopt));
     }
 };
 

@@ -13,8 +13,9 @@
 // without a workspace: the visible tiles are split evenly over the cluster's
 // warps; each warp streams its tiles through its own ring of shared-memory
 // stages (as the persistent decode kernel does) with a running maximum and
-// sum; the warps' results meet in shared memory, the CTAs' in distributed
-// shared memory, each CTA finishing 1/C of the item's output.
+// sum; the warps' results meet in shared memory, and each CTA sends its part of
+// every 1/C of the item's output to the CTA that finishes it (distributed
+// shared memory, one cluster barrier).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -29,6 +30,7 @@ namespace {
 using namespace pa::dec;
 
 constexpr int kNW = 4;  // warps per CTA
+constexpr int kMaxCluster = 16;
 
 struct WindowParams {
     void *out;
@@ -71,9 +73,11 @@ struct Layout {
     using TO = TileOf<T, D, GQ, DEEP>;
     static constexpr int WARP = TO::NST * TO::STAGE;  // ring of a warp, then its result
     static constexpr int OFF_P = kNW * WARP;
-    static constexpr int OFF_CTA = OFF_P + kNW * TO::PBUF;   // the CTA's result: acc [GQ][D]
-    static constexpr int OFF_ML = OFF_CTA + GQ * D * 4;      // its (max, sum) [GQ]
-    static constexpr int OFF_WML = OFF_ML + GQ * 8;          // the warps' (max, sum) [kNW][GQ]
+    // received from the cluster's CTAs: their acc of this CTA's outputs [C][GQ
+    // * D / C] and their (max, sum) [C][GQ]
+    static constexpr int OFF_CTA = OFF_P + kNW * TO::PBUF;
+    static constexpr int OFF_ML = OFF_CTA + GQ * D * 4;
+    static constexpr int OFF_WML = OFF_ML + kMaxCluster * GQ * 8;  // the warps' (max, sum) [kNW][GQ]
     static constexpr int OFF_BAR = OFF_WML + kNW * GQ * 8;
     static constexpr int SMEM = OFF_BAR + kNW * TO::NST * 8 + 1024;
     static_assert(GQ * D * 4 <= WARP, "a warp's result must fit its ring");
@@ -90,8 +94,10 @@ __device__ __forceinline__ uint32_t cluster_nctarank() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t rank) {
@@ -99,10 +105,9 @@ __device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
-    return v;
+__device__ __forceinline__ void st_cluster2(uint32_t addr, float2 v) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(addr), "f"(v.x), "f"(v.y)
+                 : "memory");
 }
 
 template <typename T>
@@ -186,7 +191,9 @@ __global__ void __launch_bounds__(kNW * 32, (TileOf<T, D, GQ, DEEP>::MINB))
         pa::fence_barrier_init();
     }
     __syncwarp();
+    if (C > 1) cluster_arrive();  // this CTA runs: the others may write to it (waited for below)
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- the visible tiles and this warp's share ------------------------------
     Visible vis;
@@ -302,9 +309,11 @@ __global__ void __launch_bounds__(kNW * 32, (TileOf<T, D, GQ, DEEP>::MINB))
     __syncwarp();
     put_result(st, reinterpret_cast<float *>(ring), wml + warp * GQ);
     __syncthreads();
-    float *cta_acc = reinterpret_cast<float *>(smem + Lay::OFF_CTA);
-    float2 *cta_ml = reinterpret_cast<float2 *>(smem + Lay::OFF_ML);
+    float *in_acc = reinterpret_cast<float *>(smem + Lay::OFF_CTA);
+    float2 *in_ml = reinterpret_cast<float2 *>(smem + Lay::OFF_ML);
     T *out = static_cast<T *>(p.out) + (static_cast<size_t>(b) * p.Hq + hk * GQ) * D;
+    const int share = GQ * D / C;  // outputs of a CTA; a multiple of 2: GQ * D >= 64, C <= 16
+    if (C > 1) cluster_wait();     // every CTA of the cluster has started
     for (int x = threadIdx.x * 2; x < GQ * D; x += kNW * 64) {
         const int h = x / D;
         float M = -INFINITY, l = 0.f;
@@ -323,30 +332,31 @@ __global__ void __launch_bounds__(kNW * 32, (TileOf<T, D, GQ, DEEP>::MINB))
             const float inv = vis.L > 0 ? 1.f / l : 0.f;
             store2(out + x, make_float2(a.x * inv, a.y * inv));
         } else {
-            *reinterpret_cast<float2 *>(cta_acc + x) = a;
-            if (x % D == 0) cta_ml[h] = make_float2(M, l);
+            const int to = x / share;
+            st_cluster2(map_cta(pa::smem_u32(in_acc + rank * share + x % share), to), a);
+            if (x % share == 0 || x % D == 0)
+                st_cluster2(map_cta(pa::smem_u32(in_ml + rank * GQ + h), to), make_float2(M, l));
         }
     }
     if (C == 1) return;
-    // ---- the cluster's result: this CTA finishes 1/C of the item's outputs ------
-    cluster_sync();
-    const int share = GQ * D / C;  // a multiple of 2: GQ * D >= 64, C <= 16
-    for (int x = rank * share + threadIdx.x * 2; x < (rank + 1) * share; x += kNW * 64) {
-        const int h = x / D;
-        const uint32_t aa = pa::smem_u32(cta_acc + x), am = pa::smem_u32(cta_ml + h);
+    // ---- this CTA's outputs ---------------------------------------------------------
+    cluster_arrive();
+    cluster_wait();  // nothing is sent after this: a CTA may exit before the others
+    for (int x = threadIdx.x * 2; x < share; x += kNW * 64) {
+        const int h = (rank * share + x) / D;
         float M = -INFINITY, l = 0.f;
-        for (int c = 0; c < C; ++c) M = fmaxf(M, ld_cluster2(map_cta(am, c)).x);
+        for (int c = 0; c < C; ++c) M = fmaxf(M, in_ml[c * GQ + h].x);
         float2 a = make_float2(0.f, 0.f);
         for (int c = 0; c < C; ++c) {
-            const float2 ml = ld_cluster2(map_cta(am, c)), v = ld_cluster2(map_cta(aa, c));
+            const float2 ml = in_ml[c * GQ + h];
+            const float2 v = *reinterpret_cast<const float2 *>(in_acc + c * share + x);
             const float f = weight(ml.x, M);
             l += f * ml.y;
             a = pa::ffma2(make_float2(f, f), v, a);
         }
         const float inv = vis.L > 0 ? 1.f / l : 0.f;
-        store2(out + x, make_float2(a.x * inv, a.y * inv));
+        store2(out + rank * share + x, make_float2(a.x * inv, a.y * inv));
     }
-    cluster_sync();  // the others may still read this CTA's result
 }
 
 int sm_count() {
@@ -435,10 +445,10 @@ int launch(const WindowParams &p, cudaStream_t stream) {
     const int64_t tokens = std::min<int64_t>(int64_t(p.MB) << p.bs_log2, int64_t(p.sinks) + p.window);
     const int64_t tiles = (tokens + TT - 1) / TT;
     auto fits = [&](int c) {
-        return tiles >= 2 * kNW * c && items * c <= slots && (c < 16 || items <= 16);
+        return tiles >= 2 * kNW * c && items * c <= slots && (c < kMaxCluster || items <= 16);
     };
     int c = 1;
-    while (c < 16 && fits(2 * c)) c *= 2;
+    while (c < kMaxCluster && fits(2 * c)) c *= 2;
     if constexpr (TO::MMA) {
         // A last wave of fewer CTAs than SMs leaves memory idle, each CTA alone
         // on its SM: the time lost, as a part of the whole.  The deeper ring has
