@@ -63,6 +63,26 @@ def test_long(L, n, W, S):
     bt.check(run(bt))
 
 
+@pytest.mark.parametrize("L,n,W,S", [(2500, 1, 2200, 4), (2500, 20, 2200, 0), (1100, 40, 1000, 70),
+                                     (600, 30, 500, 3), (300, 70, 100, 64), (70, 70, 20, 2), (3, 3, 9, 0)])
+@pytest.mark.parametrize("d,gq,bs", [(128, 4, 16), (64, 1, 128), (64, 8, 8), (128, 2, 64)])
+def test_few_query_tiles(L, n, W, S, d, gq, bs):
+    """Batches so small that a cluster divides the keys of one query tile, from
+    one CTA to the largest cluster, down to fewer K/V tiles than CTAs."""
+    bt = batch([L, L // 2 + n], [n, n // 2], W, S, Hq=2 * gq, Hkv=2, d=d, bs=bs, seed=L + d)
+    bt.check(run(bt))
+
+
+def test_overlapping_requests_do_not_pass_the_grid():
+    """Row ranges that overlap (no prefix sum) make more query tiles than the
+    rows bound: recorded, and nothing is read or written out of range."""
+    from paged_kv_cache_192_gb300 import ops
+    bt = batch([200, 200, 200, 200], [50, 50, 50, 50], 64, 0)
+    start = torch.tensor([0, 200, 0, 200, 0], dtype=torch.int32, device=DEV)
+    ops.prefill_window(bt.q_t, bt.k_cache, bt.v_cache, bt.table_t, start, bt.lens_t, 50, 64)
+    assert ops.device_error() == 1
+
+
 @pytest.mark.parametrize("R", [300, 1300])
 def test_many_requests(R):
     """More items than CTAs, and more requests than one launch holds."""
