@@ -368,8 +368,7 @@ int sm_count() {
 }
 
 // CTAs of a kernel that run at once on the current device (0: unknown); looked
-// up once per kernel and device, where clusters of 16 CTAs, past the portable
-// size of 8, are also allowed.
+// up once per kernel and device.
 template <typename K>
 int concurrent_ctas(K kern, size_t smem, std::atomic<int> (&cache)[64]) {
     int dev = 0;
@@ -378,8 +377,7 @@ int concurrent_ctas(K kern, size_t smem, std::atomic<int> (&cache)[64]) {
         if (const int n = cache[dev].load(std::memory_order_relaxed)) return n;
     int per_sm = 0;
     const int sms = sm_count();
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kNW * 32, smem) != cudaSuccess)
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kNW * 32, smem) != cudaSuccess)
         return 0;
     if (dev < 64) cache[dev].store(per_sm * sms, std::memory_order_relaxed);
     return per_sm * sms;
@@ -436,19 +434,23 @@ int launch(const WindowParams &p, cudaStream_t stream) {
     if (slots <= 0 || sms <= 0)
         return pa::cuda_fail(cudaGetLastError(), "decode_window: kernel attributes");
     // Cluster size: the largest that leaves every warp two tiles and all
-    // clusters running at once (clusters of 16 sit two to a GPC).  A second
-    // wave of clusters costs more than the split gains: window 4096, 8 KV heads,
-    // 4 sequences: 16.0 us with clusters of 8, 30.4 with 16; 16 sequences of
-    // window 1024: 15.9 us with clusters of 2, 21.4 with 4.  One sequence: window
-    // 8192 13.4 us with clusters of 16, 18.5 with 8.
+    // clusters running at once.  A second wave of clusters costs more than the
+    // split gains: window 4096, 8 KV heads, 4 sequences: 16.0 us with clusters of
+    // 8, 30.4 with 16; 16 sequences of window 1024: 15.9 us with clusters of 2,
+    // 21.4 with 4.  One sequence: window 8192 12.1 us with clusters of 16, 18.5
+    // with 8.
+    static std::atomic<int> cache[64][5];
     const int64_t items = int64_t(p.B) * p.Hkv;
     const int64_t tokens = std::min<int64_t>(int64_t(p.MB) << p.bs_log2, int64_t(p.sinks) + p.window);
     const int64_t tiles = (tokens + TT - 1) / TT;
-    auto fits = [&](int c) {
-        return tiles >= 2 * kNW * c && items * c <= slots && (c < kMaxCluster || items <= 16);
-    };
     int c = 1;
-    while (c < kMaxCluster && fits(2 * c)) c *= 2;
+    while (c < kMaxCluster && tiles >= 2 * kNW * 2 * c && items * 2 * c <= slots) {
+        const int n = pa::pf::clusters_at_once(decode_window_kernel<T, D, GQ, false>, kNW * 32,
+                                               Layout<T, D, GQ, false>::SMEM, 2 * c, cache);
+        if (n < 0) return pa::cuda_fail(cudaGetLastError(), "decode_window: occupancy");
+        if (items > n) break;
+        c *= 2;
+    }
     if constexpr (TO::MMA) {
         // A last wave of fewer CTAs than SMs leaves memory idle, each CTA alone
         // on its SM: the time lost, as a part of the whole.  The deeper ring has

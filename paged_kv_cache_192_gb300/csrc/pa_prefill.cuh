@@ -113,6 +113,34 @@ inline int set_smem_once(K kern, size_t smem, std::atomic<uint64_t> *done) {
     return PA_OK;
 }
 
+// Clusters of c CTAs (a power of two up to 16) of `kern` that run at once on
+// the current device; looked up once per kernel, device and size in `cache`.
+// -1: a CUDA call failed.  The kernel's shared-memory limit must be set.
+template <typename K>
+inline int clusters_at_once(K kern, int threads, size_t smem, int c, std::atomic<int> (&cache)[64][5]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+    const int i = log2_int(c);
+    if (dev < 64)
+        if (const int n = cache[dev][i].load(std::memory_order_relaxed)) return n - 1;
+    if (c > 8 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return -1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(c), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return -1;
+    if (dev < 64) cache[dev][i].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
 // Persistent tcgen05 prefill (pa_prefill_persist.cu): one CTA per SM runs a
 // list of (request, 256 query rows, KV head) items.  Usable when the batch
 // has at most 256 (request, query tile) pairs and 512 items, with the block

@@ -82,8 +82,10 @@ struct WLayout {
 
 // The split kernel: one query tile, and rings of their own for K and V (a K
 // tile is free once its scores are there, a V tile only after the softmax).
-// At the end the rings receive the cluster's partial O [2 C][D / C / 4][128] x 4
-// columns and the query tile's place their (max, sum) [2 C][128].
+// At the end the rings' place holds what the cluster's CTAs send of this CTA's
+// columns, [C][D / C / 4][128] x 4 columns, and behind it what the two groups
+// exchange, [2][D / 8][128] x 4; the query tile's place holds the (max, sum) of
+// each, [C][128] and [2][128].
 template <int D>
 struct SLayout {
     static constexpr int NST = 5;
@@ -103,8 +105,9 @@ struct SLayout {
     static constexpr int OFF_REQ = OFF_MISC + 16;
     static constexpr int SMEM = OFF_REQ + int(sizeof(ReqTables)) + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
-    static_assert(2 * 128 * D * 4 <= OFF_BAR - OFF_K, "the partial O must fit the rings");
-    static_assert(2 * MAX_C * 128 * 8 <= QT_BYTES, "(max, sum) must fit the query tile");
+    static constexpr int X_BYTES = 128 * D * 4;  // received, and as much exchanged
+    static_assert(2 * X_BYTES <= OFF_BAR - OFF_K, "the partial O must fit the rings");
+    static_assert((MAX_C + 2) * 128 * 8 <= QT_BYTES, "(max, sum) must fit the query tile");
     static_assert(OFF_BAR % 8 == 0 && OFF_REQ % 4 == 0, "alignment");
 };
 
@@ -843,59 +846,112 @@ __global__ void __launch_bounds__(SLayout<D>::THREADS, 1)
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     };
     __syncwarp();
-    cluster_sync();
-    const int cols = D / C;  // columns that a CTA finishes: 16 or more
+    if (C > 1) cluster_sync();
+    else __syncthreads();
     auto at = [](uint32_t addr, uint32_t cta) {
         uint32_t r;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
         return r;
     };
+    const int cols = D / C;  // columns that a CTA finishes: 16 or more
+    const int t = I.t0 + row / GQ;
+    __nv_bfloat16 *dst = p.out + (static_cast<size_t>(I.qs + min(t, I.n - 1)) * p.Hq + I.hk * GQ +
+                                  row % GQ) * D;
+    float2 *ml = reinterpret_cast<float2 *>(smem), *xml = ml + Lay::MAX_C * 128;
     if (!idle && warp < 8) {
+        // The two groups first: each takes half of the columns, gives the other
+        // its part of the other half, and sums what it has to its own weights.
+        float4 *xs = reinterpret_cast<float4 *>(smem + Lay::OFF_K + Lay::X_BYTES);
         const bool any = wg < nt;  // this group had a tile
-        const uint32_t part = 2 * rank + wg;
+        const uint32_t o_addr = lane_base + wg * 128;
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 16) {
+        for (int c0 = 0; c0 < D / 2; c0 += 16) {
             uint32_t u[16];
-            pa::tc::ld16(lane_base + wg * 128 + c0, u);
+            pa::tc::ld16(o_addr + (wg ^ 1) * (D / 2) + c0, u);
             pa::tc::wait_ld();
-            const uint32_t to = c0 / cols, cc = (c0 % cols) / 4;
-            const uint32_t dst = at(sk + ((part * (cols / 4) + cc) * 128 + row) * 16, to);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                asm volatile("st.shared::cluster.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + k * 128 * 16),
-                             "r"(any ? u[4 * k] : 0u), "r"(any ? u[4 * k + 1] : 0u),
-                             "r"(any ? u[4 * k + 2] : 0u), "r"(any ? u[4 * k + 3] : 0u)
-                             : "memory");
+                xs[(wg * (D / 8) + c0 / 4 + k) * 128 + row] =
+                    make_float4(__uint_as_float(u[4 * k]), __uint_as_float(u[4 * k + 1]),
+                                __uint_as_float(u[4 * k + 2]), __uint_as_float(u[4 * k + 3]));
         }
-        for (uint32_t to = 0; to < C; ++to)
-            asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(
-                             at(sq + (part * 128 + row) * 8, to)),
-                         "f"(m_used), "f"(lsum)
-                         : "memory");
+        xml[wg * 128 + row] = make_float2(m_used, lsum);
+        asm volatile("bar.sync 1, 256;" ::: "memory");  // the eight softmax warps
+        const float2 other = xml[(wg ^ 1) * 128 + row];
+        const float M = fmaxf(m_used, other.x);
+        const float fm = m_used == -INFINITY ? 0.f : exp2f(m_used - M);
+        const float fo = other.x == -INFINITY ? 0.f : exp2f(other.x - M);
+        const float l = lsum * fm + other.y * fo;
+        const bool any_other = (wg ^ 1) < nt;
+        const float inv = C == 1 ? 1.f / l : 1.f;
+        // rows past the request's tokens travel only with one that is not
+        const bool wanted = __any_sync(pa::kFull, t < I.n);
+#pragma unroll 1
+        for (int c0 = 0; c0 < D / 2 && wanted; c0 += 16) {
+            uint32_t u[16];
+            pa::tc::ld16(o_addr + wg * (D / 2) + c0, u);
+            pa::tc::wait_ld();
+            float o[16];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 v = xs[((wg ^ 1) * (D / 8) + c0 / 4 + k) * 128 + row];
+                const float vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[4 * k + e] = ((any ? __uint_as_float(u[4 * k + e]) * fm : 0.f) +
+                                    (any_other ? vv[e] * fo : 0.f)) * inv;
+            }
+            const int c = wg * (D / 2) + c0;
+            if (C == 1) {
+                if (t < I.n) {
+#pragma unroll
+                    for (int k = 0; k < 16; k += 8)
+                        *reinterpret_cast<uint4 *>(dst + c + k) = make_uint4(
+                            pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]),
+                            pack_bf16(o[k + 4], o[k + 5]), pack_bf16(o[k + 6], o[k + 7]));
+                }
+            } else {
+                const uint32_t to = at(sk + ((rank * (cols / 4) + c % cols / 4) * 128 + row) * 16, c / cols);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(to + k * 128 * 16),
+                                 "f"(o[4 * k]), "f"(o[4 * k + 1]), "f"(o[4 * k + 2]), "f"(o[4 * k + 3])
+                                 : "memory");
+            }
+        }
+        if (wg == 0 && C > 1)
+            for (uint32_t to = 0; to < C; ++to)
+                asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(
+                                 at(sq + (rank * 128 + row) * 8, to)),
+                             "f"(M), "f"(l)
+                             : "memory");
+        pa::tc::fence_before();
     }
-    pa::tc::fence_before();
     __syncwarp();
-    cluster_sync();  // nothing is sent after this: a CTA may exit before the others
-    if (!idle && warp < 8) {
-        const float2 *ml = reinterpret_cast<const float2 *>(smem);
+    if (C > 1) cluster_sync();  // nothing is sent after this: a CTA may exit before the others
+    if (!idle && warp < 8 && C > 1 && t < I.n) {
         const float4 *xs = reinterpret_cast<const float4 *>(smem + Lay::OFF_K);
-        const int parts = 2 * C, t = I.t0 + row / GQ;
-        float M = -INFINITY, l = 0.f;
-        for (int k = 0; k < parts; ++k) M = fmaxf(M, ml[k * 128 + row].x);
-        auto weight = [&](int k) {  // 0 for a part that saw nothing
-            const float m = ml[k * 128 + row].x;
-            return m == -INFINITY ? 0.f : exp2f(m - M);
-        };
-        for (int k = 0; k < parts; ++k) l += weight(k) * ml[k * 128 + row].y;
+        float w[Lay::MAX_C], M = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int k = 0; k < Lay::MAX_C; ++k)
+            if (k < C) M = fmaxf(M, ml[k * 128 + row].x);
+#pragma unroll
+        for (int k = 0; k < Lay::MAX_C; ++k) {
+            w[k] = 0.f;
+            if (k < C) {
+                const float2 v = ml[k * 128 + row];
+                w[k] = v.x == -INFINITY ? 0.f : exp2f(v.x - M);  // 0 for a CTA that saw nothing
+                l += w[k] * v.y;
+            }
+        }
         const float inv = 1.f / l;
-        __nv_bfloat16 *dst = p.out +
-                             (static_cast<size_t>(I.qs + min(t, I.n - 1)) * p.Hq + I.hk * GQ + row % GQ) * D +
-                             rank * cols;
-        // group A's threads finish the first half of the columns, B's the second
+        // group A's threads finish the first half of the CTA's columns, B's the second
         for (int c = wg * (cols / 2); c < (wg + 1) * (cols / 2); c += 8) {
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-            for (int k = 0; k < parts; ++k) {
-                const float f = weight(k) * inv;
+#pragma unroll
+            for (int k = 0; k < Lay::MAX_C; ++k) {
+                if (k >= C) break;
+                const float f = w[k];
                 const float4 u = xs[(k * (cols / 4) + c / 4) * 128 + row];
                 const float4 v = xs[(k * (cols / 4) + c / 4 + 1) * 128 + row];
                 a.x = fmaf(f, u.x, a.x), a.y = fmaf(f, u.y, a.y);
@@ -903,10 +959,9 @@ __global__ void __launch_bounds__(SLayout<D>::THREADS, 1)
                 b.x = fmaf(f, v.x, b.x), b.y = fmaf(f, v.y, b.y);
                 b.z = fmaf(f, v.z, b.z), b.w = fmaf(f, v.w, b.w);
             }
-            if (t < I.n)
-                *reinterpret_cast<uint4 *>(dst + c) =
-                    make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y),
-                               pack_bf16(b.z, b.w));
+            *reinterpret_cast<uint4 *>(dst + rank * cols + c) =
+                make_uint4(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv),
+                           pack_bf16(b.x * inv, b.y * inv), pack_bf16(b.z * inv, b.w * inv));
         }
     }
 
@@ -989,15 +1044,24 @@ int launch(const WinParams &p, const void *q, const void *k_cache, const void *v
         return pa::cuda_fail(cudaGetLastError(), "prefill_window: SM count");
     const int64_t singles = query_tiles(p, max_query_len, 128 / GQ) * p.Hkv;
     if (p.R <= kMaxR && singles <= sms) {
-        // as many CTAs per query tile as there are SMs, each with a K/V tile for
-        // both groups
-        const int64_t keys = std::min<int64_t>(int64_t(p.MB) << p.bs_log2,
-                                               int64_t(p.window) + p.sinks + 128 / GQ);
-        int c = 1;
-        while (2 * c <= SLayout<D>::MAX_C && singles * 2 * c <= sms && keys >= 4 * c * kT2KT) c *= 2;
         auto kern = prefill_window_split_kernel<D, GQ>;
         static std::atomic<uint64_t> done{0};
         if (int rc = set_smem_once(kern, SLayout<D>::SMEM, &done)) return rc;
+        // Clusters as large as run at once, with a K/V tile for each group.  8 KV
+        // heads, d 128: 40 tokens with window 4096 68 us on the kernel above, 44 as
+        // one CTA per query tile, 26.7 in two waves of clusters of 8, 18.0 in one of
+        // 4; 64 tokens of d 64 with that window 60.8, 34.7 and (clusters of 4)
+        // 13.8 us; 256 tokens of window 1024 24.3, 17.6 and (of 2) 13.6 us.
+        static std::atomic<int> cache[64][5];
+        const int64_t keys = std::min<int64_t>(int64_t(p.MB) << p.bs_log2,
+                                               int64_t(p.window) + p.sinks + 128 / GQ);
+        int c = 1;
+        while (2 * c <= SLayout<D>::MAX_C && keys >= 4 * c * kT2KT) {
+            const int n = clusters_at_once(kern, SLayout<D>::THREADS, SLayout<D>::SMEM, 2 * c, cache);
+            if (n < 0) return pa::cuda_fail(cudaGetLastError(), "prefill_window: occupancy");
+            if (singles > n) break;
+            c *= 2;
+        }
         return launch_all<D, GQ>(kern, SLayout<D>::THREADS, SLayout<D>::SMEM, c, p, q, k_cache, v_cache,
                                  [&](const WinParams &) { return singles * c; }, stream);
     }
