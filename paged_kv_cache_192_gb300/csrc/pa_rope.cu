@@ -8,8 +8,12 @@
 // the position of one axis.  Values are stored as they are.
 //
 // Bound: memory (T * (2 Hq + 4 Hkv) rows) for long prompts, launch latency
-// for decode steps.  One CTA per token: the token's angles are computed once
-// (one thread per frequency) and used by all Hq + Hkv heads.  The product
+// for decode steps.  One CTA of 128 threads per token: the token's angles are
+// computed once (one thread per frequency) and used by all Hq + Hkv heads, while
+// the first rows are on their way.  Measured (bf16, d 128): 20,001 tokens of 64/8
+// heads 122 us, 0.99 of the copy rate (137 us with 256 threads per token);
+// 2,048 tokens of 32/8 heads 11.8 us (7.4 at that rate, the rest one launch and
+// one memory latency); 64 tokens 3.3 us.  The product
 // p * f and its reduction to a fraction of a turn are taken in fp64: at
 // positions of 2^20 an fp32 product is off by up to 0.06 rad.
 #include <cmath>
