@@ -111,8 +111,8 @@ int pa_reshape_and_cache(const void *k_new, const void *v_new, void *k_cache, vo
  * elements from rot_dim on are copied.  A token has one position per axis
  * (one axis for text; time, height and width for images and video); the first
  * sections[0] frequencies take axis 0's position, the next sections[1] axis
- * 1's, and so on.  Angles are reduced in fp64, so far positions lose nothing;
- * the rotation is fp32, rounded once.
+ * 1's, and so on.  Angles are taken and reduced in fp64 (off by at most 2^-51 of
+ * themselves: 1e-6 at position 2^31); the rotation is fp32, rounded once.
  *   q_out, q      [T][Hq][head_dim], k_new, v_new [T][Hkv][head_dim] (dtype);
  *                 heads of a token contiguous, q_out_stride .. v_stride elements
  *                 (a multiple of 16 bytes, at most 2^28) between tokens: slices

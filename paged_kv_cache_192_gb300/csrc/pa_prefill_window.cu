@@ -1002,7 +1002,7 @@ __global__ void __launch_bounds__(SLayout<D>::THREADS, 1)
 // Upper bound of the query tiles of qtok tokens: at most one per request is
 // partly filled.
 int64_t query_tiles(const WinParams &p, int max_query_len, int qtok) {
-    return std::min<int64_t>(int64_t(p.R) * ((max_query_len + qtok - 1) / qtok),
+    return std::min<int64_t>(int64_t(p.R) * ((int64_t(max_query_len) + qtok - 1) / qtok),
                              int64_t(p.T) / qtok + p.R);
 }
 

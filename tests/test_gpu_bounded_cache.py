@@ -202,3 +202,66 @@ def test_decode_step_captured_as_one_graph():
         assert not out[[1, 3]].any()
         lp.trim([0, 1, 2])
     assert ops.device_error() == 0
+
+
+FIRST_CALLS = """
+import sys, torch
+sys.path.insert(0, {root!r})
+from paged_kv_cache_192_gb300 import ops
+dev, bf16 = "cuda", torch.bfloat16
+g = torch.Generator().manual_seed(1)
+R = lambda *s: torch.randn(*s, generator=g).to(bf16).to(dev)
+k, v = R(64, 2, 16, 128), R(64, 2, 16, 128)
+table = torch.arange(60, dtype=torch.int32, device=dev).view(2, 30)
+lens = torch.tensor([470, 33], dtype=torch.int32, device=dev)
+start = torch.tensor([0, 40, 73], dtype=torch.int32, device=dev)
+q, qp = R(2, 8, 128), R(73, 8, 128)
+kn, vn = R(2, 2, 128), R(2, 2, 128)
+slots = torch.tensor([1000, 1001], device=dev)
+pos = torch.tensor([5, 6], device=dev)
+inv = torch.ones(64, device=dev)
+keep = torch.arange(0, 40, 2, dtype=torch.int32, device=dev).expand(2, 2, -1).contiguous()
+kl = torch.tensor([20, 10], dtype=torch.int32, device=dev)
+dst = torch.arange(60, 64, dtype=torch.int32, device=dev).view(2, 2)
+def calls():
+    a = ops.rope_reshape_and_cache(q, kn, vn, k, v, slots, pos, inv)
+    ops.compact_cache(k, v, table, dst, keep, kl)
+    return a, ops.decode_window(q, k, v, table, lens, 200, 4), ops.prefill_window(
+        qp, k, v, table, start, lens, 40, 200, 4)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(captured, calls()))
+assert ops.device_error() == 0
+# two threads, a stream each
+import threading
+bad = []
+def work():
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.default_stream())
+    with torch.cuda.stream(s):
+        for _ in range(50):
+            o = ops.decode_window(q, k, v, table, lens, 200, 4), ops.prefill_window(
+                qp, k, v, table, start, lens, 40, 200, 4)
+            s.synchronize()
+            if not (torch.equal(o[0], captured[1]) and torch.equal(o[1], captured[2])):
+                bad.append(1)
+threads = [threading.Thread(target=work) for _ in range(3)]
+for t in threads: t.start()
+for t in threads: t.join()
+assert not bad and ops.device_error() == 0
+print("ok")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """Nothing has to be called before a capture; and threads may call at once."""
+    import subprocess
+    import sys
+
+    from conftest import ROOT
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=ROOT)], capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr
