@@ -494,7 +494,8 @@ int pa_prefill_chunk(void *out, const void *q, const void *k_cache, const void *
  *   query_start   int32 [R+1] prefix sum of new-token counts, inside
  *                 [0, total_tokens]; a request may have no new tokens
  *   total_tokens  rows of q and out
- *   max_query_len host int >= every request's new tokens (sizes the grid)
+ *   max_query_len host int >= every request's new tokens (sizes the grid; with
+ *                 less, rows may be left out and PA_DEVERR_BAD_BLOCK recorded)
  *   window        at least 1; num_sinks at least 0 (both may exceed the context)
  *   block_table   entries of blocks that no new token of the request sees are
  *                 never read: their pages may have been freed (pa_bm_trim)
@@ -588,7 +589,8 @@ int pa_bm_free_seq(pa_bm *bm, int64_t seq);
  * block list and table become -1; *freed (may be NULL) receives how many the
  * sequence gave up (a shared block returns to the free list with its last
  * holder).  Calls that read the whole context (pa_decode and the like) no longer
- * work on the sequence. */
+ * work on the sequence.  The first queries of a chunk see farther back than the
+ * newest token: trim before a chunk is appended or after it has been computed. */
 int pa_bm_trim(pa_bm *bm, int64_t seq, int64_t window, int64_t num_sinks, int64_t *freed);
 
 /* Block lists for a compaction (pa_compact_cache) of n sequences to n_tokens[i]

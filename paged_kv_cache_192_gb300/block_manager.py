@@ -71,7 +71,8 @@ class BlockManager:
     def trim(self, seq: int, window: int, num_sinks: int = 0) -> int:
         """Free the blocks that a sliding window has left (pa_bm_trim): those
         whose tokens are all past the sinks and before len - window; their
-        table entries become -1.  -> how many the sequence gave up."""
+        table entries become -1.  Not between a chunk's append and its prefill:
+        its first queries see farther back.  -> how many the sequence gave up."""
         v = ctypes.c_int64()
         check(lib().pa_bm_trim(self._h, int(seq), int(window), int(num_sinks), ctypes.byref(v)))
         return v.value

@@ -490,10 +490,12 @@ int dispatch(int gq, const WindowParams &p, cudaStream_t s) {
 namespace pa {
 
 // Validate mode of the windowed calls: lengths in [0, capacity] and every
-// block with a token visible to the first query (or a later one) in the pool.
+// block with a token visible to the first query (or a later one) in the pool;
+// of a prefill also its rows inside [0, total_tokens), no request longer than
+// max_query_len.
 int validate_window(const int32_t *block_table, int MB, const int32_t *context_lens,
-                    const int32_t *query_start, int B, int bs, int64_t num_blocks, int window,
-                    int sinks, cudaStream_t stream) try {
+                    const int32_t *query_start, int total_tokens, int max_query_len, int B, int bs,
+                    int64_t num_blocks, int window, int sinks, cudaStream_t stream) try {
     std::vector<int32_t> lens(B), table(size_t(B) * MB), qs;
     if (int rc = fetch(lens.data(), context_lens, lens.size() * 4, stream)) return rc;
     if (int rc = fetch(table.data(), block_table, table.size() * 4, stream)) return rc;
@@ -506,9 +508,13 @@ int validate_window(const int32_t *block_table, int MB, const int32_t *context_l
         if (L < 0 || L > int64_t(MB) * bs)
             return fail(PA_ERR_INVALID, "validate: context_lens[%d]=%lld outside [0,%lld]", b,
                         (long long)L, (long long)MB * bs);
-        if (query_start && (n < 0 || n > L))
-            return fail(PA_ERR_INVALID, "validate: request %d has %lld new tokens of %lld", b,
-                        (long long)n, (long long)L);
+        if (query_start && (n < 0 || n > L || n > max_query_len))
+            return fail(PA_ERR_INVALID, "validate: request %d has %lld new tokens of %lld, "
+                                        "max_query_len %d", b, (long long)n, (long long)L,
+                        max_query_len);
+        if (query_start && n > 0 && (qs[b] < 0 || qs[b + 1] > total_tokens))
+            return fail(PA_ERR_INVALID, "validate: rows [%d,%d) of request %d outside [0,%d)", qs[b],
+                        qs[b + 1], b, total_tokens);
         if (L == 0 || n == 0) continue;
         const int64_t lo = std::max<int64_t>(0, L - n - window + 1);
         for (int64_t i = 0; i < (L + bs - 1) / bs; ++i) {
@@ -560,8 +566,8 @@ extern "C" int pa_decode_window(void *out, const void *q, const void *k_cache, c
         !pa::aligned16(v_cache))
         return pa::fail(PA_ERR_INVALID, "decode_window: q, out and pools must be 16-byte aligned");
     if (pa::validate_on())
-        if (int rc = pa::validate_window(block_table, max_blocks_per_seq, context_lens, nullptr, B,
-                                         block_size, num_blocks, window, num_sinks, stream))
+        if (int rc = pa::validate_window(block_table, max_blocks_per_seq, context_lens, nullptr, 0,
+                                         0, B, block_size, num_blocks, window, num_sinks, stream))
             return rc;
     WindowParams p{};
     p.out = out;

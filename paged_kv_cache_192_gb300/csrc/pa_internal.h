@@ -85,9 +85,10 @@ int validate_slots(const int64_t *slots, int64_t T, int64_t num_blocks, int bloc
                    cudaStream_t stream);
 
 // Validate mode of the windowed calls (pa_decode_window.cu); query_start is
-// NULL for a decode (one query per sequence).
+// NULL for a decode (one query per sequence), as are total_tokens and
+// max_query_len.
 int validate_window(const int32_t *block_table, int MB, const int32_t *context_lens,
-                    const int32_t *query_start, int B, int bs, int64_t num_blocks, int window,
-                    int sinks, cudaStream_t stream);
+                    const int32_t *query_start, int total_tokens, int max_query_len, int B, int bs,
+                    int64_t num_blocks, int window, int sinks, cudaStream_t stream);
 
 }  // namespace pa

@@ -1128,7 +1128,8 @@ extern "C" int pa_prefill_window(void *out, const void *q, const void *k_cache,
         return pa::fail(PA_ERR_INVALID, "prefill_window: q, out and pools must be 16-byte aligned");
     if (pa::validate_on())
         if (int rc = pa::validate_window(block_table, max_blocks_per_seq, context_lens, query_start,
-                                         R, block_size, num_blocks, window, num_sinks, stream))
+                                         total_tokens, max_query_len, R, block_size, num_blocks,
+                                         window, num_sinks, stream))
             return rc;
     WinParams p{};
     p.out = static_cast<__nv_bfloat16 *>(out);

@@ -223,3 +223,26 @@ def test_streams_graphs_and_back_to_back():
         e = call(c)
     torch.cuda.synchronize()
     assert torch.equal(o, ra) and torch.equal(e, rc) and ops.device_error() == 0
+
+
+def test_validate_mode_checks_rows_and_the_longest_request():
+    from paged_kv_cache_192_gb300 import ops
+    from paged_kv_cache_192_gb300._lib import PAError
+    bt = batch([90, 300], [30, 70], 50, 3)
+
+    def call_with(start, max_query_len):
+        return ops.prefill_window(bt.q_t, bt.k_cache, bt.v_cache, bt.table_t,
+                                  torch.tensor(start, dtype=torch.int32, device=DEV), bt.lens_t,
+                                  max_query_len, 50, 3)
+    ops.set_validate(True)
+    try:
+        bt.check(call_with([0, 30, 100], 70))
+        call_with([30, 30, 100], 70)  # a request without new tokens
+        with pytest.raises(PAError, match="max_query_len 69"):
+            call_with([0, 30, 100], 69)
+        for start in ([-1, 29, 99], [1, 31, 101]):
+            with pytest.raises(PAError, match="rows"):
+                call_with(start, 70)
+    finally:
+        ops.set_validate(False)
+    assert ops.device_error() == 0
