@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t o_col = wg * 128, s_col = 256 + wg * 128, p_col = s_col + 64;
         const int m = wg * 128 + row;
-        auto pv_done = [&](int g) { return pa::mbar_wait(&o_done[wg], g & 1); };
+        auto pv_done = [&](int g) { return wait_all(&o_done[wg], g & 1); };
         bool ok = true;
         int g = 0;
         Item I = item_of(min(static_cast<int>(blockIdx.x), nitems - 1)), next_item = I;
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(WLayout<D>::THREADS, 1)
             const int pos = I.P + min(I.t0 + m / GQ, I.n - 1);  // this row's own key
             float m_used = -INFINITY, lsum = 0.f;
             for (int j = 0; j < I.ntiles; ++j, ++g) {
-                ok = pa::mbar_wait(&s_full[wg], g & 1);
+                ok = wait_all(&s_full[wg], g & 1);
                 if (!ok) break;
                 pa::tc::fence_after();
                 const int j0 = I.base(j);
@@ -815,11 +815,11 @@ __global__ void __launch_bounds__(SLayout<D>::THREADS, 1)
         // ---------------- softmax warp groups ----------------
         const int pos = I.P + min(I.t0 + row / GQ, I.n - 1);  // this row's own key
         const uint32_t o_col = wg * 128, s_col = 256 + wg * 128, p_col = s_col + 64;
-        auto pv_done = [&](int l) { return pa::mbar_wait(&o_done[wg], l & 1); };
+        auto pv_done = [&](int l) { return wait_all(&o_done[wg], l & 1); };
         bool ok = true;
         int l = 0;
         for (int i = wg; i < nt; i += 2, ++l) {
-            ok = pa::mbar_wait(&s_full[wg], l & 1);
+            ok = wait_all(&s_full[wg], l & 1);
             if (!ok) break;
             pa::tc::fence_after();
             const int j0 = I.base(ta + i);
@@ -834,7 +834,7 @@ __global__ void __launch_bounds__(SLayout<D>::THREADS, 1)
                 rescale_o<D>(lane_base + o_col, alpha);
             }
             if (has_hidden_rows(I, p.sinks, j0)) {
-                ok = pa::mbar_wait(&v_full[i % NST], (i / NST) & 1);  // V has landed
+                ok = wait_all(&v_full[i % NST], (i / NST) & 1);  // V has landed
                 if (!ok) break;
                 zero_hidden_rows<D>(I, p.sinks, j0, sv + (i % NST) * Lay::T_BYTES, row);
             }
