@@ -2,11 +2,13 @@
 
 Each translation unit under csrc/ is compiled by nvcc in parallel, then the
 objects are linked into ``paged_kv_cache_192_gb300/libpa_gb300.so`` (static
-CUDA runtime, no torch dependency).  Beside it, ``binding/bounded_calls.cpp``
-(the torch-facing binding of the calls whose time on the host counts) becomes
-the extension module ``_bounded_calls.so``, linked to the library and to the
-installed torch.  Objects are cached in ``_build/`` keyed by a hash of the
-sources and flags, so an unchanged tree rebuilds in no time.
+CUDA runtime, no torch dependency).  Where torch is installed,
+``binding/bounded_calls.cpp`` (the torch-facing binding of the calls whose time
+on the host counts) then becomes the extension module ``_bounded_calls.so``,
+linked to the library and to that torch; it also needs g++ and the Python
+headers.  The library needs none of them and is linked first.  Objects are
+cached in ``_build/`` keyed by a hash of the sources and flags, so an unchanged
+tree rebuilds in no time.
 """
 from __future__ import annotations
 
@@ -50,12 +52,13 @@ def _digest(paths, extra) -> str:
 
 
 def _torch_flags():
-    """(compile flags, link flags) of an extension module of the running
-    Python against the installed torch (found without importing it)."""
+    """(compile flags, link flags, version) of an extension module of the
+    running Python against the installed torch (found without importing it);
+    None without one."""
     import importlib.util
     spec = importlib.util.find_spec("torch")
     if spec is None:
-        raise RuntimeError("torch not found")
+        return None
     root = os.path.dirname(spec.origin)
     with open(os.path.join(root, "version.py")) as f:
         version = f.read()
@@ -95,11 +98,12 @@ def _compile(src: str, obj: str, headers) -> str:
     return obj
 
 
-def _link(out: str, cmd, objs, libs, stamp_name: str):
+def _link(out: str, cmd, objs, libs, stamp_name: str) -> bool:
+    """Links out unless it is there already; whether it was linked."""
     key = _digest(objs, cmd + libs)
     stamp = os.path.join(BUILD, stamp_name)
     if os.path.exists(out) and os.path.exists(stamp) and open(stamp).read() == key:
-        return
+        return False
     tmp = out + ".tmp"
     r = subprocess.run(cmd + ["-o", tmp] + objs + libs, capture_output=True, text=True)
     if r.returncode != 0:
@@ -107,16 +111,19 @@ def _link(out: str, cmd, objs, libs, stamp_name: str):
     os.replace(tmp, out)
     with open(stamp, "w") as f:
         f.write(key)
+    return True
 
 
 def build(verbose: bool = False) -> str:
-    """Compile and link the library; returns its path."""
+    """Compile and link the library, and the binding where torch is installed;
+    returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
     headers = sorted(glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
                      glob.glob(os.path.join(INCLUDE, "*.h")))
     hdr_digest = _digest(headers, NVCC_FLAGS)
-    objs = []
+    objs, binding_obj = [], None
+    torch_flags = _torch_flags()
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         futs = []
         for src in sources:
@@ -124,21 +131,27 @@ def build(verbose: bool = False) -> str:
             obj = os.path.join(BUILD, f"{os.path.basename(src)}.{key}.o")
             objs.append(obj)
             futs.append(ex.submit(_compile, src, obj, headers))
-        comp, link, torch_version = _torch_flags()
-        key = _digest([BINDING_SRC] + headers, comp + [torch_version])
-        binding_obj = os.path.join(BUILD, f"bounded_calls.cpp.{key}.o")
-        futs.append(ex.submit(_compile_binding, BINDING_SRC, binding_obj, comp))
+        if torch_flags:
+            comp, link, torch_version = torch_flags
+            key = _digest([BINDING_SRC] + headers, comp + [torch_version])
+            binding_obj = os.path.join(BUILD, f"bounded_calls.cpp.{key}.o")
+            binding_done = ex.submit(_compile_binding, BINDING_SRC, binding_obj, comp)
         for f in futs:
             f.result()
     # objects of earlier sources or flags are not reused: drop them
-    keep = {os.path.basename(o) for o in objs + [binding_obj]}
+    keep = {os.path.basename(o) for o in objs + ([binding_obj] if binding_obj else [])}
     for old in glob.glob(os.path.join(BUILD, "*.o")):
         if os.path.basename(old) not in keep:
             os.remove(old)
-    _link(LIB, [nvcc()] + ARCH + ["-shared"], objs, ["-lpthread"], "lib.stamp")
-    # (the library is found beside the module; its name is what the loader sees)
-    _link(BINDING, [shutil.which("g++") or "c++", "-shared"], [binding_obj],
-          ["-L", PKG, "-l:" + os.path.basename(LIB)] + link, "binding.stamp")
+    if _link(LIB, [nvcc()] + ARCH + ["-shared"], objs, ["-lpthread"], "lib.stamp"):
+        # a binding of an earlier library does not outlive it
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+    if binding_obj:
+        binding_done.result()
+        # (the library is found beside the module; its name is what the loader sees)
+        _link(BINDING, [shutil.which("g++") or "c++", "-shared"], [binding_obj],
+              ["-L", PKG, "-l:" + os.path.basename(LIB)] + link, "binding.stamp")
     if verbose:
         print("built", LIB)
     return LIB

@@ -9,6 +9,7 @@ allocates).
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 
 import torch
@@ -62,9 +63,14 @@ def _calls():
     global _bounded
     if _bounded is None:
         lib()  # the library, or its error if it has not been built
-        from . import _bounded_calls
-        _bounded_calls.set_check(check)
-        _bounded = _bounded_calls
+        try:
+            module = importlib.import_module("._bounded_calls", __package__)
+        except ModuleNotFoundError as e:
+            raise RuntimeError(
+                "the binding _bounded_calls.so is missing: build it with "
+                "paged_kv_cache_192_gb300.build.build() where torch is installed") from e
+        module.set_check(check)
+        _bounded = module
     return _bounded
 
 
