@@ -187,6 +187,10 @@ int pa_swap_blocks(void *dst_k, void *dst_v, const void *src_k, const void *src_
  * range is skipped and recorded (PA_DEVERR_BAD_BLOCK); positions that are not
  * ascending, or pages read and written other than in place, give undefined
  * rows.  Rows behind the last kept token keep their old bytes.
+ * A row's index is no longer its token's position.  Keys stay rotated by the
+ * position that their token had, so the next token's rotary position is still
+ * the number of tokens the sequence has had, not its length (the caller counts
+ * it); windows and sinks count rows.
  */
 int pa_compact_cache(void *k_cache, void *v_cache, const int32_t *src_table,
                      int src_blocks_per_seq, const int32_t *dst_table, int dst_blocks_per_seq,
@@ -598,8 +602,10 @@ int pa_bm_trim(pa_bm *bm, int64_t seq, int64_t window, int64_t num_sinks, int64_
  * stays at its logical place, a shared one, or the place of one that pa_bm_trim
  * gave up, gets a fresh block, and the blocks past the kept tokens are dropped.  Take the sequences'
  * block tables before (src_table) and after (dst_table), and launch the
- * compaction before anything else writes into blocks given out later.  All or
- * nothing; PA_ERR_OOM when there are too few free blocks. */
+ * compaction before anything else writes into blocks given out later.
+ * pa_bm_seq_len counts the kept rows from here on: it is not the next token's
+ * rotary position.  All or nothing; PA_ERR_OOM when there are too few free
+ * blocks. */
 int pa_bm_compact(pa_bm *bm, const int64_t *seqs, int n, const int64_t *n_tokens);
 
 /* Host int32 out[n][max_blocks]: the block table rows of seqs[0..n), padded

@@ -80,7 +80,8 @@ class BlockManager:
     def compact(self, seqs, n_tokens):
         """Block lists for ops.compact_cache of seqs to n_tokens tokens each
         (pa_bm_compact).  Take block_table(seqs) before (src_table) and after
-        (dst_table) the call."""
+        (dst_table) the call.  seq_len is the number of kept rows then, not
+        the next token's rotary position."""
         seqs = np.ascontiguousarray(seqs, dtype=np.int64)
         n_tokens = np.ascontiguousarray(n_tokens, dtype=np.int64)
         if seqs.ndim != 1 or n_tokens.shape != seqs.shape:

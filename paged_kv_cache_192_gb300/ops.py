@@ -179,7 +179,11 @@ def compact_cache(k_cache, v_cache, src_table, dst_table, keep, keep_lens, strea
     same page at the same logical block is compacted in place; other pages
     written must not be read by the call).  keep: int32 [B][Hkv][max_keep],
     for each KV head the kept positions in ascending order; keep_lens: int32
-    [B], how many of them count.  The pools are written in place, bit exact."""
+    [B], how many of them count.  The pools are written in place, bit exact.
+
+    Positions do not shrink with the rows: the next token of a sequence is
+    rotated by the number of tokens it has had, not by its new length.  Windows
+    and sinks of later calls count rows."""
     _calls().compact_cache(k_cache, v_cache, src_table, dst_table, keep, keep_lens, stream)
 
 

@@ -265,3 +265,73 @@ def test_first_calls_of_a_process_may_be_captured():
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=ROOT)], capture_output=True,
                        text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr
+
+
+def test_positions_go_on_behind_a_compaction():
+    """A compaction shortens a sequence's rows, not its positions: the next
+    tokens are rotated by how many tokens the sequence has had, which the caller
+    counts, and the plain call then equals attention over the kept tokens at
+    their own positions.  (seq_len, the row count, as the position does not.)
+
+    fp32.  Bound: the library's 1e-5 + 1e-5 |o|, and the rotations': an element
+    is off by at most 6 steps of 2^-24 of its pair (two products, a sum, sine and
+    cosine to 2^-22), a score by 2 * 6 * 2^-24 * sum |q| |k| * scale < 2.3e-5
+    (sum below 256 here), twice that relative in a weight with its sum, times
+    max |v| (below 6): 2.8e-4."""
+    from paged_kv_cache_192_gb300 import ops
+    lp = Loop(num_blocks=64, dtype=torch.float32)
+    lens, n, more = {0: 90, 1: 61}, {0: 40, 1: 17}, 3
+    raw = {s: [] for s in lens}  # (k, v) of each token before its rotation
+
+    def put(s, count, first):
+        sl, _ = lp.bm.append_n(s, count)
+        q, k, v = lp.rand(count, lp.Hq, lp.d), lp.rand(count, lp.Hkv, lp.d), lp.rand(count, lp.Hkv, lp.d)
+        raw[s] += list(zip(k.double().cpu(), v.double().cpu()))
+        pos = torch.arange(first, first + count, device=DEV)
+        r = ops.rope_reshape_and_cache(q, k, v, lp.k, lp.v, torch.from_numpy(sl).to(DEV), pos, lp.inv)
+        return q.double().cpu(), r
+
+    def turned(x, p):
+        a = p * lp.inv.double().cpu()
+        x0, x1 = x[..., :lp.d // 2], x[..., lp.d // 2:]
+        return torch.cat([x0 * a.cos() - x1 * a.sin(), x0 * a.sin() + x1 * a.cos()], -1)
+
+    for s, L in lens.items():
+        lp.bm.add_seq(s, 0)
+        put(s, L, 0)
+    seqs, rng = list(lens), np.random.default_rng(3)
+    keep = np.zeros((2, lp.Hkv, max(n.values())), dtype=np.int32)
+    for s in seqs:
+        for h in range(lp.Hkv):
+            keep[s, h, :n[s]] = np.sort(rng.permutation(lens[s])[:n[s]])
+    src, _ = lp.tables(seqs)
+    lp.bm.compact(seqs, [n[s] for s in seqs])
+    dst, rows = lp.tables(seqs)
+    assert rows.tolist() == [40, 17]
+    ops.compact_cache(lp.k, lp.v, src, dst, torch.from_numpy(keep).to(DEV), rows)
+
+    def formula(s, q, p, shift):
+        """The query at position p over the kept tokens and the new ones up to
+        itself; shift: how far the new tokens' positions are off."""
+        out = torch.zeros(lp.Hq, lp.d, dtype=torch.float64)
+        for h in range(lp.Hkv):
+            at = [int(j) for j in keep[s, h, :n[s]]] + list(range(lens[s], p + 1))
+            k = torch.stack([turned(raw[s][j][0][h], j - (shift if j >= lens[s] else 0)) for j in at])
+            v = torch.stack([raw[s][j][1][h] for j in at])
+            for x in range(h * lp.Hq // lp.Hkv, (h + 1) * lp.Hq // lp.Hkv):
+                out[x] = torch.softmax(k @ turned(q[x], p - shift) * lp.d ** -0.5, 0) @ v
+        return out
+
+    for step in range(more):
+        for s in seqs:
+            p = lens[s] + step
+            q, r = put(s, 1, p)
+            table, L = lp.tables([s])
+            assert int(L) == n[s] + step + 1
+            got = ops.decode(r, lp.k, lp.v, table, L)[0].double().cpu()
+            windowed = ops.decode_window(r, lp.k, lp.v, table, L, int(L))[0].double().cpu()
+            ref = formula(s, q[0], p, 0)
+            tol = 1e-5 + 1e-5 * ref.abs() + 2.8e-4
+            assert bool(((got - ref).abs() <= tol).all()) and bool(((windowed - ref).abs() <= tol).all())
+            assert float((formula(s, q[0], p, lens[s] - n[s]) - ref).abs().max()) > 0.01
+    assert ops.device_error() == 0
