@@ -520,6 +520,24 @@ int pa_prefill_window(void *out, const void *q, const void *k_cache, const void 
                       int block_size, int64_t num_blocks, float scale, int window, int num_sinks,
                       int dtype, pa_stream_t stream);
 
+/* kernels pa_prefill_window can launch (pa_prefill_window_kernel_for) */
+enum { PA_PREFILL_WINDOW_PERSISTENT = 1, PA_PREFILL_WINDOW_SPLIT = 2 };
+
+/*
+ * pa_prefill_window_kernel_for -- which kernel pa_prefill_window launches for
+ * these sizes on the current device (sizes only, never device data):
+ *   PA_PREFILL_WINDOW_SPLIT       a cluster of CTAs per (128 query rows, KV
+ *                                 head), when there are at most as many of
+ *                                 these as SMs and at most 256 requests;
+ *   PA_PREFILL_WINDOW_PERSISTENT  one CTA per SM running a list of (request,
+ *                                 256 query rows, KV head) items.
+ * Both meet the same error bound.  Arguments as for pa_prefill_window;
+ * PA_ERR_INVALID / PA_ERR_UNSUPPORTED on bad sizes, PA_ERR_CUDA without a
+ * current device.
+ */
+int pa_prefill_window_kernel_for(int R, int total_tokens, int max_query_len, int Hq, int Hkv,
+                                 int *kernel);
+
 /* kernels pa_prefill_chunk can launch (pa_prefill_kernel_for) */
 enum { PA_PREFILL_PERSISTENT_GRID = 1, PA_PREFILL_ITEM_GRID = 2, PA_PREFILL_SIMPLE = 3 };
 

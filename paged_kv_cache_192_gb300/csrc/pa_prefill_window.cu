@@ -1001,9 +1001,25 @@ __global__ void __launch_bounds__(SLayout<D>::THREADS, 1)
 
 // Upper bound of the query tiles of qtok tokens: at most one per request is
 // partly filled.
-int64_t query_tiles(const WinParams &p, int max_query_len, int qtok) {
-    return std::min<int64_t>(int64_t(p.R) * ((int64_t(max_query_len) + qtok - 1) / qtok),
-                             int64_t(p.T) / qtok + p.R);
+int64_t query_tiles(int R, int T, int max_query_len, int qtok) {
+    return std::min<int64_t>(int64_t(R) * ((int64_t(max_query_len) + qtok - 1) / qtok),
+                             int64_t(T) / qtok + R);
+}
+
+// Whether a call runs on the split kernel: its (query tile of 128 rows, KV
+// head) pairs, returned in *singles, fit one per SM.
+bool runs_split(int R, int T, int max_query_len, int gq, int Hkv, int sms, int64_t *singles) {
+    *singles = query_tiles(R, T, max_query_len, 128 / gq) * Hkv;
+    return R <= kMaxR && *singles <= sms;
+}
+
+// SMs of the current device; 0: a CUDA call failed.
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return sms;
 }
 
 // Launches kernel `kern` for groups of at most kMaxR requests, its tables' size;
@@ -1046,12 +1062,10 @@ int launch_all(K kern, int threads, size_t smem, int cluster, const WinParams &p
 template <int D, int GQ>
 int launch(const WinParams &p, const void *q, const void *k_cache, const void *v_cache,
            int max_query_len, cudaStream_t stream) {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return pa::cuda_fail(cudaGetLastError(), "prefill_window: SM count");
-    const int64_t singles = query_tiles(p, max_query_len, 128 / GQ) * p.Hkv;
-    if (p.R <= kMaxR && singles <= sms) {
+    const int sms = sm_count();
+    if (sms <= 0) return pa::cuda_fail(cudaGetLastError(), "prefill_window: SM count");
+    int64_t singles = 0;
+    if (runs_split(p.R, p.T, max_query_len, GQ, p.Hkv, sms, &singles)) {
         auto kern = prefill_window_split_kernel<D, GQ>;
         static std::atomic<uint64_t> done{0};
         if (int rc = set_smem_once(kern, SLayout<D>::SMEM, &done)) return rc;
@@ -1080,7 +1094,7 @@ int launch(const WinParams &p, const void *q, const void *k_cache, const void *v
         kern, WLayout<D>::THREADS, WLayout<D>::SMEM, 0, p, q, k_cache, v_cache,
         [&](const WinParams &pp) {
             return std::max<int64_t>(
-                1, std::min<int64_t>(sms, query_tiles(pp, max_query_len, 256 / GQ) * pp.Hkv));
+                1, std::min<int64_t>(sms, query_tiles(pp.R, pp.T, max_query_len, 256 / GQ) * pp.Hkv));
         },
         stream);
 }
@@ -1160,4 +1174,22 @@ extern "C" int pa_prefill_window(void *out, const void *q, const void *k_cache,
     };
     return head_dim == 128 ? pick(std::integral_constant<int, 128>{})
                            : pick(std::integral_constant<int, 64>{});
+}
+
+extern "C" int pa_prefill_window_kernel_for(int R, int total_tokens, int max_query_len, int Hq, int Hkv,
+                                            int *kernel) {
+    pa::clear_error();
+    if (!kernel) return pa::fail(PA_ERR_INVALID, "prefill_window_kernel_for: kernel is NULL");
+    if (R < 0 || total_tokens < 0 || max_query_len < 0 || Hq <= 0 || Hkv <= 0 || Hkv > 1024 || Hq % Hkv)
+        return pa::fail(PA_ERR_INVALID, "prefill_window_kernel_for: bad sizes");
+    const int gq = Hq / Hkv;
+    if (gq != 1 && gq != 2 && gq != 4 && gq != 8)
+        return pa::fail(PA_ERR_UNSUPPORTED, "prefill_window_kernel_for: Hq/Hkv=%d unsupported", gq);
+    const int sms = sm_count();
+    if (sms <= 0) return pa::cuda_fail(cudaGetLastError(), "prefill_window_kernel_for: SM count");
+    int64_t singles = 0;
+    *kernel = runs_split(R, total_tokens, max_query_len, gq, Hkv, sms, &singles)
+                  ? PA_PREFILL_WINDOW_SPLIT
+                  : PA_PREFILL_WINDOW_PERSISTENT;
+    return PA_OK;
 }

@@ -215,6 +215,17 @@ def prefill_kernel_for(R, max_query_len, Hq, Hkv, head_dim, block_size, num_bloc
             _lib.PA_PREFILL_SIMPLE: "simple"}[out.value]
 
 
+def prefill_window_kernel_for(R, total_tokens, max_query_len, Hq, Hkv) -> str:
+    """Kernel pa_prefill_window runs for these sizes on the current device:
+    "split" (a cluster per 128 query rows and KV head; few of them) or
+    "persistent" (one CTA per SM running a list of work items)."""
+    out = ctypes.c_int(0)
+    check(lib().pa_prefill_window_kernel_for(R, total_tokens, max_query_len, Hq, Hkv,
+                                             ctypes.byref(out)))
+    return {_lib.PA_PREFILL_WINDOW_PERSISTENT: "persistent",
+            _lib.PA_PREFILL_WINDOW_SPLIT: "split"}[out.value]
+
+
 def decode_tile_for(Hq, Hkv, head_dim, block_size, num_blocks, dtype=torch.bfloat16) -> str:
     """Tile the persistent decode kernel uses for these shapes: "tensor_core"
     (bf16, groups of 4 or 8 heads) or "cuda_core"."""

@@ -252,3 +252,22 @@ def test_things_that_are_no_tensors():
         ops.rope_reshape_and_cache(**{**rope_args(), "sections": 64})
     with pytest.raises(ValueError, match="1 to 4 axes"):
         ops.rope_reshape_and_cache(**{**rope_args(), "sections": (1, 1, 1, 1, 60)})
+
+
+@pytest.mark.parametrize("args,code", [
+    ((-1, 10, 5, 4, 4), 1), ((2, -1, 5, 4, 4), 1), ((2, 10, -1, 4, 4), 1), ((2, 10, 5, 0, 4), 1),
+    ((2, 10, 5, 4, 0), 1), ((2, 10, 5, 6, 4), 1), ((2, 10, 5, 2048, 2048), 1), ((2, 10, 5, 64, 4), 4),
+])
+def test_prefill_window_kernel_for_refusals(lib, args, code):
+    out = ctypes.c_int(-1)
+    assert lib.pa_prefill_window_kernel_for(*args, ctypes.byref(out)) == code
+    assert out.value == -1 and lib.pa_last_error_string()
+    assert lib.pa_prefill_window_kernel_for(2, 10, 5, 4, 4, None) == 1
+
+
+def test_prefill_window_kernel_for_needs_a_device(lib):
+    if torch.cuda.is_available():
+        pytest.skip("a CUDA device is present")
+    out = ctypes.c_int(-1)
+    assert lib.pa_prefill_window_kernel_for(2, 10, 5, 4, 4, ctypes.byref(out)) == 3
+    assert out.value == -1 and lib.pa_last_error_string()

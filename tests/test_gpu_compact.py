@@ -195,3 +195,27 @@ def test_validate_mode(plant, msg):
             run(c)
     finally:
         ops.set_validate(False)
+
+
+@pytest.mark.parametrize("mode", ["in_place", "fresh", "mixed"])
+@pytest.mark.parametrize("d,bs,dtype", [(64, 16, bf16), (128, 16, bf16), (128, 8, f32), (256, 32, bf16)])
+def test_several_batches_of_looked_up_rows(mode, d, bs, dtype):
+    """Too many lists for clusters: one CTA per list, rows looked up 512 at a
+    time; lists around and past one such batch.  Rows of 8 lanes (d 64) make a
+    batch exactly as many chunks as there are stages."""
+    B, Hkv = 40, 2
+    assert B * Hkv * 8 >= 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    n = ([511, 512, 513, 1023, 1025, 2500, 1537, 3, 0, 2048] * 4)[:B]
+    lens = [3000 if x > 1000 else 1400 + x for x in n]
+    c = Case(lens, n, Hkv, d, bs, dtype, mode, seed=d + bs)
+    run(c)
+    c.check()
+
+
+@pytest.mark.parametrize("mode", ["in_place", "mixed"])
+@pytest.mark.parametrize("d,dtype", [(64, bf16), (128, f32)])
+def test_several_batches_of_a_cluster(mode, d, dtype):
+    """Few lists: a cluster's batch is 512 rows of each of its CTAs."""
+    c = Case([20000], [17001], 2, d, 16, dtype, mode, seed=d)
+    run(c)
+    c.check()
