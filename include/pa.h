@@ -506,8 +506,9 @@ int pa_prefill_chunk(void *out, const void *q, const void *k_cache, const void *
  * Any block size and table length that pa_decode_window takes.  K and V of
  * tokens that no new token of a request sees (slots never written, tokens
  * before the first query's window) do not enter its rows, whatever they hold;
- * a NaN or infinity in a token that one of them sees may also reach the rows
- * of the same request that do not.
+ * a NaN or infinity in V of a token that one of them sees may also reach the
+ * rows of the same request and KV head that do not (their weight is 0, and
+ * 0 x NaN is NaN).
  * Other arguments and the error bound as for pa_prefill_chunk.  A request whose
  * lengths do not fit (context outside [new tokens, capacity], rows outside
  * [0, total_tokens]) is left out and PA_DEVERR_BAD_BLOCK recorded.  One launch

@@ -20,7 +20,7 @@
 // in the CTA barrier's place) when there are few.
 //
 // Measured (bf16, d 128, 8 KV heads): 64 sequences keeping about 4,000 tokens,
-// 2.1 GB read and written, 0.95 of the copy rate; before the ring, with rows
+// 2.1 GB read and written, 330 us, 0.94 of the copy rate; before the ring, with rows
 // held in registers and looked up per piece, 0.67 to 0.77.
 #include <atomic>
 #include <new>

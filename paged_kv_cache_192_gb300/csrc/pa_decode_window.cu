@@ -17,9 +17,10 @@
 // every 1/C of the item's output to the CTA that finishes it (distributed
 // shared memory, one cluster barrier).
 //
-// Measured (bf16, d 128): 64 sequences of 128 to 32,768 tokens, window 4096, 32/8
-// heads: 148 us, 6.8 TB/s (the rate of a copy); one sequence of window 1024:
-// 6.0 us, a chain of latencies (launch, length, table, tile, two exchanges).
+// Measured (bf16, d 128; GPU times, calls replayed from a graph): 64 sequences of
+// 128 to 32,768 tokens, window 4096, 32/8 heads: 149 us, 6.8 TB/s (the rate of a
+// copy); one sequence of window 1024: 6.2 us (6.4 through the Python call), a
+// chain of latencies (launch, length, table, tile, two exchanges).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -53,8 +54,10 @@ struct TileOf {  // CUDA-core tile
     using type = WarpAttn<T, D, GQ>;
     static constexpr bool MMA = false;
     static constexpr int STAGE = Cfg<T, D, GQ>::STAGE;
-    // one stage where two take 64 KB or more: several CTAs per SM instead (24
-    // sequences, window 501, d 64: 7.3 us against 8.7)
+    // one stage where two take more than 64 KB per CTA: several CTAs per SM
+    // instead (24 sequences, window 501, d 64, groups of 1: 7.2 us on the GPU
+    // against 8.7).  Stages of 8 KB keep two (64 sequences, window 4096, d 64,
+    // groups of 4: 160 us against 194 with one)
     static constexpr int NST = STAGE <= 8192 ? 2 : 1;
     static constexpr int PBUF = 2 * Cfg<T, D, GQ>::TT * GQ * 4;  // p and score buffers, per warp
     static constexpr int MINB = 1;
@@ -439,8 +442,9 @@ int launch(const WindowParams &p, cudaStream_t stream) {
     const int slots = prepare_kernel<T, D, GQ, false>(), sms = sm_count();
     if (slots <= 0 || sms <= 0)
         return pa::cuda_fail(cudaGetLastError(), "decode_window: kernel attributes");
-    // Cluster size: the largest that leaves every warp two tiles and all
-    // clusters running at once.  A second wave of clusters costs more than the
+    // Cluster size: the largest that leaves every warp two tiles (also of the
+    // types with one stage, whose warps then wait for each) and all clusters
+    // running at once.  A second wave of clusters costs more than the
     // split gains: window 4096, 8 KV heads, 4 sequences: 16.0 us with clusters of
     // 8, 30.4 with 16; 16 sequences of window 1024: 15.9 us with clusters of 2,
     // 21.4 with 4.  One sequence: window 8192 12.1 us with clusters of 16, 18.5

@@ -31,12 +31,14 @@
 // memory by log-sum-exp.
 //
 // Measured (32/8 heads, d 128): a prompt of 16,384 tokens with window 4096 and 64
-// sinks 888 us, 1,100 TFLOP/s (0.65 of cuBLAS's sustained bf16).  A 64-key tile
+// sinks 868 to 901 us, 1,080 to 1,120 TFLOP/s (0.64 to 0.66 of cuBLAS's sustained
+// bf16).  A 64-key tile
 // of both groups takes 1,870 cycles, of which the tensor core needs 1,790: PV
 // twice 512 for the two terms of P, and S twice 384 instead of 256, as it reads
 // 192 bytes of shared memory per cycle of its own (128-row A and 64-row B against
 // 64 columns).  4 chunks of 512 tokens over up to 3,584 earlier ones, window
-// 1024: 47 us, 256 items on 152 SMs.  One chunk of 40 tokens, window 513: 9.9 us.
+// 1024: 47 us: 256 items of 1 to 19 tiles on 152 SMs, 37 tiles on the fullest, 25 on
+// average.  One chunk of 40 tokens, window 513: 9.9 us.
 #include <cuda.h>
 
 #include <algorithm>

@@ -10,10 +10,13 @@
 // Bound: memory (T * (2 Hq + 4 Hkv) rows) for long prompts, launch latency
 // for decode steps.  One CTA of 128 threads per token: the token's angles are
 // computed once (one thread per frequency) and used by all Hq + Hkv heads, while
-// the first rows are on their way.  Measured (bf16, d 128): 20,001 tokens of 64/8
-// heads 122 us, 0.99 of the copy rate (137 us with 256 threads per token);
-// 2,048 tokens of 32/8 heads 11.8 us (7.4 at that rate, the rest one launch and
-// one memory latency); 64 tokens 3.3 us.  The product
+// the first rows are on their way.  Measured (bf16, d 128; GPU times, calls replayed
+// from a graph, a Python call takes 4 us or more): 20,001 tokens of 64/8 heads
+// 122 us, 0.99 of the copy rate (137 us with 256 threads per token); 64 tokens of
+// 32/8 heads 3.3 us; 2,048 tokens 11.8 us against 7.4 at that rate.  12 CTAs of 40
+// registers fit an SM, 1,824 at once: 1,824 tokens take 9.5 us, 1,900 11.2, as the
+// rest is a second wave with the latency of the first.  fp32: 2,048 tokens 17.9 us
+// (0.83), 8,192 61.5 (0.97).  The product
 // p * f and its reduction to a fraction of a turn are taken in fp64: at
 // positions of 2^20 an fp32 product is off by up to 0.06 rad.
 #include <cmath>
