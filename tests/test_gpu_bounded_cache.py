@@ -335,3 +335,106 @@ def test_positions_go_on_behind_a_compaction():
             assert bool(((got - ref).abs() <= tol).all()) and bool(((windowed - ref).abs() <= tol).all())
             assert float((formula(s, q[0], p, lens[s] - n[s]) - ref).abs().max()) > 0.01
     assert ops.device_error() == 0
+
+
+def test_captured_branches_that_join():
+    """A graph whose two branches (streams) run the calls side by side, fork
+    from a call and join into one: every node has more than one neighbour."""
+    from paged_kv_cache_192_gb300 import ops
+    lp = Loop(num_blocks=64)
+    for s in (0, 1):
+        lp.bm.add_seq(s, 0)
+    lp.store({0: 150, 1: 77})
+    table, lens = lp.tables([0, 1])
+    q, kn, vn = lp.rand(2, lp.Hq, lp.d), lp.rand(2, lp.Hkv, lp.d), lp.rand(2, lp.Hkv, lp.d)
+    qp = lp.rand(40, lp.Hq, lp.d)
+    start = torch.tensor([0, 30, 40], dtype=torch.int32, device=DEV)
+    unused = [b for b in range(64) if b not in lp.bm.seq_blocks(0) + lp.bm.seq_blocks(1)]
+    slots = torch.tensor([0, 1], dtype=torch.int64, device=DEV) + unused[4] * lp.bs
+    pos = torch.tensor([150, 77], dtype=torch.int64, device=DEV)
+    free = unused[:4]
+    dst = torch.tensor(free, dtype=torch.int32, device=DEV).view(2, 2)
+    keep = torch.arange(0, 32, 2, dtype=torch.int32, device=DEV).expand(2, lp.Hkv, -1).contiguous()
+    n = torch.tensor([16, 9], dtype=torch.int32, device=DEV)
+
+    def branches(side):
+        main = torch.cuda.current_stream()
+        r = ops.rope_reshape_and_cache(q, kn, vn, lp.k, lp.v, slots, pos, lp.inv)
+        side.wait_stream(main)
+        a = ops.decode_window(r, lp.k, lp.v, table, lens, lp.W, lp.S)
+        with torch.cuda.stream(side):
+            b = ops.prefill_window(qp, lp.k, lp.v, table, start, lens, 30, lp.W, lp.S)
+            ops.compact_cache(lp.k, lp.v, table, dst, keep, n)
+        main.wait_stream(side)
+        return r, a, b, ops.decode_window(r, lp.k, lp.v, dst, n, lp.W, lp.S)
+
+    side = torch.cuda.Stream()
+    eager = branches(side)
+    torch.cuda.synchronize()
+    for b in free:
+        lp.k[b], lp.v[b] = 0, 0
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured = branches(side)
+    for _ in range(3):
+        for o in captured:
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(captured, eager))
+    assert ops.device_error() == 0
+
+
+@pytest.mark.parametrize("R", [3, 300])
+def test_requests_without_new_tokens_leave_the_output(R):
+    from paged_kv_cache_192_gb300 import ops
+    lp = Loop(num_blocks=8)
+    out = torch.full((10, lp.Hq, lp.d), 3.0, dtype=bf16, device=DEV)
+    table = torch.full((R, 2), -1, dtype=torch.int32, device=DEV)
+    zero = torch.zeros(R + 1, dtype=torch.int32, device=DEV)
+    assert ops.prefill_window_kernel_for(R, 10, 16, lp.Hq, lp.Hkv) == ("split" if R == 3 else "persistent")
+    ops.prefill_window(torch.zeros_like(out), lp.k, lp.v, table, zero, zero[:R] + 7, 16, lp.W, lp.S, out=out)
+    torch.cuda.synchronize()
+    assert (out == 3.0).all() and ops.device_error() == 0
+
+
+def test_stores_and_compactions_from_several_threads():
+    """Each thread its stream, pools and tokens; the same bits as alone."""
+    import threading
+
+    from paged_kv_cache_192_gb300 import ops
+    g = torch.Generator().manual_seed(2)
+    R = lambda *s: torch.randn(*s, generator=g).to(bf16).to(DEV)  # noqa: E731
+    q, kn, vn = R(200, 8, 128), R(200, 2, 128), R(200, 2, 128)
+    inv = torch.rand(64, generator=g).to(DEV)
+    slots = torch.randperm(256, generator=g)[:200].to(DEV)
+    pos = torch.arange(200, device=DEV)
+    table = torch.arange(16, dtype=torch.int32, device=DEV).view(1, 16)
+    keep = torch.arange(1, 256, 3, dtype=torch.int32, device=DEV).expand(1, 2, -1).contiguous()
+    n = torch.tensor([keep.shape[2]], dtype=torch.int32, device=DEV)
+    base = R(16, 2, 16, 128)
+
+    def work():
+        k, v = base.clone(), base.clone()
+        r = ops.rope_reshape_and_cache(q, kn, vn, k, v, slots, pos, inv)
+        ops.compact_cache(k, v, table, table, keep, n)
+        return r, k, v
+    want = work()
+    torch.cuda.synchronize()
+    bad = []
+
+    def run():
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.default_stream())
+        with torch.cuda.stream(s):
+            for _ in range(40):
+                got = work()
+                s.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                    bad.append(1)
+    threads = [threading.Thread(target=run) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and ops.device_error() == 0
