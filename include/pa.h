@@ -58,7 +58,10 @@ enum { PA_BF16 = 0, PA_F32 = 1 };
 /* device error word bits (pa_device_error) */
 enum {
     PA_DEVERR_BAD_BLOCK = 1, /* a block-table entry was outside [0, num_blocks) */
-    PA_DEVERR_TIMEOUT = 2    /* a bounded pipeline wait ran out; output invalid */
+    PA_DEVERR_TIMEOUT = 2,   /* a bounded pipeline wait ran out; output invalid */
+    PA_DEVERR_BAD_REQUEST = 4, /* ids, lengths or rows of a request that do not fit (pa_plan_step,
+                                  pa_cross_attention, pa_linear_*) */
+    PA_DEVERR_NO_BLOCKS = 8  /* pa_plan_step: the step needs more pages, or a wider table, than there are */
 };
 
 /* Message of the last failing call on this thread ("" if none). */
@@ -564,6 +567,87 @@ enum { PA_PREFILL_PERSISTENT_GRID = 1, PA_PREFILL_ITEM_GRID = 2, PA_PREFILL_SIMP
 int pa_prefill_kernel_for(int R, int max_query_len, int Hq, int Hkv, int head_dim,
                           int block_size, int64_t num_blocks, int max_blocks_per_seq,
                           int *kernel);
+
+/*
+ * pa_plan_step -- a step's block tables, slots and positions from its requests'
+ * lengths, on the device: a captured step (plan, rotary store, attention) needs
+ * no host work between two replays.
+ * The sequences and their pages live on the device, written by this call only:
+ *   seq_pages   int32 [num_seqs][max_blocks_per_seq]: pages of sequence s in
+ *               logical order
+ *   seq_lens    int32 [num_seqs]: tokens of sequence s (0 at the start)
+ *   free_pages  int32 [num_blocks]: a ring of the pages that no sequence holds
+ *   free_state  int32 [4]: the ring's first entry, how many there are, a word that
+ *               is 0 between calls, and how many steps were refused so far
+ *               (at the start: all pages in the ring in any order, 0, num_blocks, 0, 0)
+ * A step:
+ *   seq_ids     int32 [R]: the sequence of row r, each at most once; negative: a
+ *               row of padding (length 0, no tokens)
+ *   new_tokens  int32 [R]: c > 0 adds c tokens to the row's sequence, c < 0 drops
+ *               its last -c (all of them if it has fewer), as rejected drafts or
+ *               a finished request
+ * Pages are taken from the ring's front row by row, pages that are no longer
+ * needed go behind its end; sequences share no pages.  Out, all of it written:
+ *   block_table   int32 [R][table_blocks]: the row's pages, 0 behind them
+ *   context_lens  int32 [R]: the new lengths
+ *   query_start   int32 [R + 1]: prefix sums of the added tokens
+ *   slots         int64 [max_tokens]: slot of each added token, -1 behind the last
+ *   positions     int64 [max_tokens]: its position, 0 behind the last
+ * All or nothing: a step that does not fit changes no state, adds no token and
+ * shows the old lengths and pages; free_state[3] counts it and PA_DEVERR_NO_BLOCKS
+ * (pages, a table too narrow for a row, max_tokens) or PA_DEVERR_BAD_REQUEST (an id
+ * past num_seqs or twice, state that this call did not write) is recorded.
+ * Validate mode also checks that every page is in the ring or with one sequence.
+ * At most 4096 rows and 2^19 sequences; table capacities at most 2^30 tokens.
+ * Steps of one state follow one another: calls that may overlap on the GPU, and
+ * replays of a graph on two streams, are a caller error.
+ */
+int pa_plan_step(const int32_t *seq_ids, const int32_t *new_tokens, int R, int32_t *seq_pages,
+                 int max_blocks_per_seq, int32_t *seq_lens, int num_seqs, int32_t *free_pages,
+                 int32_t *free_state, int64_t num_blocks, int block_size, int32_t *block_table,
+                 int table_blocks, int32_t *context_lens, int32_t *query_start, int64_t *slots,
+                 int64_t *positions, int max_tokens, pa_stream_t stream);
+
+/*
+ * pa_linear_decode, pa_linear_prefill -- linear attention with a decay for each
+ * head, whose state is all that a sequence keeps:
+ *   S_t = l_h S_{t-1} + k_t v_t^T,   o_t = scale * q_t S_t,   l_h = exp(log_decay[h])
+ *   out, q, k, v  [tokens][H][head_dim] (dtype); out is contiguous, the others have
+ *                 q_stride .. v_stride elements between tokens (heads of a token
+ *                 contiguous; a multiple of 16 bytes, at most 2^28); out overlaps
+ *                 none of them
+ *   states        float32 [num_states][H][head_dim][head_dim], element (i, j) of a
+ *                 head belonging to k_i v_j; updated in place
+ *   state_ids     int32 [R]: the state of request r, each at most once (a caller
+ *                 error otherwise; PA_ERR_INVALID in validate mode)
+ *   context_lens  int32 [R]: tokens of the sequence, the new ones included, as
+ *                 pa_plan_step gives them.  A request whose context is its new
+ *                 tokens alone starts from nothing, whatever its state holds.
+ *   log_decay     float32 [H], each at most 0
+ * pa_linear_decode: one token per request (R = B rows).  A row with a negative
+ * state id or context length 0 is padding: zeros, and no state is touched.
+ * pa_linear_prefill: request r has the rows query_start[r] .. query_start[r + 1]
+ * of total_tokens; a request without new tokens, or with a negative state id, is
+ * left out, and rows outside every request are left as they are.  max_query_len
+ * >= every request's new tokens.
+ *   workspace     device buffer of at least pa_linear_prefill_workspace_size
+ *                 bytes, 16-byte aligned, scratch (may be NULL if that is 0);
+ *                 calls that may overlap on the GPU need separate ones
+ * A request whose numbers do not fit is left out (of a decode: zeros) and
+ * PA_DEVERR_BAD_REQUEST recorded.  Sums and states are kept in fp32.
+ */
+int pa_linear_decode(void *out, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                     const void *v, int64_t v_stride, float *states, int num_states,
+                     const int32_t *state_ids, const int32_t *context_lens, const float *log_decay,
+                     int B, int H, int head_dim, float scale, int dtype, pa_stream_t stream);
+int pa_linear_prefill_workspace_size(int R, int total_tokens, int max_query_len, int H, int head_dim,
+                                     int dtype, size_t *bytes);
+int pa_linear_prefill(void *out, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                      const void *v, int64_t v_stride, float *states, int num_states,
+                      const int32_t *state_ids, const int32_t *query_start,
+                      const int32_t *context_lens, const float *log_decay, int R, int total_tokens,
+                      int max_query_len, int H, int head_dim, float scale, void *workspace,
+                      size_t workspace_bytes, int dtype, pa_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Host block manager (opaque handle; C++ behind the C ABI).

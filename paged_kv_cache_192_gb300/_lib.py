@@ -12,7 +12,7 @@ LIB_PATH = os.path.join(_HERE, "libpa_gb300.so")
 
 PA_OK, PA_ERR_INVALID, PA_ERR_OOM, PA_ERR_CUDA, PA_ERR_UNSUPPORTED, PA_ERR_DEVICE = range(6)
 PA_BF16, PA_F32 = 0, 1
-PA_DEVERR_BAD_BLOCK, PA_DEVERR_TIMEOUT = 1, 2
+PA_DEVERR_BAD_BLOCK, PA_DEVERR_TIMEOUT, PA_DEVERR_BAD_REQUEST, PA_DEVERR_NO_BLOCKS = 1, 2, 4, 8
 PA_DECODE_PERSISTENT, PA_DECODE_GRID = 1, 2
 PA_DECODE_TILE_CUDA_CORE, PA_DECODE_TILE_TENSOR_CORE = 1, 2
 PA_PREFILL_PERSISTENT_GRID, PA_PREFILL_ITEM_GRID, PA_PREFILL_SIMPLE = 1, 2, 3
@@ -83,6 +83,15 @@ SIGNATURES = {
                                               ctypes.POINTER(_c_int)]),
     "pa_prefill_kernel_for": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_i64,
                                        _c_int, ctypes.POINTER(_c_int)]),
+    "pa_plan_step": (_c_int, [_c_vp, _c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_i64,
+                              _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp]),
+    "pa_linear_decode": (_c_int, [_c_vp, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_int,
+                                  _c_vp, _c_vp, _c_vp, _c_int, _c_int, _c_int, _c_f, _c_int, _c_vp]),
+    "pa_linear_prefill_workspace_size": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                                  ctypes.POINTER(_c_sz)]),
+    "pa_linear_prefill": (_c_int, [_c_vp, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_int,
+                                   _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                   _c_f, _c_vp, _c_sz, _c_int, _c_vp]),
     "pa_bm_create": (_c_int, [_c_i64, _c_int, ctypes.c_uint64, ctypes.POINTER(_c_vp)]),
     "pa_bm_destroy": (None, [_c_vp]),
     "pa_bm_add_seq": (_c_int, [_c_vp, _c_i64, _c_i64, _p_i64]),

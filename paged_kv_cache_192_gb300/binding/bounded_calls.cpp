@@ -1,7 +1,7 @@
-// Torch-facing binding of the bounded-cache calls (rotary store, compaction,
-// windowed decode and prefill): argument checks, output allocation, and the
-// call into the C ABI of include/pa.h.  Marshalling only, as in ops.py, whose
-// functions forward here.
+// Torch-facing binding of the calls whose time on the host counts (rotary store,
+// compaction, windowed decode and prefill; a step's plan, linear attention): argument
+// checks, output allocation, and the call into the C ABI of include/pa.h.
+// Marshalling only, as in ops.py, whose functions forward here.
 //
 // Why not ctypes: a decode step's calls run 3 to 12 us on the GPU, and their
 // checks and marshalling in Python took 9 to 18 us on the host.
@@ -126,6 +126,11 @@ struct Place {
     }
     at::Tensor new_like(const at::Tensor &t) const {
         return at::Tensor(at::detail::empty_cuda(t.sizes(), t.scalar_type(), t.device(), std::nullopt));
+    }
+    at::Tensor new_empty(std::initializer_list<int64_t> dims, at::ScalarType type) const {
+        return at::Tensor(at::detail::empty_cuda(at::IntArrayRef(dims.begin(), dims.size()), type,
+                                                 c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(device)),
+                                                 std::nullopt));
     }
 };
 
@@ -364,6 +369,158 @@ PyObject *prefill_window(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// seq_pages, seq_lens, free_pages, free_state, seq_ids, new_tokens, block_size,
+// max_tokens, table_blocks (None: as seq_pages), out (None or five tensors),
+// stream; returns the five tensors of the plan
+PyObject *plan_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded("plan_step", 11, n, [&]() -> PyObject * {
+        const at::Tensor &pages = tensor(a[0], "seq_pages"), &lens = tensor(a[1], "seq_lens"),
+                         &ring = tensor(a[2], "free_pages"), &state = tensor(a[3], "free_state"),
+                         &ids = tensor(a[4], "seq_ids"), &change = tensor(a[5], "new_tokens");
+        const int bs = int32_of(a[6], "block_size"), max_tokens = int32_of(a[7], "max_tokens");
+        if (pages.dim() != 2 || ring.dim() != 1 || ids.dim() != 1)
+            value_error("seq_pages must be [num_seqs][max_blocks], free_pages [num_blocks], seq_ids [R]");
+        const int64_t S = pages.size(0), MB = pages.size(1), R = ids.size(0);
+        if (!sized(lens, {S})) value_error("seq_lens must be " + shape({S}));
+        if (!sized(state, {4})) value_error("free_state must be [4]");
+        if (!sized(change, {R})) value_error("new_tokens must be " + shape({R}));
+        if (max_tokens < 0) value_error("max_tokens must not be negative");
+        int64_t W = a[8] == Py_None ? MB : int32_of(a[8], "table_blocks");
+        if (W < 0) value_error("table_blocks must be positive");
+        at::Tensor out[5];
+        const bool given = a[9] != Py_None;
+        if (given) {
+            PyObject *seq = PySequence_Fast(a[9], "out must be a StepPlan");
+            if (!seq) throw Raised{};
+            struct Drop {
+                PyObject *o;
+                ~Drop() { Py_DECREF(o); }
+            } drop{seq};
+            if (PySequence_Fast_GET_SIZE(seq) != 5) value_error("out must be a StepPlan");
+            for (int i = 0; i < 5; ++i) out[i] = tensor(PySequence_Fast_GET_ITEM(seq, i), "out");
+            if (a[8] == Py_None && out[0].dim() == 2) W = out[0].size(1);
+            if (!sized(out[0], {R, W}) || !sized(out[1], {R}) || !sized(out[2], {R + 1}) ||
+                !sized(out[3], {max_tokens}) || !sized(out[4], {max_tokens}))
+                value_error("out must be " + shape({R, W}) + ", " + shape({R}) + ", " + shape({R + 1}) + ", " +
+                            shape({max_tokens}) + ", " + shape({max_tokens}));
+        }
+        const Place place(pages, "seq_pages", a[10]);
+        void *pp = place(pages, "seq_pages", at::kInt), *lp = place(lens, "seq_lens", at::kInt),
+             *rp = place(ring, "free_pages", at::kInt), *sp = place(state, "free_state", at::kInt);
+        const void *ip = place(ids, "seq_ids", at::kInt), *cp = place(change, "new_tokens", at::kInt);
+        if (!given) {
+            out[0] = place.new_empty({R, W}, at::kInt);
+            out[1] = place.new_empty({R}, at::kInt);
+            out[2] = place.new_empty({R + 1}, at::kInt);
+            out[3] = place.new_empty({max_tokens}, at::kLong);
+            out[4] = place.new_empty({max_tokens}, at::kLong);
+        }
+        void *op[5];
+        const char *names[5] = {"block_table", "context_lens", "query_start", "slots", "positions"};
+        for (int i = 0; i < 5; ++i) op[i] = place(out[i], names[i], i < 3 ? at::kInt : at::kLong);
+        const int iR = int32_of(R, "R"), iS = int32_of(S, "num_seqs"), iMB = int32_of(MB, "max_blocks"),
+                  iW = int32_of(W, "table_blocks");
+        launch([&] {
+            return pa_plan_step(static_cast<const int32_t *>(ip), static_cast<const int32_t *>(cp), iR,
+                                static_cast<int32_t *>(pp), iMB, static_cast<int32_t *>(lp), iS,
+                                static_cast<int32_t *>(rp), static_cast<int32_t *>(sp), ring.size(0), bs,
+                                static_cast<int32_t *>(op[0]), iW, static_cast<int32_t *>(op[1]),
+                                static_cast<int32_t *>(op[2]), static_cast<int64_t *>(op[3]),
+                                static_cast<int64_t *>(op[4]), max_tokens, place.stream);
+        });
+        PyObject *r = PyTuple_New(5);
+        if (!r) throw Raised{};
+        for (int i = 0; i < 5; ++i) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(out[i]));
+        return r;
+    });
+}
+
+// What both linear calls take; the pointers follow once the shapes are known.
+struct Linear {
+    const at::Tensor &q, &k, &v, &states, &ids, &lens, &decay;
+    int64_t T, H, d, R, qs, ks, vs;
+    Linear(PyObject *const *a, PyObject *lens_, PyObject *decay_)
+        : q(tensor(a[0], "q")), k(tensor(a[1], "k")), v(tensor(a[2], "v")), states(tensor(a[3], "states")),
+          ids(tensor(a[4], "state_ids")), lens(tensor(lens_, "context_lens")), decay(tensor(decay_, "log_decay")) {
+        if (q.dim() != 3 || states.dim() != 4 || ids.dim() != 1)
+            value_error("q must be [tokens][H][d], states [num_states][H][d][d], state_ids [R]");
+        T = q.size(0), H = q.size(1), d = q.size(2), R = ids.size(0);
+        qs = token_rows(q, "q", T, H, d), ks = token_rows(k, "k", T, H, d), vs = token_rows(v, "v", T, H, d);
+        if (!sized(states, {states.size(0), H, d, d}))
+            value_error("states must be [num_states]" + shape({H, d, d}));
+        if (!sized(lens, {R})) value_error("context_lens must be " + shape({R}));
+        if (!sized(decay, {H})) value_error("log_decay must be " + shape({H}));
+    }
+};
+
+// q, k, v, states, state_ids, context_lens, log_decay, scale, out, stream
+PyObject *linear_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded("linear_decode", 10, n, [&]() -> PyObject * {
+        const Linear x(a, a[5], a[6]);
+        if (x.R != x.T) value_error("state_ids must be " + shape({x.T}));
+        const bool given = a[8] != Py_None;
+        if (given && tensor(a[8], "out").sizes() != x.q.sizes()) value_error("out must have the shape of q");
+        const float scale = scale_of(a[7], x.d);
+        const Place place(x.q, "q", a[9]);
+        const at::ScalarType dt = x.q.scalar_type();
+        const int code = dtype_of(x.q);
+        const void *qp = place(x.q, "q", dt, false), *kp = place(x.k, "k", dt, false),
+                   *vp = place(x.v, "v", dt, false), *ip = place(x.ids, "state_ids", at::kInt),
+                   *lp = place(x.lens, "context_lens", at::kInt), *dp = place(x.decay, "log_decay", at::kFloat);
+        void *sp = place(x.states, "states", at::kFloat);
+        const at::Tensor out = given ? tensor(a[8], "out") : place.new_like(x.q);
+        void *op = place(out, "out", dt);
+        const int ns = int32_of(x.states.size(0), "num_states"), B = int32_of(x.R, "B"), H = int32_of(x.H, "H"),
+                  d = int32_of(x.d, "head_dim");
+        launch([&] {
+            return pa_linear_decode(op, qp, x.qs, kp, x.ks, vp, x.vs, static_cast<float *>(sp), ns,
+                                    static_cast<const int32_t *>(ip), static_cast<const int32_t *>(lp),
+                                    static_cast<const float *>(dp), B, H, d, scale, code, place.stream);
+        });
+        return THPVariable_Wrap(out);
+    });
+}
+
+// q, k, v, states, state_ids, query_start, context_lens, max_query_len,
+// log_decay, scale, out, workspace, stream
+PyObject *linear_prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded("linear_prefill", 13, n, [&]() -> PyObject * {
+        const Linear x(a, a[6], a[8]);
+        const at::Tensor &start = tensor(a[5], "query_start");
+        const int max_query_len = int32_of(a[7], "max_query_len");
+        if (!sized(start, {x.R + 1})) value_error("query_start must be " + shape({x.R + 1}));
+        const bool given = a[10] != Py_None;
+        if (given && tensor(a[10], "out").sizes() != x.q.sizes()) value_error("out must have the shape of q");
+        const float scale = scale_of(a[9], x.d);
+        const Place place(x.q, "q", a[12]);
+        const at::ScalarType dt = x.q.scalar_type();
+        const int code = dtype_of(x.q);
+        const void *qp = place(x.q, "q", dt, false), *kp = place(x.k, "k", dt, false),
+                   *vp = place(x.v, "v", dt, false), *ip = place(x.ids, "state_ids", at::kInt),
+                   *tp = place(start, "query_start", at::kInt), *lp = place(x.lens, "context_lens", at::kInt),
+                   *dp = place(x.decay, "log_decay", at::kFloat);
+        void *sp = place(x.states, "states", at::kFloat);
+        const int ns = int32_of(x.states.size(0), "num_states"), R = int32_of(x.R, "R"), T = int32_of(x.T, "tokens"),
+                  H = int32_of(x.H, "H"), d = int32_of(x.d, "head_dim");
+        size_t bytes = 0;
+        launch([&] { return pa_linear_prefill_workspace_size(R, T, max_query_len, H, d, code, &bytes); });
+        at::Tensor ws;
+        if (a[11] != Py_None) ws = tensor(a[11], "workspace");
+        else if (bytes) ws = place.new_empty({static_cast<int64_t>((bytes + 3) / 4)}, at::kFloat);
+        void *wp = ws.defined() ? place(ws, "workspace", at::kFloat) : nullptr;
+        const size_t have = ws.defined() ? static_cast<size_t>(ws.numel()) * 4 : 0;
+        const at::Tensor out = given ? tensor(a[10], "out") : place.new_like(x.q);
+        void *op = place(out, "out", dt);
+        launch([&] {
+            return pa_linear_prefill(op, qp, x.qs, kp, x.ks, vp, x.vs, static_cast<float *>(sp), ns,
+                                     static_cast<const int32_t *>(ip), static_cast<const int32_t *>(tp),
+                                     static_cast<const int32_t *>(lp), static_cast<const float *>(dp), R, T,
+                                     max_query_len, H, d, scale, wp, have, code, place.stream);
+        });
+        return THPVariable_Wrap(out);
+    });
+}
+
 PyObject *set_check(PyObject *, PyObject *callable) {
     Py_INCREF(callable);
     Py_XSETREF(g_check, callable);
@@ -375,6 +532,9 @@ PyMethodDef kMethods[] = {{"rope_reshape_and_cache", PA_FAST(rope_reshape_and_ca
                           {"compact_cache", PA_FAST(compact_cache)},
                           {"decode_window", PA_FAST(decode_window)},
                           {"prefill_window", PA_FAST(prefill_window)},
+                          {"plan_step", PA_FAST(plan_step)},
+                          {"linear_decode", PA_FAST(linear_decode)},
+                          {"linear_prefill", PA_FAST(linear_prefill)},
                           {"set_check", set_check, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_bounded_calls", nullptr, -1, kMethods,

@@ -1,0 +1,53 @@
+// What the translation units of linear attention share.
+#pragma once
+
+#include "pa_prefill.cuh"
+
+namespace pa {
+namespace lin {
+
+struct LinParams {
+    void *out;
+    const void *q, *k, *v;  // [T][H][D], q_stride .. v_stride elements between tokens
+    int64_t q_stride, k_stride, v_stride;
+    float *states;  // [num_states][H][D][D]: element (i, j) belongs to k_i v_j
+    const int32_t *state_ids, *query_start, *context_lens;  // query_start NULL: one token per row
+    const float *log_decay;
+    int *err;
+    int R, T, H, num_states;
+    float scale;
+};
+
+// What a request of the call is: its rows [t0, t0 + n) of q, its state, and
+// whether the state holds something (else it starts from nothing).
+struct Request {
+    int t0, n, state;  // state -1: padding, or numbers that do not fit
+    bool held;
+};
+
+__device__ __forceinline__ Request request(const LinParams &p, int r) {
+    Request x;
+    const int L = p.context_lens[r];
+    x.state = p.state_ids[r];
+    x.t0 = p.query_start ? p.query_start[r] : r;
+    x.n = p.query_start ? p.query_start[r + 1] - x.t0 : (L != 0);
+    x.held = L > x.n;
+    const bool padding = x.n == 0 || x.state < 0;
+    if (padding || x.state >= p.num_states || x.t0 < 0 || x.n < 0 || x.n > p.T - x.t0 || L < x.n) {
+        if (!padding) record_error(p.err, PA_DEVERR_BAD_REQUEST);
+        x.state = -1;
+    }
+    return x;
+}
+
+// Decay per token as a power of two: l = 2^x.  Logarithms below -1e4 (l is 0 in
+// 32 bits long before) stay finite, so that l^0 is 1.
+__device__ __forceinline__ float log2_decay(const LinParams &p, int h) {
+    return fmaxf(p.log_decay[h], -1e4f) * pf::kLog2e;
+}
+
+// The recurrent kernel (pa_linear.cu), any number of tokens and both types.
+int launch_recurrent(const LinParams &p, int D, int dtype, cudaStream_t stream);
+
+}  // namespace lin
+}  // namespace pa

@@ -40,6 +40,16 @@ def alloc_pools(num_blocks, Hkv, block_size, head_dim, dtype, device="cuda", poi
     return k, v
 
 
+def page_state(num_seqs, max_blocks, num_blocks, device="cuda"):
+    """An ops.PageState of sequences without tokens: every page is free, in the
+    pool's order."""
+    return ops.PageState(
+        torch.zeros(num_seqs, max_blocks, dtype=torch.int32, device=device),
+        torch.zeros(num_seqs, dtype=torch.int32, device=device),
+        torch.arange(num_blocks, dtype=torch.int32, device=device),
+        torch.tensor([0, num_blocks, 0, 0], dtype=torch.int32, device=device))
+
+
 def all_slots(table, lens, block_size):
     """Slots of every token of every sequence, stacked in logical order."""
     parts = [slots_for(table[s], np.arange(int(L)), block_size) for s, L in enumerate(lens)]

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import importlib
 import math
+from typing import NamedTuple
 
 import torch
 
@@ -57,9 +58,9 @@ _bounded = None
 
 def _calls():
     """The extension module that binds the bounded-cache calls (rotary store,
-    compaction, windowed decode and prefill): the same checks and marshalling
-    as here, in C++, because small calls are bound by their time on the host.
-    They run on the device of their tensors."""
+    compaction, windowed decode and prefill), a step's plan and linear attention: the
+    same checks and marshalling as here, in C++, because small calls are bound by
+    their time on the host.  They run on the device of their tensors."""
     global _bounded
     if _bounded is None:
         lib()  # the library, or its error if it has not been built
@@ -489,3 +490,75 @@ def prefill_window(q, k_cache, v_cache, block_table, query_start, context_lens, 
     result.  Returns out [tokens][Hq][d]."""
     return _calls().prefill_window(q, k_cache, v_cache, block_table, query_start, context_lens,
                                    max_query_len, window, num_sinks, scale, out, stream)
+
+
+class PageState(NamedTuple):
+    """Sequences and pages that plan_step keeps on the device (layout.page_state
+    makes them); only plan_step writes them."""
+    seq_pages: torch.Tensor   # int32 [num_seqs][max_blocks]: each sequence's pages in logical order
+    seq_lens: torch.Tensor    # int32 [num_seqs]: each sequence's tokens
+    free_pages: torch.Tensor  # int32 [num_blocks]: ring of the pages that no sequence holds
+    free_state: torch.Tensor  # int32 [4]: its first entry, their number, 0, steps refused so far
+
+
+class StepPlan(NamedTuple):
+    """What a step's other calls read (plan_step)."""
+    block_table: torch.Tensor   # int32 [R][table_blocks], 0 behind a row's pages
+    context_lens: torch.Tensor  # int32 [R], the new tokens included
+    query_start: torch.Tensor   # int32 [R + 1], prefix sums of the added tokens
+    slots: torch.Tensor         # int64 [max_tokens], -1 behind the last added token
+    positions: torch.Tensor     # int64 [max_tokens], 0 behind the last
+
+
+def plan_step(state, seq_ids, new_tokens, block_size, max_tokens, table_blocks=None, out=None,
+              stream=None) -> StepPlan:
+    """Block tables, slots and positions of a step, built on the device from its
+    requests' lengths (pa_plan_step).
+
+    state: a PageState, advanced in place.  seq_ids: int32 [R], the sequence of
+    each row, each at most once; negative: a row of padding.  new_tokens: int32
+    [R], tokens that the row's sequence gains, or loses if negative (its last
+    ones; all of them if it has fewer).  Pages are taken from the front of the
+    ring row by row and given back behind its end.  max_tokens: length of slots
+    and positions; table_blocks: width of block_table (seq_pages' by default).
+    All or nothing: a step that does not fit is refused (free_state[3] counts it,
+    the device error word says why) and shows the old lengths, no new token.
+    out: a StepPlan to write into.  Returns the StepPlan."""
+    return StepPlan(*_calls().plan_step(state[0], state[1], state[2], state[3], seq_ids, new_tokens,
+                                        block_size, max_tokens, table_blocks, out, stream))
+
+
+def linear_decode(q, k, v, states, state_ids, context_lens, log_decay, scale=None, out=None,
+                  stream=None):
+    """Linear attention with a decay for each head, one token per sequence
+    (pa_linear_decode).
+
+    q, k, v: [B][H][d], bf16 or fp32, the heads of a token contiguous (slices of
+    a fused projection are fine).  states: float32 [num_states][H][d][d], updated
+    in place: S = exp(log_decay) S + k v^T; out = scale q S (scale: 1/sqrt(d) by
+    default).  state_ids: int32 [B], each state at most once.  context_lens: int32
+    [B]: 1 starts from nothing, whatever the state holds; 0, or a negative state
+    id, is padding (zeros).  log_decay: float32 [H], at most 0.  Returns out."""
+    return _calls().linear_decode(q, k, v, states, state_ids, context_lens, log_decay, scale, out,
+                                  stream)
+
+
+def linear_prefill_workspace_size(R, total_tokens, max_query_len, H, head_dim, dtype=torch.bfloat16):
+    out = ctypes.c_size_t(0)
+    check(lib().pa_linear_prefill_workspace_size(R, total_tokens, max_query_len, H, head_dim,
+                                                 _DTYPES[dtype], ctypes.byref(out)))
+    return out.value
+
+
+def linear_prefill(q, k, v, states, state_ids, query_start, context_lens, max_query_len, log_decay,
+                   scale=None, out=None, workspace=None, stream=None):
+    """linear_decode for chunks of several tokens (pa_linear_prefill).
+
+    Request r owns rows query_start[r] .. query_start[r + 1] (int32 [R + 1]) of
+    q, k, v [tokens][H][d]; context_lens[r] counts its earlier tokens too, and a
+    request without earlier ones starts from nothing.  max_query_len bounds the
+    chunks' lengths.  Requests without new tokens or with a negative state id are
+    left out; rows outside every request get no result.  workspace: float32, at
+    least linear_prefill_workspace_size bytes (allocated when not given)."""
+    return _calls().linear_prefill(q, k, v, states, state_ids, query_start, context_lens,
+                                   max_query_len, log_decay, scale, out, workspace, stream)
