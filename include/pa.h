@@ -609,6 +609,34 @@ int pa_plan_step(const int32_t *seq_ids, const int32_t *new_tokens, int R, int32
                  int64_t *positions, int max_tokens, pa_stream_t stream);
 
 /*
+ * pa_cross_attention -- attention of each request's query tokens to the states of
+ * an encoder, kept in pages like any K and V: request r has n_r = query_start[r+1]
+ * - query_start[r] query tokens (any number, also none), each of which sees all
+ * L_r = encoder_lens[r] states:
+ *   o = sum_{j < L_r} softmax(scale q . k_j) v_j;   zeros where L_r = 0
+ *   out, q        [total_tokens][Hq][head_dim]  (bf16 only); rows outside every
+ *                 request are left as they are
+ *   query_start   int32 [R+1] prefix sum of query token counts, inside
+ *                 [0, total_tokens]
+ *   encoder_lens  int32 [R], each in [0, capacity]
+ *   max_query_len host int >= every request's query tokens (with less, rows may be
+ *                 left out and PA_DEVERR_BAD_REQUEST recorded)
+ * The states of a request are read once for all of its tokens (beams that share an
+ * encoder run are the query tokens of one request).  Slots behind the last state
+ * do not enter the result, whatever they hold, nor are table entries behind it
+ * read; a NaN or infinity in a state reaches the rows of its own request.  A request
+ * whose numbers do not fit is left out and PA_DEVERR_BAD_REQUEST recorded.  Other
+ * arguments and the error bound as for pa_prefill_window.  At most 65535 requests;
+ * one launch per 256 requests, without a workspace.
+ */
+int pa_cross_attention(void *out, const void *q, const void *k_cache, const void *v_cache,
+                       const int32_t *block_table, int max_blocks_per_seq,
+                       const int32_t *query_start, const int32_t *encoder_lens, int R,
+                       int total_tokens, int max_query_len, int Hq, int Hkv, int head_dim,
+                       int block_size, int64_t num_blocks, float scale, int dtype,
+                       pa_stream_t stream);
+
+/*
  * pa_linear_decode, pa_linear_prefill -- linear attention with a decay for each
  * head, whose state is all that a sequence keeps:
  *   S_t = l_h S_{t-1} + k_t v_t^T,   o_t = scale * q_t S_t,   l_h = exp(log_decay[h])

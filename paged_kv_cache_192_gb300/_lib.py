@@ -85,6 +85,9 @@ SIGNATURES = {
                                        _c_int, ctypes.POINTER(_c_int)]),
     "pa_plan_step": (_c_int, [_c_vp, _c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_i64,
                               _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp]),
+    "pa_cross_attention": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_int,
+                                    _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_i64, _c_f,
+                                    _c_int, _c_vp]),
     "pa_linear_decode": (_c_int, [_c_vp, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_int,
                                   _c_vp, _c_vp, _c_vp, _c_int, _c_int, _c_int, _c_f, _c_int, _c_vp]),
     "pa_linear_prefill_workspace_size": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int,

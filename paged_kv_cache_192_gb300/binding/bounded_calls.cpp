@@ -1,6 +1,6 @@
 // Torch-facing binding of the calls whose time on the host counts (rotary store,
-// compaction, windowed decode and prefill; a step's plan, linear attention): argument
-// checks, output allocation, and the call into the C ABI of include/pa.h.
+// compaction, windowed decode and prefill; a step's plan, cross and linear attention):
+// argument checks, output allocation, and the call into the C ABI of include/pa.h.
 // Marshalling only, as in ops.py, whose functions forward here.
 //
 // Why not ctypes: a decode step's calls run 3 to 12 us on the GPU, and their
@@ -435,6 +435,49 @@ PyObject *plan_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// q, k_cache, v_cache, block_table, query_start, encoder_lens, max_query_len,
+// scale, out, stream
+PyObject *cross_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded("cross_attention", 10, n, [&]() -> PyObject * {
+        const at::Tensor &q = tensor(a[0], "q"), &k_cache = tensor(a[1], "k_cache"),
+                         &v_cache = tensor(a[2], "v_cache"), &table = tensor(a[3], "block_table"),
+                         &start = tensor(a[4], "query_start"), &lens = tensor(a[5], "encoder_lens");
+        const int max_query_len = int32_of(a[6], "max_query_len");
+        if (q.dim() != 3 || k_cache.dim() != 4 || lens.dim() != 1)
+            value_error("q must be [tokens][Hq][d], pools [NB][Hkv][bs][d], encoder_lens [R]");
+        const int64_t T = q.size(0), d = q.size(2), R = lens.size(0);
+        if (k_cache.size(3) != d)
+            value_error("pools must have head_dim " + std::to_string(d) + " like q");
+        same_pools(k_cache, v_cache);
+        if (!sized(start, {R + 1})) value_error("query_start must be " + shape({R + 1}));
+        if (table.dim() != 2 || table.size(0) != R)
+            value_error("block_table must be " + shape({R}) + "[max_blocks_per_seq]");
+        const bool given = a[8] != Py_None;
+        if (given && tensor(a[8], "out").sizes() != q.sizes())
+            value_error("out must have the shape of q");
+        const float scale = scale_of(a[7], d);
+        const Place place(q, "q", a[9]);
+        const at::ScalarType dt = k_cache.scalar_type();
+        const int code = dtype_of(k_cache);
+        const void *qp = place(q, "q", dt), *kc = place(k_cache, "k_cache", dt),
+                   *vc = place(v_cache, "v_cache", dt), *tp = place(table, "block_table", at::kInt),
+                   *sp = place(start, "query_start", at::kInt), *lp = place(lens, "encoder_lens", at::kInt);
+        const at::Tensor out = given ? tensor(a[8], "out") : place.new_like(q);
+        void *op = place(out, "out", dt);
+        const int MB = int32_of(table.size(1), "block_table"), iR = int32_of(R, "R"),
+                  iT = int32_of(T, "tokens"), Hq = int32_of(q.size(1), "Hq"),
+                  Hkv = int32_of(k_cache.size(1), "Hkv"),
+                  bs = int32_of(k_cache.size(2), "block_size"), id = int32_of(d, "head_dim");
+        launch([&] {
+            return pa_cross_attention(op, qp, kc, vc, static_cast<const int32_t *>(tp), MB,
+                                      static_cast<const int32_t *>(sp), static_cast<const int32_t *>(lp), iR,
+                                      iT, max_query_len, Hq, Hkv, id, bs, k_cache.size(0), scale, code,
+                                      place.stream);
+        });
+        return THPVariable_Wrap(out);
+    });
+}
+
 // What both linear calls take; the pointers follow once the shapes are known.
 struct Linear {
     const at::Tensor &q, &k, &v, &states, &ids, &lens, &decay;
@@ -533,6 +576,7 @@ PyMethodDef kMethods[] = {{"rope_reshape_and_cache", PA_FAST(rope_reshape_and_ca
                           {"decode_window", PA_FAST(decode_window)},
                           {"prefill_window", PA_FAST(prefill_window)},
                           {"plan_step", PA_FAST(plan_step)},
+                          {"cross_attention", PA_FAST(cross_attention)},
                           {"linear_decode", PA_FAST(linear_decode)},
                           {"linear_prefill", PA_FAST(linear_prefill)},
                           {"set_check", set_check, METH_O, nullptr},

@@ -27,6 +27,7 @@
 #include <new>
 #include <vector>
 
+#include "pa_cluster.cuh"
 #include "pa_decode_tile.cuh"
 #include "pa_prefill.cuh"
 
@@ -93,43 +94,6 @@ struct Layout {
     static_assert(WARP % 1024 == 0, "swizzled stages must stay aligned");
 };
 
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_nctarank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void st_cluster2(uint32_t addr, float2 v) {
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(addr), "f"(v.x), "f"(v.y)
-                 : "memory");
-}
-
-template <typename T>
-__device__ __forceinline__ void store2(T *dst, float2 v);
-template <>
-__device__ __forceinline__ void store2<__nv_bfloat16>(__nv_bfloat16 *dst, float2 v) {
-    *reinterpret_cast<__nv_bfloat162 *>(dst) = __floats2bfloat162_rn(v.x, v.y);
-}
-template <>
-__device__ __forceinline__ void store2<float>(float *dst, float2 v) {
-    *reinterpret_cast<float2 *>(dst) = v;
-}
-
 // The visible tiles of one sequence: ns sink tiles from token 0, then nw
 // window tiles from token wbase; lo is the window's first token.  With the
 // window reaching the sinks there is one range from token 0.
@@ -167,12 +131,6 @@ __device__ __forceinline__ void put_result(WarpAttn<T, D, GQ> &st, float *acc, f
     float lh[GQ];
     st.reduce(lh);
     st.store_partial(acc, D, reinterpret_cast<float *>(ml), 2, lh);
-}
-
-// weight of a partial with maximum m under the common maximum M (0 for an
-// empty one; also when every partial is empty)
-__device__ __forceinline__ float weight(float m, float M) {
-    return m == -INFINITY ? 0.f : exp2f(m - M);
 }
 
 template <typename T, int D, int GQ, bool DEEP>

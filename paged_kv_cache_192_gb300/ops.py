@@ -58,9 +58,9 @@ _bounded = None
 
 def _calls():
     """The extension module that binds the bounded-cache calls (rotary store,
-    compaction, windowed decode and prefill), a step's plan and linear attention: the
-    same checks and marshalling as here, in C++, because small calls are bound by
-    their time on the host.  They run on the device of their tensors."""
+    compaction, windowed decode and prefill), a step's plan, cross and linear attention:
+    the same checks and marshalling as here, in C++, because small calls are bound
+    by their time on the host.  They run on the device of their tensors."""
     global _bounded
     if _bounded is None:
         lib()  # the library, or its error if it has not been built
@@ -526,6 +526,21 @@ def plan_step(state, seq_ids, new_tokens, block_size, max_tokens, table_blocks=N
     out: a StepPlan to write into.  Returns the StepPlan."""
     return StepPlan(*_calls().plan_step(state[0], state[1], state[2], state[3], seq_ids, new_tokens,
                                         block_size, max_tokens, table_blocks, out, stream))
+
+
+def cross_attention(q, k_cache, v_cache, block_table, query_start, encoder_lens, max_query_len,
+                    scale=None, out=None, stream=None):
+    """Attention to an encoder's states in pages (pa_cross_attention), bf16.
+
+    R requests; request r owns query rows query_start[r] .. query_start[r+1] of
+    q [tokens][Hq][d], all of which see its encoder_lens[r] states (int32 [R], 0:
+    the rows get zeros) through block_table int32 [R][max_blocks_per_seq] into the
+    pools [NB][Hkv][bs][d].  One query token per request is a decode step; beams
+    over one encoder run are the rows of one request, for which the states are
+    read once.  max_query_len bounds the requests' rows; rows of q outside every
+    request get no result.  Returns out [tokens][Hq][d]."""
+    return _calls().cross_attention(q, k_cache, v_cache, block_table, query_start, encoder_lens,
+                                    max_query_len, scale, out, stream)
 
 
 def linear_decode(q, k, v, states, state_ids, context_lens, log_decay, scale=None, out=None,
