@@ -46,6 +46,11 @@ int encode_pool_map(CUtensorMap *map, const void *pool, int64_t rows, int D, int
 int encode_q_map(CUtensorMap *map, const void *q, int64_t tokens, int Hq, int D, int gq,
                  int box_tokens);
 
+// 3D tensor map over rows [tokens][H][D] (bf16) with token_stride elements between
+// tokens: boxes of 64 columns x one head x box_tokens tokens, 128-byte swizzle.
+int encode_rows_map(CUtensorMap *map, const void *x, int64_t tokens, int64_t token_stride, int H, int D,
+                    int box_tokens);
+
 inline size_t dtype_size(int dtype) { return dtype == PA_BF16 ? 2 : (dtype == PA_F32 ? 4 : 0); }
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

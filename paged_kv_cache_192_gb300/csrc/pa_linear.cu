@@ -60,7 +60,9 @@ __global__ void __launch_bounds__(256) recurrent_kernel(const LinParams p) {
 #pragma unroll
     for (int i = 0; i < NR; ++i)
         s[i] = x.held ? *reinterpret_cast<const float4 *>(S + (row0 + i * RG) * D) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float l = exp2f(pa::lin::log2_decay(p, h));
+    // l S = S + (l - 1) S: as exact as its rounding where l is close to 1 and a state
+    // lives long
+    const float lm1 = expm1f(pa::lin::log_decay(p, h));
     auto stage = [&](int t) {
         const int64_t tok = x.t0 + t;
         for (int i = tid; i < 2 * D + CW; i += NT) {
@@ -79,10 +81,10 @@ __global__ void __launch_bounds__(256) recurrent_kernel(const LinParams p) {
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             const float ki = sk[b][row0 + i * RG], qi = sq[b][row0 + i * RG];
-            s[i].x = fmaf(l, s[i].x, ki * vv.x);
-            s[i].y = fmaf(l, s[i].y, ki * vv.y);
-            s[i].z = fmaf(l, s[i].z, ki * vv.z);
-            s[i].w = fmaf(l, s[i].w, ki * vv.w);
+            s[i].x = fmaf(lm1, s[i].x, fmaf(ki, vv.x, s[i].x));
+            s[i].y = fmaf(lm1, s[i].y, fmaf(ki, vv.y, s[i].y));
+            s[i].z = fmaf(lm1, s[i].z, fmaf(ki, vv.z, s[i].z));
+            s[i].w = fmaf(lm1, s[i].w, fmaf(ki, vv.w, s[i].w));
             o.x = fmaf(qi, s[i].x, o.x);
             o.y = fmaf(qi, s[i].y, o.y);
             o.z = fmaf(qi, s[i].z, o.z);
@@ -181,6 +183,14 @@ int check(const char *what, const LinParams &p, int max_query_len, int D, int dt
     return PA_OK;
 }
 
+// Whether a prompt runs on the chunk kernels: bf16 of more tokens than the recurrent
+// kernel takes in the time of one chunk.
+bool uses_chunks(int max_query_len, int dtype) { return dtype == PA_BF16 && max_query_len > 8; }
+
+size_t workspace_bytes_for(const pa::lin::Segments &s, int max_query_len, int H, int D, int dtype) {
+    return uses_chunks(max_query_len, dtype) && s.tokens ? size_t(s.slots) * H * D * D * 4 : 0;
+}
+
 LinParams make(void *out, const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                int64_t v_stride, float *states, int num_states, const int32_t *state_ids, const int32_t *query_start,
                const int32_t *context_lens, const float *log_decay, int R, int T, int H, float scale) {
@@ -257,10 +267,17 @@ extern "C" int pa_linear_prefill(void *out, const void *q, int64_t q_stride, con
     if (int rc = check("linear_prefill", p, max_query_len, head_dim, dtype, &empty)) return rc;
     if (empty) return PA_OK;
     if (!query_start) return pa::fail(PA_ERR_INVALID, "linear_prefill: NULL pointer");
+    const pa::lin::Segments seg = pa::lin::segments_for(R, total_tokens, max_query_len, H);
+    const size_t need = workspace_bytes_for(seg, max_query_len, H, head_dim, dtype);
+    if (need && (!workspace || workspace_bytes < need))
+        return pa::fail(PA_ERR_INVALID, "linear_prefill: workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    if (need && !pa::aligned16(workspace))
+        return pa::fail(PA_ERR_INVALID, "linear_prefill: workspace must be 16-byte aligned");
     if (pa::validate_on())
         if (int rc = validate_linear(p, max_query_len, stream)) return rc;
     p.err = pa::device_error_word();
-    return pa::lin::launch_recurrent(p, head_dim, dtype, stream);
+    if (!uses_chunks(max_query_len, dtype)) return pa::lin::launch_recurrent(p, head_dim, dtype, stream);
+    return pa::lin::launch_chunks(p, head_dim, static_cast<float *>(workspace), seg, stream);
 }
 
 extern "C" int pa_linear_prefill_workspace_size(int R, int total_tokens, int max_query_len, int H, int head_dim,
@@ -270,6 +287,7 @@ extern "C" int pa_linear_prefill_workspace_size(int R, int total_tokens, int max
     if (R < 0 || R > 65535 || total_tokens < 0 || max_query_len < 0 || H <= 0 || H > 1024 ||
         (head_dim != 64 && head_dim != 128) || (dtype != PA_BF16 && dtype != PA_F32))
         return pa::fail(PA_ERR_INVALID, "linear_prefill_workspace_size: bad sizes");
-    *bytes = 0;
+    *bytes = workspace_bytes_for(pa::lin::segments_for(R, total_tokens, max_query_len, H), max_query_len, H, head_dim,
+                                 dtype);
     return PA_OK;
 }

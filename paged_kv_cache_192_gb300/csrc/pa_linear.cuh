@@ -40,14 +40,21 @@ __device__ __forceinline__ Request request(const LinParams &p, int r) {
     return x;
 }
 
-// Decay per token as a power of two: l = 2^x.  Logarithms below -1e4 (l is 0 in
-// 32 bits long before) stay finite, so that l^0 is 1.
-__device__ __forceinline__ float log2_decay(const LinParams &p, int h) {
-    return fmaxf(p.log_decay[h], -1e4f) * pf::kLog2e;
-}
+// Logarithm of a head's decay.  Below -1e4 (the decay is 0 in 32 bits long before) it
+// stays finite, so that l^0 is 1.
+__device__ __forceinline__ float log_decay(const LinParams &p, int h) { return fmaxf(p.log_decay[h], -1e4f); }
 
 // The recurrent kernel (pa_linear.cu), any number of tokens and both types.
 int launch_recurrent(const LinParams &p, int D, int dtype, cudaStream_t stream);
+
+// The kernels of long prompts (pa_linear_chunk.cu), bf16.  A call cuts its requests
+// into segments of `tokens` tokens (0: it does not), at most `slots` of them, whose
+// states [slots][H][D][D] fp32 are the workspace.
+struct Segments {
+    int tokens, slots;
+};
+Segments segments_for(int R, int T, int max_query_len, int H);
+int launch_chunks(const LinParams &p, int D, float *ws, const Segments &s, cudaStream_t stream);
 
 }  // namespace lin
 }  // namespace pa

@@ -1,0 +1,638 @@
+// Linear attention with a decay for each head over chunks of tokens (bf16, tcgen05).
+//
+// With the state S before a chunk of C = 64 tokens, and i, j its tokens,
+//   o_i = scale [ sum_{j <= i} l^(i-j) (q_i . k_j) v_j  +  l^(i+1) q_i S ]
+//   S  <- l^C S + sum_j k_j (l^(C-1-j) v_j)^T
+// so that a chunk is four products: Q K^T, P V with P = Q K^T times the decays, Q S
+// and K^T V'.
+//
+// Bound: HBM (q, k, v and o: 8 D bytes per token and head) if the products, the
+// conversions between them and the copies overlap; a chunk of D = 128 costs 2,800
+// cycles of an SM's part of HBM, 1,800 of its tensor core and about as many
+// issue slots.  Hence one CTA per (request, head) with a warp group for each job:
+//   warps 0-3, 4-7  the state, in registers in fp32 (thread = value dimension, half of
+//                   the key dimensions each): adds a chunk's K^T V' to it and gives
+//                   it to the next chunk's Q S as two bf16 terms in TMEM
+//   warps 8-11      V' = l^(C-1-j) v_j as three bf16 terms in shared memory
+//   warps 12-15     P as two bf16 terms in shared memory (12, 13), outputs
+//   warp 16         loads (TMA); warp 17 issues the tcgen05.mma
+// Outputs are computed transposed (lanes = value dimensions, columns = tokens), so the
+// state is an operand that lies in TMEM, where the threads that own it write it;
+// with tokens as lanes it would take 64 KB of shared memory.  Q K^T has its tokens
+// in lanes 0-63; the other lanes, and for D = 64 the value dimensions from 64 on,
+// hold products of whatever lies behind the operand and are never read.
+//
+// Terms: a state's own sums (K^T V') take V' in three bf16 terms, as exact as its
+// fp32 accumulation; P and S enter an output, which is rounded to bf16, in two
+// (2^-16 of a term).
+//
+// Few (request, head) pairs leave SMs idle: then a request's tokens are cut into
+// segments.  One launch sums each segment's own state (the kernel without its output
+// part), one chains them, and the segments then run like requests.
+#include <algorithm>
+#include <cmath>
+
+#include "pa_linear.cuh"
+
+namespace {
+
+using namespace pa::pf;
+using pa::lin::LinParams;
+using pa::lin::Request;
+
+constexpr int C = 64;  // tokens per chunk
+
+struct ChunkParams {
+    LinParams p;
+    float *ws;     // [slots][H][D][D]: segments' sums, then the states before them
+    int seg;       // tokens per segment (a multiple of C); 0: whole requests
+    int slots;     // segments that the grid and the workspace have room for
+};
+
+template <int D>
+struct Lay {
+    static constexpr int THREADS = 18 * 32;
+    static constexpr int LOAD_WARP = 16, MMA_WARP = 17;
+    static constexpr int NST = D == 128 ? 3 : 4;
+    static constexpr int TILE = C * D * 2;       // a chunk's q, k or v
+    static constexpr int STAGE = 3 * TILE;       // q, k, v
+    static constexpr int OFF_VP = NST * STAGE;   // V' terms
+    static constexpr int P_TERM = C * C * 2;
+    static constexpr int OFF_P = OFF_VP + 3 * TILE;  // [buffer][term]
+    static constexpr int OFF_BAR = OFF_P + 4 * P_TERM;
+    // full, empty [NST]; s1_full, s1_free, p_full [2]; vp_full, u_full, u_free,
+    // s_full, o1_done, o2_done, o_free, drain
+    static constexpr int N_BAR = 2 * NST + 6 + 8;
+    static constexpr int OFF_F = OFF_BAR + N_BAR * 8;  // scale l^(i+1)
+    static constexpr int OFF_MISC = OFF_F + C * 4;     // TMEM slot, fail flag
+    static constexpr int SMEM = OFF_MISC + 16 + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static constexpr int TMEM_COLS = 512;
+    static constexpr int U = 0, S = D, S1 = 2 * D, O2 = S1 + 2 * C, O1 = O2 + C;
+    static_assert(O1 + C <= TMEM_COLS, "tensor memory");
+    static constexpr int LANE_WARPS = D / 32;  // warps of a group whose lanes mean something
+};
+
+// A CTA's work: tokens [t0, t0 + n) of head h; the state before them and where the
+// state behind them goes (NULL: nothing, nowhere).
+struct Work {
+    int t0, n, h;
+    const float *from;
+    float *to;
+};
+
+// Segments of a request.
+__device__ __forceinline__ int segments(const ChunkParams &a, const Request &x) {
+    return x.state < 0 ? 0 : a.seg ? (x.n + a.seg - 1) / a.seg : 1;
+}
+
+// The request that owns segment `slot`, and the slot of its first one; false if none
+// does.  Whole warp, the same for all.
+__device__ __forceinline__ bool find_request(const ChunkParams &a, int slot, int *r, int *first) {
+    const int lane = threadIdx.x & 31;
+    int carry = 0;
+    for (int r0 = 0; r0 < a.p.R; r0 += 32) {
+        const int ns = r0 + lane < a.p.R ? segments(a, pa::lin::request(a.p, r0 + lane)) : 0;
+        int incl = ns;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(pa::kFull, incl, o);
+            if (lane >= o) incl += y;
+        }
+        const int f = carry + incl - ns;
+        const unsigned mine = __ballot_sync(pa::kFull, slot >= f && slot < f + ns && f + ns <= a.slots);
+        if (mine) {
+            const int src = __ffs(mine) - 1;
+            *r = r0 + src;
+            *first = __shfl_sync(pa::kFull, f, src);
+            return true;
+        }
+        carry += __shfl_sync(pa::kFull, incl, 31);
+    }
+    return false;
+}
+
+template <int D, bool SUM>
+__device__ __forceinline__ Work find_work(const ChunkParams &a) {
+    Work w{0, 0, 0, nullptr, nullptr};
+    const int slot = blockIdx.x / a.p.H;
+    w.h = blockIdx.x % a.p.H;
+    int r = slot, first = 0;
+    if (a.seg && !find_request(a, slot, &r, &first)) return w;
+    const Request x = pa::lin::request(a.p, r);
+    if (x.state < 0) return w;
+    constexpr int64_t DD = D * D;
+    float *pool = a.p.states + (static_cast<int64_t>(x.state) * a.p.H + w.h) * DD;
+    float *own = a.ws + (static_cast<int64_t>(slot) * a.p.H + w.h) * DD;
+    if (!a.seg) {
+        w.t0 = x.t0;
+        w.n = x.n;
+        w.from = x.held ? pool : nullptr;
+        w.to = pool;
+        return w;
+    }
+    const int s = slot - first;
+    const bool last = s == segments(a, x) - 1;
+    if (SUM && last) return w;  // (the state behind the last segment comes from its own run)
+    w.t0 = x.t0 + s * a.seg;
+    w.n = min(a.seg, x.n - s * a.seg);
+    w.from = SUM ? nullptr : own;
+    w.to = SUM ? own : last ? pool : nullptr;
+    return w;
+}
+
+// x as two or three bf16 terms, two values at a time
+__device__ __forceinline__ uint32_t take_bf16(float2 &x) {
+    const uint32_t t = pack_bf16(x.x, x.y);
+    x = pa::ffma2(pa::bf16x2_to_float2(t), make_float2(-1.f, -1.f), x);
+    return t;
+}
+
+template <int D, bool SUM>
+__global__ void __launch_bounds__(Lay<D>::THREADS, 1)
+    chunk_kernel(const ChunkParams a, const __grid_constant__ CUtensorMap qmap,
+                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using L = Lay<D>;
+    constexpr int NST = L::NST;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t s0 = pa::smem_u32(smem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
+    uint64_t *full = bars, *empty = full + NST, *s1_full = empty + NST, *s1_free = s1_full + 2,
+             *p_full = s1_free + 2, *vp_full = p_full + 2, *u_full = vp_full + 1, *u_free = u_full + 1,
+             *s_full = u_free + 1, *o1_done = s_full + 1, *o2_done = o1_done + 1, *o_free = o2_done + 1,
+             *drain = o_free + 1;
+    float *fdec = reinterpret_cast<float *>(smem + L::OFF_F);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
+    volatile int *fail = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // ---- set-up: barriers, TMEM ------------------------------------------------
+    if (tid == 0) {
+        for (const CUtensorMap *map : {&qmap, &kmap, &vmap})
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+        for (int i = 0; i < NST; ++i) {
+            pa::mbar_init(&full[i], 1);
+            pa::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            pa::mbar_init(&s1_full[i], 1);
+            pa::mbar_init(&s1_free[i], 2);
+            pa::mbar_init(&p_full[i], 2);
+        }
+        pa::mbar_init(vp_full, 4);
+        pa::mbar_init(u_full, 1);
+        pa::mbar_init(u_free, 2 * L::LANE_WARPS);
+        pa::mbar_init(s_full, 2 * L::LANE_WARPS);
+        pa::mbar_init(o1_done, 1);
+        pa::mbar_init(o2_done, 1);
+        pa::mbar_init(o_free, L::LANE_WARPS);
+        pa::mbar_init(drain, 1);
+        *fail = 0;
+        pa::fence_barrier_init();
+    }
+    if (warp == L::MMA_WARP) pa::tc::alloc(tslot, L::TMEM_COLS);
+    // launched as a programmatic dependent: the inputs are ready past this point
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Work w = find_work<D, SUM>(a);
+    const float g = pa::lin::log_decay(a.p, w.h), g2 = g * kLog2e;
+    if (tid < C) fdec[tid] = a.p.scale * exp2f(g2 * (tid + 1));
+    pa::tc::fence_before();
+    __syncthreads();
+    pa::tc::fence_after();
+    const uint32_t tmem = *tslot;
+    const int nc = (w.n + C - 1) / C;
+    int loads_issued = 0;
+    auto signal = [&](uint64_t *bar) {  // one arrival per warp, behind its writes
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+
+    if (warp == L::LOAD_WARP) {
+        // ---------------- loads ----------------
+        // Whole tiles of 64 tokens: rows past the work's tokens are other tokens' (or
+        // zeros past the last), see below.
+        constexpr int FIRST = SUM ? 1 : 0;  // (no q)
+        for (int c = 0; c < nc; ++c) {
+            const int st = c % NST;
+            if (c >= NST && !wait_all(&empty[st], ((c / NST) - 1) & 1)) {
+                *fail = 1;
+                break;
+            }
+            if (lane == 0) {
+                pa::mbar_arrive_expect_tx(&full[st], (3 - FIRST) * L::TILE);
+                ++loads_issued;
+#pragma unroll
+                for (int x = FIRST; x < 3; ++x)
+#pragma unroll
+                    for (int b = 0; b < D / 64; ++b)
+                        tma_load_3d(s0 + st * L::STAGE + x * L::TILE + b * (C * 128),
+                                    x == 0 ? &qmap : x == 1 ? &kmap : &vmap, b * 64, w.h, w.t0 + c * C,
+                                    &full[st]);
+            }
+            __syncwarp();
+        }
+    } else if (warp == L::MMA_WARP) {
+        // ---------------- MMA ----------------
+        constexpr uint32_t kIdS1 = pa::tc::idesc_bf16(128, C, 0, 0);  // Q K^T
+        constexpr uint32_t kIdU = pa::tc::idesc_bf16(128, D, 1, 1);   // V'^T K
+        constexpr uint32_t kIdO1 = pa::tc::idesc_bf16(128, C, 1, 0);  // V^T P^T
+        constexpr uint32_t kIdO2 = pa::tc::idesc_bf16(128, C, 0, 0);  // S^T Q^T
+        constexpr uint32_t kStage = L::STAGE >> 4, kTile = L::TILE >> 4;
+        // rows of 128 bytes, K-major; tokens as K (64 tokens per column block)
+        const uint64_t row_major = pa::tc::sdesc(s0, 16, 1024), col_major = pa::tc::sdesc(s0, C * 128, 1024);
+        auto issue_s1 = [&](int c) {
+            if (!wait_all(&full[c % NST], (c / NST) & 1)) return false;
+            if (c >= 2 && !wait_all(&s1_free[c & 1], ((c >> 1) - 1) & 1)) return false;
+            pa::tc::fence_after();
+            if (pa::tc::elect_one()) {
+                const uint64_t q = row_major + static_cast<uint32_t>((c % NST) * kStage), k = q + kTile;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = ((ks >> 2) * C * 128 + (ks & 3) * 32) >> 4;
+                    pa::tc::mma_ss(tmem + L::S1 + (c & 1) * C, q + off, k + off, kIdS1, ks > 0);
+                }
+                pa::tc::commit(&s1_full[c & 1]);
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = SUM || nc == 0 || issue_s1(0);
+        for (int c = 0; c < nc && ok; ++c) {
+            const uint32_t stage = static_cast<uint32_t>((c % NST) * kStage);
+            if (SUM) ok = wait_all(&full[c % NST], (c / NST) & 1);
+            ok = ok && wait_all(vp_full, c & 1) && (c == 0 || wait_all(u_free, (c - 1) & 1));
+            if (!ok) break;
+            pa::tc::fence_after();
+            if (pa::tc::elect_one()) {
+                const uint64_t k = col_major + stage + kTile, vp = col_major + (L::OFF_VP >> 4);
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks)
+#pragma unroll
+                    for (int term = 0; term < 3; ++term)
+                        pa::tc::mma_ss(tmem + L::U, vp + term * kTile + ((ks * 16 * 128) >> 4),
+                                       k + ((ks * 16 * 128) >> 4), kIdU, ks + term > 0);
+                pa::tc::commit(u_full);
+                if (SUM) pa::tc::commit(&empty[c % NST]);
+            }
+            __syncwarp();
+            if (SUM) continue;
+            if (c + 1 < nc) ok = issue_s1(c + 1);
+            ok = ok && wait_all(&p_full[c & 1], (c >> 1) & 1) && (c == 0 || wait_all(o_free, (c - 1) & 1));
+            if (!ok) break;
+            pa::tc::fence_after();
+            if (pa::tc::elect_one()) {
+                const uint64_t v = col_major + stage + 2 * kTile;
+                const uint64_t p = row_major + ((L::OFF_P + (c & 1) * 2 * L::P_TERM) >> 4);
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks)
+#pragma unroll
+                    for (int term = 0; term < 2; ++term)
+                        pa::tc::mma_ss(tmem + L::O1, v + ((ks * 16 * 128) >> 4),
+                                       p + ((term * L::P_TERM + ks * 32) >> 4), kIdO1, ks + term > 0);
+                pa::tc::commit(o1_done);
+            }
+            __syncwarp();
+            ok = wait_all(s_full, c & 1);
+            if (!ok) break;
+            pa::tc::fence_after();
+            if (pa::tc::elect_one()) {
+                const uint64_t q = row_major + stage;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                    for (int term = 0; term < 2; ++term)
+                        pa::tc::mma_ts(tmem + L::O2, tmem + L::S + term * (D / 2) + ks * 8,
+                                       q + (((ks >> 2) * C * 128 + (ks & 3) * 32) >> 4), kIdO2, ks + term > 0);
+                pa::tc::commit(o2_done);
+                pa::tc::commit(&empty[c % NST]);
+            }
+            __syncwarp();
+        }
+        if (!ok) *fail = 1;
+    } else if (warp < 8) {
+        // ---------------- the state ----------------
+        constexpr int HALF = D / 2;  // key dimensions of this warp group
+        const int k0 = warp < 4 ? 0 : HALF, dv = (warp & 3) * 32 + lane;
+        const uint32_t base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        if (dv < D) {
+            float s[HALF];
+#pragma unroll
+            for (int k = 0; k < HALF; ++k) s[k] = w.from ? w.from[(k0 + k) * D + dv] : 0.f;
+            auto give = [&]() {  // to the next Q S
+#pragma unroll
+                for (int k = 0; k < HALF; k += 16) {
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float2 x = make_float2(s[k + 2 * e], s[k + 2 * e + 1]);
+                        hi[e] = take_bf16(x);
+                        lo[e] = pack_bf16(x.x, x.y);
+                    }
+                    pa::tc::st8(base + L::S + (k0 + k) / 2, hi);
+                    pa::tc::st8(base + L::S + (D + k0 + k) / 2, lo);
+                }
+                pa::tc::wait_st();
+                pa::tc::fence_before();
+                signal(s_full);
+            };
+            if (!SUM && nc > 0) give();
+            const float em_full = expm1f(g * C);
+            bool ok = true;
+            for (int c = 0; c < nc; ++c) {
+                ok = wait_all(u_full, c & 1);
+                if (!ok) break;
+                pa::tc::fence_after();
+                // l^m S = S + (l^m - 1) S: as exact as its rounding where l is close to 1
+                const float em = c + 1 < nc ? em_full : expm1f(g * (w.n - c * C));
+#pragma unroll
+                for (int k = 0; k < HALF; k += 16) {
+                    uint32_t u[16];
+                    pa::tc::ld16(base + L::U + k0 + k, u);
+                    pa::tc::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) s[k + e] = fmaf(em, s[k + e], s[k + e]) + __uint_as_float(u[e]);
+                }
+                pa::tc::fence_before();
+                signal(u_free);
+                if (!SUM && c + 1 < nc) {
+                    ok = wait_all(o2_done, c & 1);  // the last Q S has read its state
+                    if (!ok) break;
+                    pa::tc::fence_after();
+                    give();
+                }
+            }
+            if (!ok) *fail = 1;
+            else if (w.to && nc > 0) {
+#pragma unroll
+                for (int k = 0; k < HALF; ++k) w.to[(k0 + k) * D + dv] = s[k];
+            }
+        }
+    } else if (warp < 12) {
+        // ---------------- V' ----------------
+        // 16 bytes at a time, at the same place of the tile: whatever the swizzle, byte
+        // x of a column block belongs to token x / 128.  A thread's tokens are t0 + 16 k.
+        const int id = tid - 8 * 32, tok = id >> 3;
+        float wt[4];
+        auto weights = [&](int m) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = tok + 16 * k;
+                wt[k] = j < m ? exp2f(g2 * (m - 1 - j)) : 0.f;
+            }
+        };
+        weights(C);
+        bool ok = true;
+        for (int c = 0; c < nc; ++c) {
+            const int m = min(C, w.n - c * C);
+            if (m < C) weights(m);
+            ok = wait_all(&full[c % NST], (c / NST) & 1) && (c == 0 || wait_all(u_full, (c - 1) & 1));
+            if (!ok) break;
+            const uint32_t kt = s0 + (c % NST) * L::STAGE + L::TILE, vt = kt + L::TILE;
+#pragma unroll
+            for (int b = 0; b < D / 64; ++b)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t off = b * (C * 128) + k * 2048 + id * 16;
+                    if (tok + 16 * k >= m) {
+                        // no token of this work: its V and K may hold anything, and
+                        // 0 x NaN is NaN
+                        for (const uint32_t at : {kt + off, vt + off, s0 + L::OFF_VP + off,
+                                                  s0 + L::OFF_VP + L::TILE + off, s0 + L::OFF_VP + 2 * L::TILE + off})
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0u) : "memory");
+                        continue;
+                    }
+                    const uint4 v = pa::lds128(vt + off);
+                    float2 x[4];
+                    pa::Elem<__nv_bfloat16>::unpack(v, x);
+                    uint32_t t[3][4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float2 y = __fmul2_rn(x[e], make_float2(wt[k], wt[k]));
+                        t[0][e] = take_bf16(y);
+                        t[1][e] = take_bf16(y);
+                        t[2][e] = pack_bf16(y.x, y.y);
+                    }
+#pragma unroll
+                    for (int term = 0; term < 3; ++term)
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(s0 + L::OFF_VP + term * L::TILE + off),
+                                     "r"(t[term][0]), "r"(t[term][1]), "r"(t[term][2]), "r"(t[term][3])
+                                     : "memory");
+                }
+            pa::fence_proxy_async();
+            signal(vp_full);
+        }
+        if (!ok) *fail = 1;
+    } else if (!SUM && warp < 12 + L::LANE_WARPS) {
+        // ---------------- P; outputs ----------------
+        const int lw = warp & 3, row = lw * 32 + lane;
+        const uint32_t base = tmem + (static_cast<uint32_t>(lw * 32) << 16);
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.p.out) +
+                             (static_cast<int64_t>(w.t0) * a.p.H + w.h) * D + row;
+        const int64_t step = static_cast<int64_t>(a.p.H) * D;
+        bool ok = true;
+        auto make_p = [&](int c) {  // row = token of the chunk (warps 12 and 13)
+            if (!wait_all(&s1_full[c & 1], (c >> 1) & 1)) return false;
+            pa::tc::fence_after();
+            const uint32_t to = s0 + L::OFF_P + (c & 1) * 2 * L::P_TERM + row * 128;
+#pragma unroll
+            for (int j0 = 0; j0 < C; j0 += 32) {
+                uint32_t u[32];
+                if (j0 <= lw * 32) {  // (else every token of it is later than the warp's)
+                    pa::tc::ld32(base + L::S1 + (c & 1) * C + j0, u);
+                    pa::tc::wait_ld();
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int j = j0 + e + 2 * y;
+                        float2 x;
+                        x.x = j <= row && j0 <= lw * 32 ? __uint_as_float(u[e + 2 * y]) * fast_exp2(g2 * (row - j)) : 0.f;
+                        x.y = j < row && j0 <= lw * 32 ? __uint_as_float(u[e + 2 * y + 1]) * fast_exp2(g2 * (row - j - 1)) : 0.f;
+                        hi[y] = take_bf16(x);
+                        lo[y] = pack_bf16(x.x, x.y);
+                    }
+                    const uint32_t at = to + ((((j0 + e) >> 3) ^ (row & 7)) << 4);
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]),
+                                 "r"(hi[3])
+                                 : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + L::P_TERM), "r"(lo[0]), "r"(lo[1]),
+                                 "r"(lo[2]), "r"(lo[3])
+                                 : "memory");
+                }
+            }
+            pa::tc::fence_before();
+            signal(&s1_free[c & 1]);
+            pa::fence_proxy_async();
+            signal(&p_full[c & 1]);
+            return true;
+        };
+        auto put_o = [&](int c) {  // row = value dimension
+            if (!wait_all(o1_done, c & 1) || !wait_all(o2_done, c & 1)) return false;
+            pa::tc::fence_after();
+            const int m = min(C, w.n - c * C);
+            __nv_bfloat16 *dst = out + static_cast<int64_t>(c) * C * step;
+#pragma unroll 1
+            for (int i0 = 0; i0 < C; i0 += 32) {
+                uint32_t x1[32], x2[32];
+                pa::tc::ld32(base + L::O1 + i0, x1);
+                pa::tc::ld32(base + L::O2 + i0, x2);
+                pa::tc::wait_ld();
+                if (i0 + 32 == C) {
+                    pa::tc::fence_before();
+                    signal(o_free);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (i0 + e < m)
+                        dst[(i0 + e) * step] = __float2bfloat16_rn(
+                            fmaf(fdec[i0 + e], __uint_as_float(x2[e]), a.p.scale * __uint_as_float(x1[e])));
+            }
+            return true;
+        };
+        for (int c = 0; c < nc && ok; ++c) {
+            if (lw < 2) ok = make_p(c);
+            if (ok && c > 0) ok = put_o(c - 1);
+        }
+        if (ok && nc > 0) ok = put_o(nc - 1);
+        if (!ok) *fail = 1;
+    }
+
+    // ---- tear-down ----------------------------------------------------------------
+    pa::tc::fence_before();
+    __syncthreads();
+    if (*fail) {
+        // a wait ran out: record it, then let the MMAs and the copies in flight land
+        // (bounded) before TMEM and shared memory go away
+        if (tid == 0) pa::record_error(a.p.err, PA_DEVERR_TIMEOUT);
+        if (warp == L::MMA_WARP) {
+            if (pa::tc::elect_one()) pa::tc::commit(drain);
+            __syncwarp();
+            (void)pa::mbar_wait(drain, 0);
+        }
+        if (warp == L::LOAD_WARP && lane == 0)
+            for (int st = 0; st < NST && st < loads_issued; ++st) {
+                const int last = st + NST * ((loads_issued - 1 - st) / NST);
+                (void)pa::mbar_wait(&full[st], (last / NST) & 1);
+            }
+        pa::tc::fence_before();
+        __syncthreads();
+    }
+    if (warp == L::MMA_WARP) {
+        pa::tc::fence_after();
+        pa::tc::dealloc(tmem, L::TMEM_COLS);
+    }
+}
+
+// The states before each segment from the segments' own sums, four elements of one
+// (request, head) per thread; `ws` holds the former afterwards.
+template <int D>
+__global__ void __launch_bounds__(256) chain_kernel(const ChunkParams a) {
+    constexpr int PER = D * D / 4 / 256;  // CTAs per (request, head)
+    const int x = blockIdx.x / PER, r = x / a.p.H, h = x % a.p.H;
+    const int e = (blockIdx.x % PER) * 256 + threadIdx.x;  // of 16 bytes
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Request q = pa::lin::request(a.p, r);
+    // the segments of the requests before this one
+    __shared__ int before;
+    if (threadIdx.x == 0) before = 0;
+    __syncthreads();
+    int mine = 0;
+    for (int i = threadIdx.x; i < r; i += 256) mine += segments(a, pa::lin::request(a.p, i));
+    if (mine) atomicAdd(&before, mine);
+    __syncthreads();
+    const int ns = segments(a, q);
+    if (ns == 0) return;
+    if (before + ns > a.slots) {  // (the requests' rows overlap: the others run)
+        if (threadIdx.x == 0) pa::record_error(a.p.err, PA_DEVERR_BAD_REQUEST);
+        return;
+    }
+    constexpr int64_t DD4 = D * D / 4;
+    const float em = expm1f(pa::lin::log_decay(a.p, h) * a.seg);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (q.held) s = reinterpret_cast<const float4 *>(a.p.states)[(static_cast<int64_t>(q.state) * a.p.H + h) * DD4 + e];
+    float4 *at = reinterpret_cast<float4 *>(a.ws) + (static_cast<int64_t>(before) * a.p.H + h) * DD4 + e;
+    const int64_t step = a.p.H * DD4;
+    constexpr int AHEAD = 4;  // sums requested before they are needed
+    for (int i0 = 0; i0 < ns; i0 += AHEAD) {
+        float4 u[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (i0 + k < ns - 1) u[k] = at[(i0 + k) * step];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            if (i0 + k >= ns) break;
+            at[(i0 + k) * step] = s;
+            if (i0 + k == ns - 1) break;
+            s.x = fmaf(em, s.x, s.x) + u[k].x;
+            s.y = fmaf(em, s.y, s.y) + u[k].y;
+            s.z = fmaf(em, s.z, s.z) + u[k].z;
+            s.w = fmaf(em, s.w, s.w) + u[k].w;
+        }
+    }
+}
+
+template <typename K, typename... Args>
+int go(K kern, int64_t ctas, int threads, size_t smem, cudaStream_t stream, Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    (void)cudaGetLastError();  // drop a stale error that is not ours
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e != cudaSuccess) return pa::cuda_fail(e, "linear_prefill launch");
+    return pa::check_launch("linear_prefill launch");
+}
+
+template <int D>
+int launch(const ChunkParams &a, cudaStream_t stream) {
+    using L = Lay<D>;
+    static std::atomic<uint64_t> done{0}, done_sum{0};
+    if (int rc = set_smem_once(chunk_kernel<D, false>, L::SMEM, &done)) return rc;
+    if (int rc = set_smem_once(chunk_kernel<D, true>, L::SMEM, &done_sum)) return rc;
+    CUtensorMap q, k, v;
+    if (int rc = pa::encode_rows_map(&q, a.p.q, a.p.T, a.p.q_stride, a.p.H, D, C)) return rc;
+    if (int rc = pa::encode_rows_map(&k, a.p.k, a.p.T, a.p.k_stride, a.p.H, D, C)) return rc;
+    if (int rc = pa::encode_rows_map(&v, a.p.v, a.p.T, a.p.v_stride, a.p.H, D, C)) return rc;
+    const int64_t ctas = int64_t(a.seg ? a.slots : a.p.R) * a.p.H;
+    if (a.seg) {
+        if (int rc = go(chunk_kernel<D, true>, ctas, L::THREADS, L::SMEM, stream, a, q, k, v)) return rc;
+        if (int rc = go(chain_kernel<D>, int64_t(a.p.R) * a.p.H * (D * D / 4 / 256), 256, 0, stream, a)) return rc;
+    }
+    return go(chunk_kernel<D, false>, ctas, L::THREADS, L::SMEM, stream, a, q, k, v);
+}
+
+}  // namespace
+
+namespace pa {
+namespace lin {
+
+Segments segments_for(int R, int T, int max_query_len, int H) {
+    Segments s{0, 0};
+    constexpr int kSMs = 152;
+    const int64_t pairs = int64_t(R) * H;
+    if (pairs >= 2 * kSMs || max_query_len < 16 * C) return s;
+    // (to be measured)
+    s.tokens = 1024;
+    s.slots = static_cast<int>(int64_t(T) / s.tokens + R);
+    return s;
+}
+
+int launch_chunks(const LinParams &p, int D, float *ws, const Segments &s, cudaStream_t stream) {
+    const ChunkParams a{p, ws, s.tokens, s.slots};
+    return D == 128 ? launch<128>(a, stream) : launch<64>(a, stream);
+}
+
+}  // namespace lin
+}  // namespace pa

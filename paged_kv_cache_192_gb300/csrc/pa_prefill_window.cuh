@@ -98,15 +98,6 @@ struct Item {
     }
 };
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                            int z, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(pa::smem_u32(bar))
-        : "memory");
-}
-
 // The requests of a launch and the prefix sum of their query tiles of `qtok`
 // tokens into the tables; returns the number of tiles.  A request whose numbers
 // do not fit gets none.  Whole CTA of 12 warps; ends with a barrier.
@@ -376,10 +367,6 @@ __device__ __forceinline__ void mma_pv(uint32_t o_col, uint32_t p_col, uint64_t 
         pa::tc::mma_ts(o_col, p_col + ks * 8, b, kIdO, ks == 0 ? accumulate : 1);
         pa::tc::mma_ts(o_col, p_col + 32 + ks * 8, b, kIdO, 1);
     }
-}
-
-__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity) {
-    return __all_sync(pa::kFull, pa::mbar_wait(bar, parity));
 }
 
 template <int D, int GQ, bool CROSS>

@@ -75,13 +75,13 @@ class Linear:
             at += n
         return out, states, oa, ob, sa, sb
 
-    def check(self, out, states=None, scale=None, terms=0.0):
+    def check(self, out, states=None, scale=None, terms=(0.0, 0.0)):
         """Bounds.  A term of a state that is `age` tokens old has been multiplied by the
         decay `age` times: a factor in 32 bits (off by 2^-22: 2 ulp of exp2, and its
         argument) and a rounding (2^-24) each, after its own product's; sums of D
         terms in any order add D 2^-24 of their amounts.  `terms`: what else a term
-        may be off by (a kernel that takes products of 16-bit terms).  An output is
-        rounded to its type by half a step."""
+        of an output, and of a state, may be off by (a kernel that takes products of
+        16-bit terms).  An output is rounded to its type by half a step."""
         ref, rs, oa, ob, sa, sb = self.reference(scale)
         e, age = 2.0 ** -23, 2.0 ** -22 + 2.0 ** -24
         states = self.states if states is None else states
@@ -96,13 +96,13 @@ class Linear:
         got = states[t].double()
         assert torch.isfinite(got).all()
         err = (got - rs[t]).abs()
-        tol = (2 * e + 2.0 ** -24 * 16 + terms) * sa[t] + age * sb[t]
+        tol = (2 * e + 2.0 ** -24 * 16 + terms[1]) * sa[t] + age * sb[t]
         assert bool((err <= tol).all()), f"states: {(err / tol.clamp(min=1e-300)).max():.3f} of the bound"
         inside = ~torch.isnan(ref[:, 0, 0])
         got, ref, oa, ob = out[inside].double(), ref[inside], oa[inside], ob[inside]
         assert torch.isfinite(got).all(), "something that no token sees entered the result"
         err = (got - ref).abs()
-        tol = torch.finfo(self.dtype).eps / 2 * ref.abs() + ((self.d + 20) * 2.0 ** -24 + terms) * oa + age * ob
+        tol = torch.finfo(self.dtype).eps / 2 * ref.abs() + ((self.d + 20) * 2.0 ** -24 + terms[0]) * oa + age * ob
         worst = float((err / tol.clamp(min=1e-300)).max()) if err.numel() else 0.0
         assert worst <= 1, f"outputs: {worst:.3f} of the bound"
         return worst
