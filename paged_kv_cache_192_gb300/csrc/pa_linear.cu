@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(256) recurrent_kernel(const LinParams p) {
     for (int i = 0; i < NR; ++i)
         s[i] = x.held ? *reinterpret_cast<const float4 *>(S + (row0 + i * RG) * D) : make_float4(0.f, 0.f, 0.f, 0.f);
     // l S = S + (l - 1) S: as exact as its rounding where l is close to 1 and a state
-    // lives long
+    // lives long (and before k v is added, of which S may be many times larger)
     const float lm1 = expm1f(pa::lin::log_decay(p, h));
     auto stage = [&](int t) {
         const int64_t tok = x.t0 + t;
@@ -81,10 +81,10 @@ __global__ void __launch_bounds__(256) recurrent_kernel(const LinParams p) {
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             const float ki = sk[b][row0 + i * RG], qi = sq[b][row0 + i * RG];
-            s[i].x = fmaf(lm1, s[i].x, fmaf(ki, vv.x, s[i].x));
-            s[i].y = fmaf(lm1, s[i].y, fmaf(ki, vv.y, s[i].y));
-            s[i].z = fmaf(lm1, s[i].z, fmaf(ki, vv.z, s[i].z));
-            s[i].w = fmaf(lm1, s[i].w, fmaf(ki, vv.w, s[i].w));
+            s[i].x = fmaf(ki, vv.x, fmaf(lm1, s[i].x, s[i].x));
+            s[i].y = fmaf(ki, vv.y, fmaf(lm1, s[i].y, s[i].y));
+            s[i].z = fmaf(ki, vv.z, fmaf(lm1, s[i].z, s[i].z));
+            s[i].w = fmaf(ki, vv.w, fmaf(lm1, s[i].w, s[i].w));
             o.x = fmaf(qi, s[i].x, o.x);
             o.y = fmaf(qi, s[i].y, o.y);
             o.z = fmaf(qi, s[i].z, o.z);

@@ -12,10 +12,14 @@
 // issue slots.  Hence one CTA per (request, head) with a warp group for each job:
 //   warps 0-3, 4-7  the state, in registers in fp32 (thread = value dimension, half of
 //                   the key dimensions each): adds a chunk's K^T V' to it and gives
-//                   it to the next chunk's Q S as two bf16 terms in TMEM
-//   warps 8-11      V' = l^(C-1-j) v_j as three bf16 terms in shared memory
-//   warps 12-15     P as two bf16 terms in shared memory (12, 13), outputs
-//   warp 16         loads (TMA); warp 17 issues the tcgen05.mma
+//                   it to the next chunk's Q S as two bf16 terms in TMEM; in between,
+//                   0, 1, 4 and 5 write P as two bf16 terms to shared memory
+//   warp 8          issues the tcgen05.mma
+//   warps 9-11      V' = l^(C-1-j) v_j as three bf16 terms in shared memory, 32 tokens at
+//                   a time (the other 32 are in use meanwhile)
+//   warps 12-15     outputs, through the place of the chunk's q to a TMA store, whose
+//                   issuer (15) then has the chunk after the ring's loaded there; without
+//                   outputs V' too
 // Outputs are computed transposed (lanes = value dimensions, columns = tokens), so the
 // state is an operand that lies in TMEM, where the threads that own it write it;
 // with tokens as lanes it would take 64 KB of shared memory.  Q K^T has its tokens
@@ -51,8 +55,8 @@ struct ChunkParams {
 
 template <int D>
 struct Lay {
-    static constexpr int THREADS = 18 * 32;
-    static constexpr int LOAD_WARP = 16, MMA_WARP = 17;
+    static constexpr int THREADS = 16 * 32;  // 128 registers each
+    static constexpr int MMA_WARP = 8, LOAD_WARP = 15;
     static constexpr int NST = D == 128 ? 3 : 4;
     static constexpr int TILE = C * D * 2;       // a chunk's q, k or v
     static constexpr int STAGE = 3 * TILE;       // q, k, v
@@ -60,11 +64,13 @@ struct Lay {
     static constexpr int P_TERM = C * C * 2;
     static constexpr int OFF_P = OFF_VP + 3 * TILE;  // [buffer][term]
     static constexpr int OFF_BAR = OFF_P + 4 * P_TERM;
-    // full, empty [NST]; s1_full, s1_free, p_full [2]; vp_full, u_full, u_free,
-    // s_full, o1_done, o2_done, o_free, drain
-    static constexpr int N_BAR = 2 * NST + 6 + 8;
+    // full, empty (without outputs only) [NST]; s1_full, s1_free, p_full, vp_full [2];
+    // u_half, u_full, u_free, s_full, o1_done, o2_done, o_free, drain
+    static constexpr int N_BAR = 2 * NST + 8 + 8;
     static constexpr int OFF_F = OFF_BAR + N_BAR * 8;  // scale l^(i+1)
-    static constexpr int OFF_MISC = OFF_F + C * 4;     // TMEM slot, fail flag
+    static constexpr int OFF_W = OFF_F + C * 4;        // l^(C-1-j), and of the last chunk
+    static constexpr int OFF_D = OFF_W + 2 * C * 4;    // l^x, x = 1 - C .. C - 1 (1 below 0)
+    static constexpr int OFF_MISC = OFF_D + 2 * C * 4; // TMEM slot, fail flag
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static constexpr int TMEM_COLS = 512;
@@ -151,7 +157,8 @@ __device__ __forceinline__ uint32_t take_bf16(float2 &x) {
 template <int D, bool SUM>
 __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
     chunk_kernel(const ChunkParams a, const __grid_constant__ CUtensorMap qmap,
-                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                 const __grid_constant__ CUtensorMap omap) {
     using L = Lay<D>;
     constexpr int NST = L::NST;
     extern __shared__ uint8_t smem_raw[];
@@ -160,17 +167,18 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
     const uint32_t s0 = pa::smem_u32(smem);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
     uint64_t *full = bars, *empty = full + NST, *s1_full = empty + NST, *s1_free = s1_full + 2,
-             *p_full = s1_free + 2, *vp_full = p_full + 2, *u_full = vp_full + 1, *u_free = u_full + 1,
+             *p_full = s1_free + 2, *vp_full = p_full + 2, *u_half = vp_full + 2, *u_full = u_half + 1, *u_free = u_full + 1,
              *s_full = u_free + 1, *o1_done = s_full + 1, *o2_done = o1_done + 1, *o_free = o2_done + 1,
              *drain = o_free + 1;
-    float *fdec = reinterpret_cast<float *>(smem + L::OFF_F);
+    float *fdec = reinterpret_cast<float *>(smem + L::OFF_F), *wdec = reinterpret_cast<float *>(smem + L::OFF_W),
+          *pdec = reinterpret_cast<float *>(smem + L::OFF_D) + C;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *fail = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     // ---- set-up: barriers, TMEM ------------------------------------------------
     if (tid == 0) {
-        for (const CUtensorMap *map : {&qmap, &kmap, &vmap})
+        for (const CUtensorMap *map : {&qmap, &kmap, &vmap, &omap})
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
         for (int i = 0; i < NST; ++i) {
             pa::mbar_init(&full[i], 1);
@@ -178,10 +186,11 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             pa::mbar_init(&s1_full[i], 1);
-            pa::mbar_init(&s1_free[i], 2);
-            pa::mbar_init(&p_full[i], 2);
+            pa::mbar_init(&s1_free[i], 4);
+            pa::mbar_init(&p_full[i], 4);
+            pa::mbar_init(&vp_full[i], SUM ? 6 : 3);
         }
-        pa::mbar_init(vp_full, 4);
+        pa::mbar_init(u_half, 1);
         pa::mbar_init(u_full, 1);
         pa::mbar_init(u_free, 2 * L::LANE_WARPS);
         pa::mbar_init(s_full, 2 * L::LANE_WARPS);
@@ -193,48 +202,57 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         pa::fence_barrier_init();
     }
     if (warp == L::MMA_WARP) pa::tc::alloc(tslot, L::TMEM_COLS);
+    // P of the first 32 tokens and the last 32: always 0 (both buffers and terms)
+    for (int x = tid; x < 4 * 32 * 4; x += L::THREADS) {
+        const int i = x >> 2 & 31;
+        *reinterpret_cast<uint4 *>(smem + L::OFF_P + (x >> 7) * L::P_TERM + i * 128 + (((x & 3) + 4) ^ (i & 7)) * 16) =
+            make_uint4(0, 0, 0, 0);
+    }
+    pa::fence_proxy_async();
     // launched as a programmatic dependent: the inputs are ready past this point
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Work w = find_work<D, SUM>(a);
     const float g = pa::lin::log_decay(a.p, w.h), g2 = g * kLog2e;
-    if (tid < C) fdec[tid] = a.p.scale * exp2f(g2 * (tid + 1));
+    const int nc = (w.n + C - 1) / C, rest = w.n - (nc - 1) * C;  // chunks, tokens of the last
+    if (tid < C) {
+        fdec[tid] = a.p.scale * exp2f(g2 * (tid + 1));
+        wdec[tid] = exp2f(g2 * (C - 1 - tid));
+        pdec[tid] = exp2f(g2 * tid);
+        pdec[tid - C] = 1.f;
+        wdec[C + tid] = tid < rest ? exp2f(g2 * (rest - 1 - tid)) : 0.f;
+    }
     pa::tc::fence_before();
     __syncthreads();
     pa::tc::fence_after();
     const uint32_t tmem = *tslot;
-    const int nc = (w.n + C - 1) / C;
     int loads_issued = 0;
     auto signal = [&](uint64_t *bar) {  // one arrival per warp, behind its writes
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
 
-    if (warp == L::LOAD_WARP) {
-        // ---------------- loads ----------------
-        // Whole tiles of 64 tokens: rows past the work's tokens are other tokens' (or
-        // zeros past the last), see below.
+    // Copies of chunk c into its stage (warp 15).  Whole tiles of 64 tokens: rows past the
+    // work's tokens are other tokens' (or zeros past the last), see below.
+    auto load = [&](int c) {
         constexpr int FIRST = SUM ? 1 : 0;  // (no q)
-        for (int c = 0; c < nc; ++c) {
-            const int st = c % NST;
-            if (c >= NST && !wait_all(&empty[st], ((c / NST) - 1) & 1)) {
-                *fail = 1;
-                break;
-            }
-            if (lane == 0) {
-                pa::mbar_arrive_expect_tx(&full[st], (3 - FIRST) * L::TILE);
-                ++loads_issued;
+        const int st = c % NST;
+        if (lane == 0) {
+            pa::mbar_arrive_expect_tx(&full[st], (3 - FIRST) * L::TILE);
+            ++loads_issued;
 #pragma unroll
-                for (int x = FIRST; x < 3; ++x)
+            for (int x = FIRST; x < 3; ++x)
 #pragma unroll
-                    for (int b = 0; b < D / 64; ++b)
-                        tma_load_3d(s0 + st * L::STAGE + x * L::TILE + b * (C * 128),
-                                    x == 0 ? &qmap : x == 1 ? &kmap : &vmap, b * 64, w.h, w.t0 + c * C,
-                                    &full[st]);
-            }
-            __syncwarp();
+                for (int b = 0; b < D / 64; ++b)
+                    tma_load_3d(s0 + st * L::STAGE + x * L::TILE + b * (C * 128),
+                                x == 0 ? &qmap : x == 1 ? &kmap : &vmap, b * 64, w.h, w.t0 + c * C, &full[st]);
         }
-    } else if (warp == L::MMA_WARP) {
+        __syncwarp();
+    };
+    if (warp == L::LOAD_WARP)
+        for (int c = 0; c < min(nc, NST); ++c) load(c);
+
+    if (warp == L::MMA_WARP) {
         // ---------------- MMA ----------------
         constexpr uint32_t kIdS1 = pa::tc::idesc_bf16(128, C, 0, 0);  // Q K^T
         constexpr uint32_t kIdU = pa::tc::idesc_bf16(128, D, 1, 1);   // V'^T K
@@ -263,21 +281,26 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         for (int c = 0; c < nc && ok; ++c) {
             const uint32_t stage = static_cast<uint32_t>((c % NST) * kStage);
             if (SUM) ok = wait_all(&full[c % NST], (c / NST) & 1);
-            ok = ok && wait_all(vp_full, c & 1) && (c == 0 || wait_all(u_free, (c - 1) & 1));
-            if (!ok) break;
-            pa::tc::fence_after();
-            if (pa::tc::elect_one()) {
-                const uint64_t k = col_major + stage + kTile, vp = col_major + (L::OFF_VP >> 4);
+            if (c > 0) ok = ok && wait_all(u_free, (c - 1) & 1);
 #pragma unroll
-                for (int ks = 0; ks < C / 16; ++ks)
+            for (int half = 0; half < 2; ++half) {
+                ok = ok && wait_all(&vp_full[half], c & 1);
+                if (!ok) break;
+                pa::tc::fence_after();
+                if (pa::tc::elect_one()) {
+                    const uint64_t k = col_major + stage + kTile, vp = col_major + (L::OFF_VP >> 4);
 #pragma unroll
-                    for (int term = 0; term < 3; ++term)
-                        pa::tc::mma_ss(tmem + L::U, vp + term * kTile + ((ks * 16 * 128) >> 4),
-                                       k + ((ks * 16 * 128) >> 4), kIdU, ks + term > 0);
-                pa::tc::commit(u_full);
-                if (SUM) pa::tc::commit(&empty[c % NST]);
+                    for (int ks = half * C / 32; ks < (half + 1) * C / 32; ++ks)
+#pragma unroll
+                        for (int term = 0; term < 3; ++term)
+                            pa::tc::mma_ss(tmem + L::U, vp + term * kTile + ((ks * 16 * 128) >> 4),
+                                           k + ((ks * 16 * 128) >> 4), kIdU, ks + term > 0);
+                    pa::tc::commit(half ? u_full : u_half);
+                    if (SUM && half) pa::tc::commit(&empty[c % NST]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            if (!ok) break;
             if (SUM) continue;
             if (c + 1 < nc) ok = issue_s1(c + 1);
             ok = ok && wait_all(&p_full[c & 1], (c >> 1) & 1) && (c == 0 || wait_all(o_free, (c - 1) & 1));
@@ -307,7 +330,6 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                         pa::tc::mma_ts(tmem + L::O2, tmem + L::S + term * (D / 2) + ks * 8,
                                        q + (((ks >> 2) * C * 128 + (ks & 3) * 32) >> 4), kIdO2, ks + term > 0);
                 pa::tc::commit(o2_done);
-                pa::tc::commit(&empty[c % NST]);
             }
             __syncwarp();
         }
@@ -318,47 +340,102 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         const int k0 = warp < 4 ? 0 : HALF, dv = (warp & 3) * 32 + lane;
         const uint32_t base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         if (dv < D) {
-            float s[HALF];
+            float2 s[HALF / 2];
 #pragma unroll
-            for (int k = 0; k < HALF; ++k) s[k] = w.from ? w.from[(k0 + k) * D + dv] : 0.f;
+            for (int k = 0; k < HALF; k += 2)
+                s[k / 2] = w.from ? make_float2(w.from[(k0 + k) * D + dv], w.from[(k0 + k + 1) * D + dv])
+                                  : make_float2(0.f, 0.f);
             auto give = [&]() {  // to the next Q S
 #pragma unroll
-                for (int k = 0; k < HALF; k += 16) {
+                for (int k = 0; k < HALF / 2; k += 8) {
                     uint32_t hi[8], lo[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        float2 x = make_float2(s[k + 2 * e], s[k + 2 * e + 1]);
+                        // (not before the wait ahead of this: state and terms together
+                        // are more than a thread's registers)
+                        asm volatile("" : "+f"(s[k + e].x), "+f"(s[k + e].y));
+                        float2 x = s[k + e];
                         hi[e] = take_bf16(x);
                         lo[e] = pack_bf16(x.x, x.y);
                     }
-                    pa::tc::st8(base + L::S + (k0 + k) / 2, hi);
-                    pa::tc::st8(base + L::S + (D + k0 + k) / 2, lo);
+                    pa::tc::st8(base + L::S + k0 / 2 + k, hi);
+                    pa::tc::st8(base + L::S + (D + k0) / 2 + k, lo);
                 }
                 pa::tc::wait_st();
                 pa::tc::fence_before();
                 signal(s_full);
             };
-            if (!SUM && nc > 0) give();
-            const float em_full = expm1f(g * C);
+            // P of chunk c: lane = token i of the chunk, columns j.  Warps 0 and 4 have rows
+            // 0-31, whose columns from 32 on are 0 (and stay so), 1 and 5 rows 32-63.
+            const int lw = warp & 3, row = lw * 32 + lane, j_step = (lw + 1) * 16;
+            auto make_p = [&](int c) {
+                if (!wait_all(&s1_full[c & 1], (c >> 1) & 1)) return false;
+                pa::tc::fence_after();
+                const uint32_t to = s0 + L::OFF_P + (c & 1) * 2 * L::P_TERM + row * 128;
+#pragma unroll 1
+                for (int j0 = (warp >> 2) * j_step; j0 < ((warp >> 2) + 1) * j_step; j0 += 16) {
+                    uint32_t hi[8], lo[8], u[16];
+                    pa::tc::ld16(base + L::S1 + (c & 1) * C + j0, u);
+                    const float *f = pdec + (row - j0);  // l^(row - j): neighbours in neighbouring lanes
+                    float2 x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = make_float2(f[-2 * e], f[-2 * e - 1]);
+                    pa::tc::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        // (a score of a later token may be anything, also NaN)
+                        x[e].x = j0 + 2 * e <= row ? x[e].x * __uint_as_float(u[2 * e]) : 0.f;
+                        x[e].y = j0 + 2 * e < row ? x[e].y * __uint_as_float(u[2 * e + 1]) : 0.f;
+                        hi[e] = take_bf16(x[e]);
+                        lo[e] = pack_bf16(x[e].x, x[e].y);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) {
+                        const uint32_t at = to + ((((j0 + 2 * e) >> 3) ^ (row & 7)) << 4);
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi[e]), "r"(hi[e + 1]),
+                                     "r"(hi[e + 2]), "r"(hi[e + 3])
+                                     : "memory");
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + L::P_TERM), "r"(lo[e]),
+                                     "r"(lo[e + 1]), "r"(lo[e + 2]), "r"(lo[e + 3])
+                                     : "memory");
+                    }
+                }
+                pa::tc::fence_before();
+                signal(&s1_free[c & 1]);
+                pa::fence_proxy_async();
+                signal(&p_full[c & 1]);
+                return true;
+            };
             bool ok = true;
-            for (int c = 0; c < nc; ++c) {
+            if (!SUM && nc > 0) {
+                give();
+                if (lw < 2) ok = make_p(0);
+            }
+            const float em_full = expm1f(g * C), em_rest = expm1f(g * rest);
+            for (int c = 0; c < nc && ok; ++c) {
                 ok = wait_all(u_full, c & 1);
                 if (!ok) break;
                 pa::tc::fence_after();
-                // l^m S = S + (l^m - 1) S: as exact as its rounding where l is close to 1
-                const float em = c + 1 < nc ? em_full : expm1f(g * (w.n - c * C));
+                // l^m S = S + (l^m - 1) S: as exact as its rounding where l is close to 1, and
+                // before anything is added, of which S may be many times larger
+                const float em = c + 1 < nc ? em_full : em_rest;
+                const float2 em2 = make_float2(em, em);
 #pragma unroll
-                for (int k = 0; k < HALF; k += 16) {
+                for (int k = 0; k < HALF / 2; k += 8) {
                     uint32_t u[16];
-                    pa::tc::ld16(base + L::U + k0 + k, u);
+                    pa::tc::ld16(base + L::U + k0 + 2 * k, u);
                     pa::tc::wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) s[k + e] = fmaf(em, s[k + e], s[k + e]) + __uint_as_float(u[e]);
+                    for (int e = 0; e < 8; ++e)
+                        s[k + e] = __fadd2_rn(pa::ffma2(em2, s[k + e], s[k + e]),
+                                              make_float2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1])));
                 }
                 pa::tc::fence_before();
                 signal(u_free);
                 if (!SUM && c + 1 < nc) {
-                    ok = wait_all(o2_done, c & 1);  // the last Q S has read its state
+                    // (the place of this P was read before the last Q S)
+                    if (lw < 2) ok = make_p(c + 1);
+                    ok = ok && wait_all(o2_done, c & 1);  // the last Q S has read its state
                     if (!ok) break;
                     pa::tc::fence_after();
                     give();
@@ -367,138 +444,173 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
             if (!ok) *fail = 1;
             else if (w.to && nc > 0) {
 #pragma unroll
-                for (int k = 0; k < HALF; ++k) w.to[(k0 + k) * D + dv] = s[k];
+                for (int k = 0; k < HALF; k += 2) {
+                    w.to[(k0 + k) * D + dv] = s[k / 2].x;
+                    w.to[(k0 + k + 1) * D + dv] = s[k / 2].y;
+                }
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < (SUM ? 15 : 12)) {
         // ---------------- V' ----------------
         // 16 bytes at a time, at the same place of the tile: whatever the swizzle, byte
-        // x of a column block belongs to token x / 128.  A thread's tokens are t0 + 16 k.
-        const int id = tid - 8 * 32, tok = id >> 3;
-        float wt[4];
-        auto weights = [&](int m) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int j = tok + 16 * k;
-                wt[k] = j < m ? exp2f(g2 * (m - 1 - j)) : 0.f;
-            }
-        };
-        weights(C);
+        // x of a column block belongs to token x / 128.  Four loads at once, as each
+        // takes longer than the work on it.
+        constexpr int PIECES = C * D / 16, STEP = SUM ? 192 : 96;  // of half the tokens
+        constexpr int BATCH = (PIECES + STEP - 1) / STEP;
+        const int id = tid - 9 * 32;
+        auto place = [&](int half, int y) { return (y >> 8) * 512 + half * 256 + (y & 255); };
         bool ok = true;
-        for (int c = 0; c < nc; ++c) {
-            const int m = min(C, w.n - c * C);
-            if (m < C) weights(m);
-            ok = wait_all(&full[c % NST], (c / NST) & 1) && (c == 0 || wait_all(u_full, (c - 1) & 1));
+        for (int c = 0; c < nc && ok; ++c) {
+            const int m = c + 1 < nc ? C : rest;
+            const float *wt = wdec + (c + 1 < nc ? 0 : C);
+            ok = wait_all(&full[c % NST], (c / NST) & 1);
             if (!ok) break;
             const uint32_t kt = s0 + (c % NST) * L::STAGE + L::TILE, vt = kt + L::TILE;
-#pragma unroll
-            for (int b = 0; b < D / 64; ++b)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t off = b * (C * 128) + k * 2048 + id * 16;
-                    if (tok + 16 * k >= m) {
-                        // no token of this work: its V and K may hold anything, and
-                        // 0 x NaN is NaN
-                        for (const uint32_t at : {kt + off, vt + off, s0 + L::OFF_VP + off,
-                                                  s0 + L::OFF_VP + L::TILE + off, s0 + L::OFF_VP + 2 * L::TILE + off})
-                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0u) : "memory");
-                        continue;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                if (m < C) {
+                    // no tokens of this work: their V and K may hold anything, and 0 x NaN is NaN
+                    for (int y = id; y < PIECES; y += STEP) {
+                        const int x = place(half, y);
+                        if (((x >> 3) & (C - 1)) >= m)
+                            for (const uint32_t at : {kt + x * 16, vt + x * 16})
+                                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0u) : "memory");
                     }
-                    const uint4 v = pa::lds128(vt + off);
-                    float2 x[4];
-                    pa::Elem<__nv_bfloat16>::unpack(v, x);
+                    __syncwarp();  // (a lane reads back what it wrote)
+                }
+                uint4 v[BATCH];
+                float f[BATCH];
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int x = place(half, min(id + k * STEP, PIECES - 1));
+                    v[k] = pa::lds128(vt + x * 16);
+                    f[k] = wt[(x >> 3) & (C - 1)];
+                }
+                if (c > 0) ok = wait_all(half ? u_full : u_half, (c - 1) & 1);
+                if (!ok) break;
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    float2 y[4];
+                    pa::Elem<__nv_bfloat16>::unpack(v[k], y);
                     uint32_t t[3][4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float2 y = __fmul2_rn(x[e], make_float2(wt[k], wt[k]));
-                        t[0][e] = take_bf16(y);
-                        t[1][e] = take_bf16(y);
-                        t[2][e] = pack_bf16(y.x, y.y);
+                        y[e] = __fmul2_rn(y[e], make_float2(f[k], f[k]));
+                        t[0][e] = take_bf16(y[e]);
+                        t[1][e] = take_bf16(y[e]);
+                        t[2][e] = pack_bf16(y[e].x, y[e].y);
                     }
+                    if (PIECES % STEP && id + k * STEP >= PIECES) break;
+                    const uint32_t at = s0 + L::OFF_VP + place(half, id + k * STEP) * 16;
 #pragma unroll
                     for (int term = 0; term < 3; ++term)
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(s0 + L::OFF_VP + term * L::TILE + off),
-                                     "r"(t[term][0]), "r"(t[term][1]), "r"(t[term][2]), "r"(t[term][3])
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + term * L::TILE), "r"(t[term][0]),
+                                     "r"(t[term][1]), "r"(t[term][2]), "r"(t[term][3])
                                      : "memory");
                 }
-            pa::fence_proxy_async();
-            signal(vp_full);
+                pa::fence_proxy_async();
+                signal(&vp_full[half]);
+            }
         }
         if (!ok) *fail = 1;
-    } else if (!SUM && warp < 12 + L::LANE_WARPS) {
-        // ---------------- P; outputs ----------------
+    } else if (SUM) {
+        for (int c = NST; c < nc && warp == L::LOAD_WARP; ++c) {
+            if (!wait_all(&empty[c % NST], ((c / NST) - 1) & 1)) {
+                *fail = 1;
+                break;
+            }
+            load(c);
+        }
+    } else if (warp < 12 + L::LANE_WARPS || warp == L::LOAD_WARP) {
+        // ---------------- outputs ----------------
         const int lw = warp & 3, row = lw * 32 + lane;
         const uint32_t base = tmem + (static_cast<uint32_t>(lw * 32) << 16);
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.p.out) +
-                             (static_cast<int64_t>(w.t0) * a.p.H + w.h) * D + row;
-        const int64_t step = static_cast<int64_t>(a.p.H) * D;
         bool ok = true;
-        auto make_p = [&](int c) {  // row = token of the chunk (warps 12 and 13)
-            if (!wait_all(&s1_full[c & 1], (c >> 1) & 1)) return false;
+        constexpr bool ALL = L::LANE_WARPS == 4;  // (else warp 15 has no lanes of its own)
+        constexpr int GROUP = ALL ? 128 : 96;     // threads that meet: of the outputs and warp 15
+        // row = value dimension.  Whether a wait of any of the group's warps has run out is
+        // known to all of them behind the barrier, so that none waits there alone.
+        auto put_o = [&](int c) {
+            const bool good = wait_all(o1_done, c & 1) && wait_all(o2_done, c & 1);
             pa::tc::fence_after();
-            const uint32_t to = s0 + L::OFF_P + (c & 1) * 2 * L::P_TERM + row * 128;
-#pragma unroll
-            for (int j0 = 0; j0 < C; j0 += 32) {
-                uint32_t u[32];
-                if (j0 <= lw * 32) {  // (else every token of it is later than the warp's)
-                    pa::tc::ld32(base + L::S1 + (c & 1) * C + j0, u);
-                    pa::tc::wait_ld();
-                }
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const int j = j0 + e + 2 * y;
-                        float2 x;
-                        x.x = j <= row && j0 <= lw * 32 ? __uint_as_float(u[e + 2 * y]) * fast_exp2(g2 * (row - j)) : 0.f;
-                        x.y = j < row && j0 <= lw * 32 ? __uint_as_float(u[e + 2 * y + 1]) * fast_exp2(g2 * (row - j - 1)) : 0.f;
-                        hi[y] = take_bf16(x);
-                        lo[y] = pack_bf16(x.x, x.y);
-                    }
-                    const uint32_t at = to + ((((j0 + e) >> 3) ^ (row & 7)) << 4);
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]),
-                                 "r"(hi[3])
-                                 : "memory");
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + L::P_TERM), "r"(lo[0]), "r"(lo[1]),
-                                 "r"(lo[2]), "r"(lo[3])
-                                 : "memory");
-                }
-            }
-            pa::tc::fence_before();
-            signal(&s1_free[c & 1]);
-            pa::fence_proxy_async();
-            signal(&p_full[c & 1]);
-            return true;
-        };
-        auto put_o = [&](int c) {  // row = value dimension
-            if (!wait_all(o1_done, c & 1) || !wait_all(o2_done, c & 1)) return false;
-            pa::tc::fence_after();
-            const int m = min(C, w.n - c * C);
-            __nv_bfloat16 *dst = out + static_cast<int64_t>(c) * C * step;
+            const int m = c + 1 < nc ? C : rest;
+            const uint32_t tile = s0 + (c % NST) * L::STAGE;  // of q, which has been used
+            if (good && (ALL || warp < 12 + L::LANE_WARPS)) {
+                // Lanes 2 x and 2 x + 1 trade: the even one writes both dimensions of token
+                // i, the odd one of token i + 4, whose 16-byte pieces the swizzle puts
+                // into the other banks.
+                uint8_t *to = smem + (c % NST) * L::STAGE + (row >> 6) * (C * 128) + (row & 6) * 2;
+                const uint32_t piece = (row & 63) >> 3;
+                const bool odd = lane & 1;
 #pragma unroll 1
-            for (int i0 = 0; i0 < C; i0 += 32) {
-                uint32_t x1[32], x2[32];
-                pa::tc::ld32(base + L::O1 + i0, x1);
-                pa::tc::ld32(base + L::O2 + i0, x2);
-                pa::tc::wait_ld();
-                if (i0 + 32 == C) {
-                    pa::tc::fence_before();
-                    signal(o_free);
-                }
+                for (int i0 = 0; i0 < C; i0 += 16) {
+                    uint32_t x1[16], x2[16];
+                    pa::tc::ld16(base + L::O1 + i0, x1);
+                    pa::tc::ld16(base + L::O2 + i0, x2);
+                    float o[16], got[8];
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (i0 + e < m)
-                        dst[(i0 + e) * step] = __float2bfloat16_rn(
-                            fmaf(fdec[i0 + e], __uint_as_float(x2[e]), a.p.scale * __uint_as_float(x1[e])));
+                    for (int e = 0; e < 16; e += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(fdec + i0 + e);
+                        o[e] = f.x, o[e + 1] = f.y, o[e + 2] = f.z, o[e + 3] = f.w;
+                    }
+                    pa::tc::wait_ld();
+                    if (i0 + 16 == C) {
+                        pa::tc::fence_before();
+                        signal(o_free);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        o[e] = fmaf(o[e], __uint_as_float(x2[e]), a.p.scale * __uint_as_float(x1[e]));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int i = (e & 3) + 8 * (e >> 2);  // tokens i and i + 4
+                        got[e] = __shfl_xor_sync(pa::kFull, odd ? o[i] : o[i + 4], 1);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int i = (e & 3) + 8 * (e >> 2);
+                        const uint32_t v = odd ? pack_bf16(got[e], o[i + 4]) : pack_bf16(o[i], got[e]);
+                        const uint32_t x = (odd ? 4 : 0) + (i & 3);  // token of 8: the swizzle's row
+                        *reinterpret_cast<uint32_t *>(to + (i0 + i - (i & 3)) * 128 + x * 128 + ((piece ^ x) << 4)) = v;
+                    }
+                }
+            }
+            pa::fence_proxy_async();
+            uint32_t all;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred p, 1, %2, p;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(all)
+                : "r"(static_cast<uint32_t>(good)), "n"(GROUP)
+                : "memory");
+            if (!all) return false;
+            if (m < C) {  // the last chunk's rows end inside the tile
+                const int id = ALL || warp < 14 ? tid - 12 * 32 : tid - 13 * 32;
+                for (int x = id; x < m * (D / 8); x += GROUP) {
+                    const int i = x / (D / 8), ch = x % (D / 8);
+                    const uint4 v = pa::lds128(tile + (ch >> 3) * (C * 128) + i * 128 + (((ch & 7) ^ (i & 7)) << 4));
+                    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.p.out) +
+                                               (static_cast<int64_t>(w.t0 + c * C + i) * a.p.H + w.h) * D + ch * 8) = v;
+                }
+            } else if (warp == L::LOAD_WARP) {
+                if (lane == 0) {
+#pragma unroll
+                    for (int b = 0; b < D / 64; ++b)
+                        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                                         reinterpret_cast<uint64_t>(&omap)),
+                                     "r"(b * 64), "r"(w.h), "r"(w.t0 + c * C), "r"(tile + b * (C * 128))
+                                     : "memory");
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                }
+                __syncwarp();
+                // every product of the chunk is done (o2_done) and its outputs have left
+                if (c + NST < nc) load(c + NST);
             }
             return true;
         };
-        for (int c = 0; c < nc && ok; ++c) {
-            if (lw < 2) ok = make_p(c);
-            if (ok && c > 0) ok = put_o(c - 1);
-        }
-        if (ok && nc > 0) ok = put_o(nc - 1);
+        for (int c = 0; c < nc && ok; ++c) ok = put_o(c);
+        if (warp == L::LOAD_WARP && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (!ok) *fail = 1;
     }
 
@@ -601,16 +713,17 @@ int launch(const ChunkParams &a, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0}, done_sum{0};
     if (int rc = set_smem_once(chunk_kernel<D, false>, L::SMEM, &done)) return rc;
     if (int rc = set_smem_once(chunk_kernel<D, true>, L::SMEM, &done_sum)) return rc;
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, o;
     if (int rc = pa::encode_rows_map(&q, a.p.q, a.p.T, a.p.q_stride, a.p.H, D, C)) return rc;
     if (int rc = pa::encode_rows_map(&k, a.p.k, a.p.T, a.p.k_stride, a.p.H, D, C)) return rc;
     if (int rc = pa::encode_rows_map(&v, a.p.v, a.p.T, a.p.v_stride, a.p.H, D, C)) return rc;
+    if (int rc = pa::encode_rows_map(&o, a.p.out, a.p.T, int64_t(a.p.H) * D, a.p.H, D, C)) return rc;
     const int64_t ctas = int64_t(a.seg ? a.slots : a.p.R) * a.p.H;
     if (a.seg) {
-        if (int rc = go(chunk_kernel<D, true>, ctas, L::THREADS, L::SMEM, stream, a, q, k, v)) return rc;
+        if (int rc = go(chunk_kernel<D, true>, ctas, L::THREADS, L::SMEM, stream, a, q, k, v, o)) return rc;
         if (int rc = go(chain_kernel<D>, int64_t(a.p.R) * a.p.H * (D * D / 4 / 256), 256, 0, stream, a)) return rc;
     }
-    return go(chunk_kernel<D, false>, ctas, L::THREADS, L::SMEM, stream, a, q, k, v);
+    return go(chunk_kernel<D, false>, ctas, L::THREADS, L::SMEM, stream, a, q, k, v, o);
 }
 
 }  // namespace
