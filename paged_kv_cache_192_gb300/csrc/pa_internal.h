@@ -46,8 +46,9 @@ int encode_pool_map(CUtensorMap *map, const void *pool, int64_t rows, int D, int
 int encode_q_map(CUtensorMap *map, const void *q, int64_t tokens, int Hq, int D, int gq,
                  int box_tokens);
 
-// 3D tensor map over rows [tokens][H][D] (bf16) with token_stride elements between
-// tokens: boxes of 64 columns x one head x box_tokens tokens, 128-byte swizzle.
+// 4D tensor map over rows [tokens][H][D] (bf16) with token_stride elements between
+// tokens, as columns of 64 (0), heads (1), tokens (2), blocks of 64 columns (3): boxes of
+// box_tokens rows of a head, block by block, 128-byte swizzle.
 int encode_rows_map(CUtensorMap *map, const void *x, int64_t tokens, int64_t token_stride, int H, int D,
                     int box_tokens);
 

@@ -12,14 +12,14 @@
 // issue slots.  Hence one CTA per (request, head) with a warp group for each job:
 //   warps 0-3, 4-7  the state, in registers in fp32 (thread = value dimension, half of
 //                   the key dimensions each): adds a chunk's K^T V' to it and gives
-//                   it to the next chunk's Q S as two bf16 terms in TMEM; in between,
-//                   0, 1, 4 and 5 write P as two bf16 terms to shared memory
+//                   it to the next chunk's Q S as two bf16 terms in TMEM; in between
+//                   0, 1, 4, 5 (and 13) write P as two bf16 terms to shared memory, and
+//                   7 copies: a chunk's outputs out, the chunk after the ring's in
 //   warp 8          issues the tcgen05.mma
 //   warps 9-11      V' = l^(C-1-j) v_j as three bf16 terms in shared memory, 32 tokens at
 //                   a time (the other 32 are in use meanwhile)
-//   warps 12-15     outputs, through the place of the chunk's q to a TMA store, whose
-//                   issuer (15) then has the chunk after the ring's loaded there; without
-//                   outputs V' too
+//   warps 12-15     outputs, into the place of the chunk's q for a TMA store; without
+//                   outputs V' too, and 15 copies
 // Outputs are computed transposed (lanes = value dimensions, columns = tokens), so the
 // state is an operand that lies in TMEM, where the threads that own it write it;
 // with tokens as lanes it would take 64 KB of shared memory.  Q K^T has its tokens
@@ -56,7 +56,7 @@ struct ChunkParams {
 template <int D>
 struct Lay {
     static constexpr int THREADS = 16 * 32;  // 128 registers each
-    static constexpr int MMA_WARP = 8, LOAD_WARP = 15;
+    static constexpr int MMA_WARP = 8, P_WARP = 13;
     static constexpr int NST = D == 128 ? 3 : 4;
     static constexpr int TILE = C * D * 2;       // a chunk's q, k or v
     static constexpr int STAGE = 3 * TILE;       // q, k, v
@@ -64,15 +64,18 @@ struct Lay {
     static constexpr int P_TERM = C * C * 2;
     static constexpr int OFF_P = OFF_VP + 3 * TILE;  // [buffer][term]
     static constexpr int OFF_BAR = OFF_P + 4 * P_TERM;
-    // full, empty (without outputs only) [NST]; s1_full, s1_free, p_full, vp_full [2];
+    // full (k, v), q_full, ready (the outputs lie in the stage; without outputs: empty)
+    // [NST]; s1_full, s1_free, p_full, vp_full [2];
     // u_half, u_full, u_free, s_full, o1_done, o2_done, o_free, drain
-    static constexpr int N_BAR = 2 * NST + 8 + 8;
-    static constexpr int OFF_F = OFF_BAR + N_BAR * 8;  // scale l^(i+1)
+    static constexpr int N_BAR = 3 * NST + 8 + 8;
+    static constexpr int OFF_F = (OFF_BAR + N_BAR * 8 + 15) / 16 * 16;  // scale l^(i+1)
     static constexpr int OFF_W = OFF_F + C * 4;        // l^(C-1-j), and of the last chunk
     static constexpr int OFF_D = OFF_W + 2 * C * 4;    // l^x, x = 1 - C .. C - 1 (1 below 0)
     static constexpr int OFF_MISC = OFF_D + 2 * C * 4; // TMEM slot, fail flag
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(OFF_VP % 1024 == 0 && OFF_P % 1024 == 0 && OFF_BAR % 8 == 0 && OFF_F % 16 == 0 && OFF_MISC % 8 == 0,
+                  "alignment");
     static constexpr int TMEM_COLS = 512;
     static constexpr int U = 0, S = D, S1 = 2 * D, O2 = S1 + 2 * C, O1 = O2 + C;
     static_assert(O1 + C <= TMEM_COLS, "tensor memory");
@@ -147,6 +150,22 @@ __device__ __forceinline__ Work find_work(const ChunkParams &a) {
     return w;
 }
 
+// The chunk of tokens t0 .. of head h into shared memory, completing on `bar`; and out.
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, int h, int t0, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %2}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(h), "r"(t0), "r"(pa::smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void store_rows(const CUtensorMap *map, int h, int t0, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %1}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(0), "r"(h), "r"(t0), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
 // x as two or three bf16 terms, two values at a time
 __device__ __forceinline__ uint32_t take_bf16(float2 &x) {
     const uint32_t t = pack_bf16(x.x, x.y);
@@ -166,7 +185,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s0 = pa::smem_u32(smem);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
-    uint64_t *full = bars, *empty = full + NST, *s1_full = empty + NST, *s1_free = s1_full + 2,
+    uint64_t *full = bars, *q_full = full + NST, *ready = q_full + NST, *s1_full = ready + NST, *s1_free = s1_full + 2,
              *p_full = s1_free + 2, *vp_full = p_full + 2, *u_half = vp_full + 2, *u_full = u_half + 1, *u_free = u_full + 1,
              *s_full = u_free + 1, *o1_done = s_full + 1, *o2_done = o1_done + 1, *o_free = o2_done + 1,
              *drain = o_free + 1;
@@ -182,12 +201,13 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
         for (int i = 0; i < NST; ++i) {
             pa::mbar_init(&full[i], 1);
-            pa::mbar_init(&empty[i], 1);
+            pa::mbar_init(&q_full[i], 1);
+            pa::mbar_init(&ready[i], SUM ? 1 : L::LANE_WARPS);
         }
         for (int i = 0; i < 2; ++i) {
             pa::mbar_init(&s1_full[i], 1);
-            pa::mbar_init(&s1_free[i], 4);
-            pa::mbar_init(&p_full[i], 4);
+            pa::mbar_init(&s1_free[i], 5);
+            pa::mbar_init(&p_full[i], 5);
             pa::mbar_init(&vp_full[i], SUM ? 6 : 3);
         }
         pa::mbar_init(u_half, 1);
@@ -226,31 +246,99 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
     __syncthreads();
     pa::tc::fence_after();
     const uint32_t tmem = *tslot;
-    int loads_issued = 0;
+    int loads_issued = 0, q_issued = 0;
     auto signal = [&](uint64_t *bar) {  // one arrival per warp, behind its writes
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
 
-    // Copies of chunk c into its stage (warp 15).  Whole tiles of 64 tokens: rows past the
+    constexpr int LOAD_WARP = SUM ? 15 : 7;
+    // Copies of chunk c into its stage (that warp).  Whole tiles of 64 tokens: rows past the
     // work's tokens are other tokens' (or zeros past the last), see below.
-    auto load = [&](int c) {
-        constexpr int FIRST = SUM ? 1 : 0;  // (no q)
+    auto load_kv = [&](int c) {
         const int st = c % NST;
         if (lane == 0) {
-            pa::mbar_arrive_expect_tx(&full[st], (3 - FIRST) * L::TILE);
+            pa::mbar_arrive_expect_tx(&full[st], 2 * L::TILE);
             ++loads_issued;
-#pragma unroll
-            for (int x = FIRST; x < 3; ++x)
-#pragma unroll
-                for (int b = 0; b < D / 64; ++b)
-                    tma_load_3d(s0 + st * L::STAGE + x * L::TILE + b * (C * 128),
-                                x == 0 ? &qmap : x == 1 ? &kmap : &vmap, b * 64, w.h, w.t0 + c * C, &full[st]);
+            load_rows(s0 + st * L::STAGE + L::TILE, &kmap, w.h, w.t0 + c * C, &full[st]);
+            load_rows(s0 + st * L::STAGE + 2 * L::TILE, &vmap, w.h, w.t0 + c * C, &full[st]);
         }
         __syncwarp();
     };
-    if (warp == L::LOAD_WARP)
-        for (int c = 0; c < min(nc, NST); ++c) load(c);
+    auto load_q = [&](int c) {
+        const int st = c % NST;
+        if (lane == 0) {
+            pa::mbar_arrive_expect_tx(&q_full[st], L::TILE);
+            ++q_issued;
+            load_rows(s0 + st * L::STAGE, &qmap, w.h, w.t0 + c * C, &q_full[st]);
+        }
+        __syncwarp();
+    };
+    // The outputs of chunk c out of its stage, and q of the chunk after the ring's into
+    // it.  (k and v of that chunk need not wait for the outputs: for D = 128 this warp
+    // sees the end of the chunk's products by itself.)  The last chunk's rows may end
+    // inside the tile, then the output warps have written them.
+    auto turn = [&](int c) {
+        if (c + 1 == nc && rest < C) return true;
+        if (!wait_all(&ready[c % NST], (c / NST) & 1)) return false;
+        const bool more = c + NST < nc;
+        if (D == 64 && more) load_kv(c + NST);
+        if (lane == 0) {
+            store_rows(&omap, w.h, w.t0 + c * C, s0 + (c % NST) * L::STAGE);
+            if (more) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        }
+        __syncwarp();
+        if (more) load_q(c + NST);
+        return true;
+    };
+    if (warp == LOAD_WARP)
+        for (int c = 0; c < min(nc, NST); ++c) {
+            load_kv(c);
+            if (!SUM) load_q(c);
+        }
+
+    // P of chunk c, columns j0 .. j1 (whole 16s): lane = token i of the chunk (warps whose
+    // lanes are 0-63).  Of tokens 0-31 the columns from 32 on are 0 and stay so.
+    auto make_p = [&](int c, int j0, int j1) {
+        const int row = (warp & 1) * 32 + lane;
+        const uint32_t from = tmem + (static_cast<uint32_t>((warp & 1) * 32) << 16) + L::S1 + (c & 1) * C;
+        if (!wait_all(&s1_full[c & 1], (c >> 1) & 1)) return false;
+        pa::tc::fence_after();
+        const uint32_t to = s0 + L::OFF_P + (c & 1) * 2 * L::P_TERM + row * 128;
+#pragma unroll 1
+        for (; j0 < j1; j0 += 16) {
+            uint32_t hi[8], lo[8], u[16];
+            pa::tc::ld16(from + j0, u);
+            const float *f = pdec + (row - j0);  // l^(row - j): neighbours in neighbouring lanes
+            float2 x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = make_float2(f[-2 * e], f[-2 * e - 1]);
+            pa::tc::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                // (a score of a later token may be anything, also NaN)
+                x[e].x = j0 + 2 * e <= row ? x[e].x * __uint_as_float(u[2 * e]) : 0.f;
+                x[e].y = j0 + 2 * e < row ? x[e].y * __uint_as_float(u[2 * e + 1]) : 0.f;
+                hi[e] = take_bf16(x[e]);
+                lo[e] = pack_bf16(x[e].x, x[e].y);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                const uint32_t at = to + ((((j0 + 2 * e) >> 3) ^ (row & 7)) << 4);
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi[e]), "r"(hi[e + 1]),
+                             "r"(hi[e + 2]), "r"(hi[e + 3])
+                             : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + L::P_TERM), "r"(lo[e]),
+                             "r"(lo[e + 1]), "r"(lo[e + 2]), "r"(lo[e + 3])
+                             : "memory");
+            }
+        }
+        pa::tc::fence_before();
+        signal(&s1_free[c & 1]);
+        pa::fence_proxy_async();
+        signal(&p_full[c & 1]);
+        return true;
+    };
 
     if (warp == L::MMA_WARP) {
         // ---------------- MMA ----------------
@@ -262,7 +350,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         // rows of 128 bytes, K-major; tokens as K (64 tokens per column block)
         const uint64_t row_major = pa::tc::sdesc(s0, 16, 1024), col_major = pa::tc::sdesc(s0, C * 128, 1024);
         auto issue_s1 = [&](int c) {
-            if (!wait_all(&full[c % NST], (c / NST) & 1)) return false;
+            if (!wait_all(&full[c % NST], (c / NST) & 1) || !wait_all(&q_full[c % NST], (c / NST) & 1)) return false;
             if (c >= 2 && !wait_all(&s1_free[c & 1], ((c >> 1) - 1) & 1)) return false;
             pa::tc::fence_after();
             if (pa::tc::elect_one()) {
@@ -296,7 +384,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                             pa::tc::mma_ss(tmem + L::U, vp + term * kTile + ((ks * 16 * 128) >> 4),
                                            k + ((ks * 16 * 128) >> 4), kIdU, ks + term > 0);
                     pa::tc::commit(half ? u_full : u_half);
-                    if (SUM && half) pa::tc::commit(&empty[c % NST]);
+                    if (SUM && half) pa::tc::commit(&ready[c % NST]);
                 }
                 __syncwarp();
             }
@@ -365,51 +453,13 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                 pa::tc::fence_before();
                 signal(s_full);
             };
-            // P of chunk c: lane = token i of the chunk, columns j.  Warps 0 and 4 have rows
-            // 0-31, whose columns from 32 on are 0 (and stay so), 1 and 5 rows 32-63.
-            const int lw = warp & 3, row = lw * 32 + lane, j_step = (lw + 1) * 16;
-            auto make_p = [&](int c) {
-                if (!wait_all(&s1_full[c & 1], (c >> 1) & 1)) return false;
-                pa::tc::fence_after();
-                const uint32_t to = s0 + L::OFF_P + (c & 1) * 2 * L::P_TERM + row * 128;
-#pragma unroll 1
-                for (int j0 = (warp >> 2) * j_step; j0 < ((warp >> 2) + 1) * j_step; j0 += 16) {
-                    uint32_t hi[8], lo[8], u[16];
-                    pa::tc::ld16(base + L::S1 + (c & 1) * C + j0, u);
-                    const float *f = pdec + (row - j0);  // l^(row - j): neighbours in neighbouring lanes
-                    float2 x[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = make_float2(f[-2 * e], f[-2 * e - 1]);
-                    pa::tc::wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        // (a score of a later token may be anything, also NaN)
-                        x[e].x = j0 + 2 * e <= row ? x[e].x * __uint_as_float(u[2 * e]) : 0.f;
-                        x[e].y = j0 + 2 * e < row ? x[e].y * __uint_as_float(u[2 * e + 1]) : 0.f;
-                        hi[e] = take_bf16(x[e]);
-                        lo[e] = pack_bf16(x[e].x, x[e].y);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; e += 4) {
-                        const uint32_t at = to + ((((j0 + 2 * e) >> 3) ^ (row & 7)) << 4);
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi[e]), "r"(hi[e + 1]),
-                                     "r"(hi[e + 2]), "r"(hi[e + 3])
-                                     : "memory");
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + L::P_TERM), "r"(lo[e]),
-                                     "r"(lo[e + 1]), "r"(lo[e + 2]), "r"(lo[e + 3])
-                                     : "memory");
-                    }
-                }
-                pa::tc::fence_before();
-                signal(&s1_free[c & 1]);
-                pa::fence_proxy_async();
-                signal(&p_full[c & 1]);
-                return true;
-            };
+            // P: warps 0 and 4 have tokens 0-31, 1 and 5 (and 13) tokens 32-63
+            const bool has_p = (warp & 3) < 2;
+            const int j0 = (warp >> 2) * 16;
             bool ok = true;
             if (!SUM && nc > 0) {
                 give();
-                if (lw < 2) ok = make_p(0);
+                if (has_p) ok = make_p(0, j0, j0 + 16);
             }
             const float em_full = expm1f(g * C), em_rest = expm1f(g * rest);
             for (int c = 0; c < nc && ok; ++c) {
@@ -434,13 +484,17 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                 signal(u_free);
                 if (!SUM && c + 1 < nc) {
                     // (the place of this P was read before the last Q S)
-                    if (lw < 2) ok = make_p(c + 1);
+                    if (has_p) ok = make_p(c + 1, j0, j0 + 16);
+                    if (warp == LOAD_WARP && c > 0) ok = turn(c - 1);
                     ok = ok && wait_all(o2_done, c & 1);  // the last Q S has read its state
                     if (!ok) break;
                     pa::tc::fence_after();
+                    if (warp == LOAD_WARP && c + NST < nc) load_kv(c + NST);
                     give();
                 }
             }
+            if (!SUM && ok && warp == LOAD_WARP)
+                for (int c = max(0, nc - 2); c < nc && ok; ++c) ok = turn(c);
             if (!ok) *fail = 1;
             else if (w.to && nc > 0) {
 #pragma unroll
@@ -449,7 +503,12 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                     w.to[(k0 + k + 1) * D + dv] = s[k / 2].y;
                 }
             }
+        } else if (!SUM && warp == LOAD_WARP) {  // (D = 64)
+            bool ok = true;
+            for (int c = 0; c < nc && ok; ++c) ok = turn(c);
+            if (!ok) *fail = 1;
         }
+        if (!SUM && warp == LOAD_WARP && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else if (warp < (SUM ? 15 : 12)) {
         // ---------------- V' ----------------
         // 16 bytes at a time, at the same place of the tile: whatever the swizzle, byte
@@ -514,103 +573,83 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         }
         if (!ok) *fail = 1;
     } else if (SUM) {
-        for (int c = NST; c < nc && warp == L::LOAD_WARP; ++c) {
-            if (!wait_all(&empty[c % NST], ((c / NST) - 1) & 1)) {
+        for (int c = NST; c < nc; ++c) {
+            if (!wait_all(&ready[c % NST], ((c / NST) - 1) & 1)) {
                 *fail = 1;
                 break;
             }
-            load(c);
+            load_kv(c);
         }
-    } else if (warp < 12 + L::LANE_WARPS || warp == L::LOAD_WARP) {
+    } else if (warp < 12 + L::LANE_WARPS) {
         // ---------------- outputs ----------------
         const int lw = warp & 3, row = lw * 32 + lane;
         const uint32_t base = tmem + (static_cast<uint32_t>(lw * 32) << 16);
         bool ok = true;
-        constexpr bool ALL = L::LANE_WARPS == 4;  // (else warp 15 has no lanes of its own)
-        constexpr int GROUP = ALL ? 128 : 96;     // threads that meet: of the outputs and warp 15
-        // row = value dimension.  Whether a wait of any of the group's warps has run out is
-        // known to all of them behind the barrier, so that none waits there alone.
-        auto put_o = [&](int c) {
-            const bool good = wait_all(o1_done, c & 1) && wait_all(o2_done, c & 1);
+        auto put_o = [&](int c) {  // row = value dimension
+            if (!wait_all(o1_done, c & 1) || !wait_all(o2_done, c & 1)) return false;
             pa::tc::fence_after();
             const int m = c + 1 < nc ? C : rest;
             const uint32_t tile = s0 + (c % NST) * L::STAGE;  // of q, which has been used
-            if (good && (ALL || warp < 12 + L::LANE_WARPS)) {
-                // Lanes 2 x and 2 x + 1 trade: the even one writes both dimensions of token
-                // i, the odd one of token i + 4, whose 16-byte pieces the swizzle puts
-                // into the other banks.
-                uint8_t *to = smem + (c % NST) * L::STAGE + (row >> 6) * (C * 128) + (row & 6) * 2;
-                const uint32_t piece = (row & 63) >> 3;
-                const bool odd = lane & 1;
-#pragma unroll 1
-                for (int i0 = 0; i0 < C; i0 += 16) {
-                    uint32_t x1[16], x2[16];
-                    pa::tc::ld16(base + L::O1 + i0, x1);
-                    pa::tc::ld16(base + L::O2 + i0, x2);
-                    float o[16], got[8];
+            // Lanes 2 x and 2 x + 1 trade: the even one writes both dimensions of token
+            // i, the odd one of token i + 4, whose 16-byte pieces the swizzle puts
+            // into the other banks.
+            uint8_t *to = smem + (c % NST) * L::STAGE + (row >> 6) * (C * 128) + (row & 6) * 2;
+            const uint32_t piece = (row & 63) >> 3;
+            const bool odd = lane & 1;
+            // (all columns first: the next chunk's products wait for these)
+            float o[C];
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(fdec + i0 + e);
-                        o[e] = f.x, o[e + 1] = f.y, o[e + 2] = f.z, o[e + 3] = f.w;
-                    }
-                    pa::tc::wait_ld();
-                    if (i0 + 16 == C) {
-                        pa::tc::fence_before();
-                        signal(o_free);
-                    }
+            for (int i0 = 0; i0 < C; i0 += 16) {
+                uint32_t x1[16], x2[16];
+                pa::tc::ld16(base + L::O1 + i0, x1);
+                pa::tc::ld16(base + L::O2 + i0, x2);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        o[e] = fmaf(o[e], __uint_as_float(x2[e]), a.p.scale * __uint_as_float(x1[e]));
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(fdec + i0 + e);
+                    o[i0 + e] = f.x, o[i0 + e + 1] = f.y, o[i0 + e + 2] = f.z, o[i0 + e + 3] = f.w;
+                }
+                pa::tc::wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int i = (e & 3) + 8 * (e >> 2);  // tokens i and i + 4
-                        got[e] = __shfl_xor_sync(pa::kFull, odd ? o[i] : o[i + 4], 1);
-                    }
+                for (int e = 0; e < 16; ++e)
+                    o[i0 + e] = fmaf(o[i0 + e], __uint_as_float(x2[e]), a.p.scale * __uint_as_float(x1[e]));
+            }
+            pa::tc::fence_before();
+            signal(o_free);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int i = (e & 3) + 8 * (e >> 2);
-                        const uint32_t v = odd ? pack_bf16(got[e], o[i + 4]) : pack_bf16(o[i], got[e]);
-                        const uint32_t x = (odd ? 4 : 0) + (i & 3);  // token of 8: the swizzle's row
-                        *reinterpret_cast<uint32_t *>(to + (i0 + i - (i & 3)) * 128 + x * 128 + ((piece ^ x) << 4)) = v;
-                    }
+            for (int i0 = 0; i0 < C; i0 += 16) {
+                float got[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int i = i0 + (e & 3) + 8 * (e >> 2);  // tokens i and i + 4
+                    got[e] = __shfl_xor_sync(pa::kFull, odd ? o[i] : o[i + 4], 1);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int i = i0 + (e & 3) + 8 * (e >> 2);
+                    const uint32_t v = odd ? pack_bf16(got[e], o[i + 4]) : pack_bf16(o[i], got[e]);
+                    const uint32_t x = (odd ? 4 : 0) + (i & 3);  // token of 8: the swizzle's row
+                    *reinterpret_cast<uint32_t *>(to + (i - (i & 3)) * 128 + x * 128 + ((piece ^ x) << 4)) = v;
                 }
             }
             pa::fence_proxy_async();
-            uint32_t all;
-            asm volatile(
-                "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred p, 1, %2, p;\n\t"
-                "selp.u32 %0, 1, 0, p;\n\t}"
-                : "=r"(all)
-                : "r"(static_cast<uint32_t>(good)), "n"(GROUP)
-                : "memory");
-            if (!all) return false;
-            if (m < C) {  // the last chunk's rows end inside the tile
-                const int id = ALL || warp < 14 ? tid - 12 * 32 : tid - 13 * 32;
-                for (int x = id; x < m * (D / 8); x += GROUP) {
+            signal(&ready[c % NST]);
+            if (m < C) {  // the last chunk's rows end inside the tile: copied here
+                if (!wait_all(&ready[c % NST], (c / NST) & 1)) return false;
+                for (int x = tid - 12 * 32; x < m * (D / 8); x += L::LANE_WARPS * 32) {
                     const int i = x / (D / 8), ch = x % (D / 8);
                     const uint4 v = pa::lds128(tile + (ch >> 3) * (C * 128) + i * 128 + (((ch & 7) ^ (i & 7)) << 4));
                     *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.p.out) +
                                                (static_cast<int64_t>(w.t0 + c * C + i) * a.p.H + w.h) * D + ch * 8) = v;
                 }
-            } else if (warp == L::LOAD_WARP) {
-                if (lane == 0) {
-#pragma unroll
-                    for (int b = 0; b < D / 64; ++b)
-                        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                                         reinterpret_cast<uint64_t>(&omap)),
-                                     "r"(b * 64), "r"(w.h), "r"(w.t0 + c * C), "r"(tile + b * (C * 128))
-                                     : "memory");
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                }
-                __syncwarp();
-                // every product of the chunk is done (o2_done) and its outputs have left
-                if (c + NST < nc) load(c + NST);
             }
             return true;
         };
-        for (int c = 0; c < nc && ok; ++c) ok = put_o(c);
-        if (warp == L::LOAD_WARP && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        // (P of tokens 32-63, columns 32-63)
+        if (nc > 0 && warp == L::P_WARP) ok = make_p(0, 32, 64);
+        for (int c = 0; c < nc && ok; ++c) {
+            if (c + 1 < nc && warp == L::P_WARP) ok = make_p(c + 1, 32, 64);
+            ok = ok && put_o(c);
+        }
         if (!ok) *fail = 1;
     }
 
@@ -626,10 +665,10 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
             __syncwarp();
             (void)pa::mbar_wait(drain, 0);
         }
-        if (warp == L::LOAD_WARP && lane == 0)
-            for (int st = 0; st < NST && st < loads_issued; ++st) {
-                const int last = st + NST * ((loads_issued - 1 - st) / NST);
-                (void)pa::mbar_wait(&full[st], (last / NST) & 1);
+        if (warp == LOAD_WARP && lane == 0)
+            for (int st = 0; st < NST; ++st) {
+                if (st < loads_issued) (void)pa::mbar_wait(&full[st], (loads_issued - 1 - st) / NST & 1);
+                if (st < q_issued) (void)pa::mbar_wait(&q_full[st], (q_issued - 1 - st) / NST & 1);
             }
         pa::tc::fence_before();
         __syncthreads();
