@@ -15,11 +15,12 @@
 //                   it to the next chunk's Q S as two bf16 terms in TMEM; in between
 //                   0, 1, 4, 5 (and 13) write P as two bf16 terms to shared memory, and
 //                   7 copies: a chunk's outputs out, the chunk after the ring's in
-//   warp 8          issues the tcgen05.mma
-//   warps 9-11      V' = l^(C-1-j) v_j as three bf16 terms in shared memory, 32 tokens at
-//                   a time (the other 32 are in use meanwhile)
+//   warp 9          issues the tcgen05.mma
+//   warps 8, 10, 11 V' = l^(C-1-j) v_j as three bf16 terms in shared memory, 32 tokens at
+//                   a time (the other 32 are in use meanwhile).  P is made by warps of
+//                   schedulers 0 and 1, so 8 has a smaller share than 10 and 11
 //   warps 12-15     outputs, into the place of the chunk's q for a TMA store; without
-//                   outputs V' too, and 15 copies
+//                   outputs 13 has a quarter of V', and 15 copies
 // Outputs are computed transposed (lanes = value dimensions, columns = tokens), so the
 // state is an operand that lies in TMEM, where the threads that own it write it;
 // with tokens as lanes it would take 64 KB of shared memory.  Q K^T has its tokens
@@ -56,7 +57,7 @@ struct ChunkParams {
 template <int D>
 struct Lay {
     static constexpr int THREADS = 16 * 32;  // 128 registers each
-    static constexpr int MMA_WARP = 8, P_WARP = 13;
+    static constexpr int MMA_WARP = 9, P_WARP = 13;
     static constexpr int NST = D == 128 ? 3 : 4;
     static constexpr int TILE = C * D * 2;       // a chunk's q, k or v
     static constexpr int STAGE = 3 * TILE;       // q, k, v
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
             pa::mbar_init(&s1_full[i], 1);
             pa::mbar_init(&s1_free[i], 5);
             pa::mbar_init(&p_full[i], 5);
-            pa::mbar_init(&vp_full[i], SUM ? 6 : 3);
+            pa::mbar_init(&vp_full[i], SUM ? 4 : 3);
         }
         pa::mbar_init(u_half, 1);
         pa::mbar_init(u_full, 1);
@@ -509,15 +510,20 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
             if (!ok) *fail = 1;
         }
         if (!SUM && warp == LOAD_WARP && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    } else if (warp < (SUM ? 15 : 12)) {
+    } else if (warp < 12 || (SUM && warp == 13)) {
         // ---------------- V' ----------------
         // 16 bytes at a time, at the same place of the tile: whatever the swizzle, byte
         // x of a column block belongs to token x / 128.  Four loads at once, as each
         // takes longer than the work on it.
-        constexpr int PIECES = C * D / 16, STEP = SUM ? 192 : 96;  // of half the tokens
-        constexpr int BATCH = (PIECES + STEP - 1) / STEP;
-        const int id = tid - 9 * 32;
-        auto place = [&](int half, int y) { return (y >> 8) * 512 + half * 256 + (y & 255); };
+        constexpr int PIECES = C * D / 16;  // of half the tokens
+        constexpr int MOST = PIECES / 32 * (SUM ? 4 : 6) / 16;  // per thread: 4 of 16 parts each, or 4, 6 and 6
+        const int part = SUM ? (warp == 13 ? 12 : (warp - 8 - (warp > 8)) * 4) : warp == 8 ? 0 : warp == 10 ? 4 : 10;
+        const int mine = SUM || warp > 8 ? MOST : PIECES / 32 * 4 / 16, first = PIECES / 16 * part + lane;
+        // byte offset of a thread's k-th piece
+        auto place = [&](int half, int k) {
+            const int y = first + k * 32;
+            return ((y >> 8) * 512 + half * 256 + (y & 255)) * 16;
+        };
         bool ok = true;
         for (int c = 0; c < nc && ok; ++c) {
             const int m = c + 1 < nc ? C : rest;
@@ -529,26 +535,27 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
             for (int half = 0; half < 2; ++half) {
                 if (m < C) {
                     // no tokens of this work: their V and K may hold anything, and 0 x NaN is NaN
-                    for (int y = id; y < PIECES; y += STEP) {
-                        const int x = place(half, y);
-                        if (((x >> 3) & (C - 1)) >= m)
-                            for (const uint32_t at : {kt + x * 16, vt + x * 16})
+                    for (int k = 0; k < mine; ++k) {
+                        const int x = place(half, k);
+                        if (((x >> 7) & (C - 1)) >= m)
+                            for (const uint32_t at : {kt + x, vt + x})
                                 asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0u) : "memory");
                     }
                     __syncwarp();  // (a lane reads back what it wrote)
                 }
-                uint4 v[BATCH];
-                float f[BATCH];
+                uint4 v[MOST];
+                float f[MOST];
 #pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    const int x = place(half, min(id + k * STEP, PIECES - 1));
-                    v[k] = pa::lds128(vt + x * 16);
-                    f[k] = wt[(x >> 3) & (C - 1)];
+                for (int k = 0; k < MOST; ++k) {
+                    const int x = place(half, min(k, mine - 1));
+                    v[k] = pa::lds128(vt + x);
+                    f[k] = wt[(x >> 7) & (C - 1)];
                 }
                 if (c > 0) ok = wait_all(half ? u_full : u_half, (c - 1) & 1);
                 if (!ok) break;
 #pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
+                for (int k = 0; k < MOST; ++k) {
+                    if (k >= mine) break;
                     float2 y[4];
                     pa::Elem<__nv_bfloat16>::unpack(v[k], y);
                     uint32_t t[3][4];
@@ -559,8 +566,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                         t[1][e] = take_bf16(y[e]);
                         t[2][e] = pack_bf16(y[e].x, y[e].y);
                     }
-                    if (PIECES % STEP && id + k * STEP >= PIECES) break;
-                    const uint32_t at = s0 + L::OFF_VP + place(half, id + k * STEP) * 16;
+                    const uint32_t at = s0 + L::OFF_VP + place(half, k);
 #pragma unroll
                     for (int term = 0; term < 3; ++term)
                         asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + term * L::TILE), "r"(t[term][0]),
@@ -573,7 +579,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         }
         if (!ok) *fail = 1;
     } else if (SUM) {
-        for (int c = NST; c < nc; ++c) {
+        for (int c = NST; c < nc && warp == LOAD_WARP; ++c) {  // (one warp: 12 and 14 are idle)
             if (!wait_all(&ready[c % NST], ((c / NST) - 1) & 1)) {
                 *fail = 1;
                 break;
