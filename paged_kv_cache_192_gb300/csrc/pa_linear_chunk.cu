@@ -356,11 +356,13 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
             pa::tc::fence_after();
             if (pa::tc::elect_one()) {
                 const uint64_t q = row_major + static_cast<uint32_t>((c % NST) * kStage), k = q + kTile;
+#pragma unroll 1
+                for (int b = 0; b < D / 64; ++b)
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = ((ks >> 2) * C * 128 + (ks & 3) * 32) >> 4;
-                    pa::tc::mma_ss(tmem + L::S1 + (c & 1) * C, q + off, k + off, kIdS1, ks > 0);
-                }
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint32_t off = (b * C * 128 + ks * 32) >> 4;
+                        pa::tc::mma_ss(tmem + L::S1 + (c & 1) * C, q + off, k + off, kIdS1, b + ks > 0);
+                    }
                 pa::tc::commit(&s1_full[c & 1]);
             }
             __syncwarp();
@@ -371,14 +373,14 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
             const uint32_t stage = static_cast<uint32_t>((c % NST) * kStage);
             if (SUM) ok = wait_all(&full[c % NST], (c / NST) & 1);
             if (c > 0) ok = ok && wait_all(u_free, (c - 1) & 1);
-#pragma unroll
+#pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 ok = ok && wait_all(&vp_full[half], c & 1);
                 if (!ok) break;
                 pa::tc::fence_after();
                 if (pa::tc::elect_one()) {
                     const uint64_t k = col_major + stage + kTile, vp = col_major + (L::OFF_VP >> 4);
-#pragma unroll
+#pragma unroll 1
                     for (int ks = half * C / 32; ks < (half + 1) * C / 32; ++ks)
 #pragma unroll
                         for (int term = 0; term < 3; ++term)
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
             if (pa::tc::elect_one()) {
                 const uint64_t v = col_major + stage + 2 * kTile;
                 const uint64_t p = row_major + ((L::OFF_P + (c & 1) * 2 * L::P_TERM) >> 4);
-#pragma unroll
+#pragma unroll 1
                 for (int ks = 0; ks < C / 16; ++ks)
 #pragma unroll
                     for (int term = 0; term < 2; ++term)
@@ -412,12 +414,14 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
             pa::tc::fence_after();
             if (pa::tc::elect_one()) {
                 const uint64_t q = row_major + stage;
+#pragma unroll 1
+                for (int b = 0; b < D / 64; ++b)
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
+                    for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-                    for (int term = 0; term < 2; ++term)
-                        pa::tc::mma_ts(tmem + L::O2, tmem + L::S + term * (D / 2) + ks * 8,
-                                       q + (((ks >> 2) * C * 128 + (ks & 3) * 32) >> 4), kIdO2, ks + term > 0);
+                        for (int term = 0; term < 2; ++term)
+                            pa::tc::mma_ts(tmem + L::O2, tmem + L::S + term * (D / 2) + b * 32 + ks * 8,
+                                           q + ((b * C * 128 + ks * 32) >> 4), kIdO2, b + ks + term > 0);
                 pa::tc::commit(o2_done);
             }
             __syncwarp();
@@ -543,36 +547,41 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                     }
                     __syncwarp();  // (a lane reads back what it wrote)
                 }
-                uint4 v[MOST];
-                float f[MOST];
-#pragma unroll
-                for (int k = 0; k < MOST; ++k) {
+                uint4 v[2];
+                float f[2];
+                auto fetch = [&](int k, int to) {
                     const int x = place(half, min(k, mine - 1));
-                    v[k] = pa::lds128(vt + x);
-                    f[k] = wt[(x >> 7) & (C - 1)];
-                }
+                    v[to] = pa::lds128(vt + x);
+                    f[to] = wt[(x >> 7) & (C - 1)];
+                };
+                fetch(0, 0);
                 if (c > 0) ok = wait_all(half ? u_full : u_half, (c - 1) & 1);
                 if (!ok) break;
+                // (not unrolled further: the roles' loops together have to stay near the
+                // instruction caches)
+#pragma unroll 1
+                for (int k0 = 0; k0 < mine; k0 += 2)
 #pragma unroll
-                for (int k = 0; k < MOST; ++k) {
-                    if (k >= mine) break;
-                    float2 y[4];
-                    pa::Elem<__nv_bfloat16>::unpack(v[k], y);
-                    uint32_t t[3][4];
+                    for (int k = 0; k < 2; ++k) {
+                        fetch(k0 + k + 1, k ^ 1);
+                        if (k0 + k >= mine) break;
+                        float2 y[4];
+                        pa::Elem<__nv_bfloat16>::unpack(v[k], y);
+                        uint32_t t[3][4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        y[e] = __fmul2_rn(y[e], make_float2(f[k], f[k]));
-                        t[0][e] = take_bf16(y[e]);
-                        t[1][e] = take_bf16(y[e]);
-                        t[2][e] = pack_bf16(y[e].x, y[e].y);
+                        for (int e = 0; e < 4; ++e) {
+                            y[e] = __fmul2_rn(y[e], make_float2(f[k], f[k]));
+                            t[0][e] = take_bf16(y[e]);
+                            t[1][e] = take_bf16(y[e]);
+                            t[2][e] = pack_bf16(y[e].x, y[e].y);
+                        }
+                        const uint32_t at = s0 + L::OFF_VP + place(half, k0 + k);
+#pragma unroll
+                        for (int term = 0; term < 3; ++term)
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + term * L::TILE),
+                                         "r"(t[term][0]), "r"(t[term][1]), "r"(t[term][2]), "r"(t[term][3])
+                                         : "memory");
                     }
-                    const uint32_t at = s0 + L::OFF_VP + place(half, k);
-#pragma unroll
-                    for (int term = 0; term < 3; ++term)
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + term * L::TILE), "r"(t[term][0]),
-                                     "r"(t[term][1]), "r"(t[term][2]), "r"(t[term][3])
-                                     : "memory");
-                }
                 pa::fence_proxy_async();
                 signal(&vp_full[half]);
             }
@@ -602,39 +611,36 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
             uint8_t *to = smem + (c % NST) * L::STAGE + (row >> 6) * (C * 128) + (row & 6) * 2;
             const uint32_t piece = (row & 63) >> 3;
             const bool odd = lane & 1;
-            // (all columns first: the next chunk's products wait for these)
-            float o[C];
-#pragma unroll
+#pragma unroll 1
             for (int i0 = 0; i0 < C; i0 += 16) {
                 uint32_t x1[16], x2[16];
                 pa::tc::ld16(base + L::O1 + i0, x1);
                 pa::tc::ld16(base + L::O2 + i0, x2);
+                float o[16], got[8];
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     const float4 f = *reinterpret_cast<const float4 *>(fdec + i0 + e);
-                    o[i0 + e] = f.x, o[i0 + e + 1] = f.y, o[i0 + e + 2] = f.z, o[i0 + e + 3] = f.w;
+                    o[e] = f.x, o[e + 1] = f.y, o[e + 2] = f.z, o[e + 3] = f.w;
                 }
                 pa::tc::wait_ld();
+                if (i0 + 16 == C) {
+                    pa::tc::fence_before();
+                    signal(o_free);
+                }
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    o[i0 + e] = fmaf(o[i0 + e], __uint_as_float(x2[e]), a.p.scale * __uint_as_float(x1[e]));
-            }
-            pa::tc::fence_before();
-            signal(o_free);
-#pragma unroll
-            for (int i0 = 0; i0 < C; i0 += 16) {
-                float got[8];
+                    o[e] = fmaf(o[e], __uint_as_float(x2[e]), a.p.scale * __uint_as_float(x1[e]));
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int i = i0 + (e & 3) + 8 * (e >> 2);  // tokens i and i + 4
+                    const int i = (e & 3) + 8 * (e >> 2);  // tokens i and i + 4
                     got[e] = __shfl_xor_sync(pa::kFull, odd ? o[i] : o[i + 4], 1);
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int i = i0 + (e & 3) + 8 * (e >> 2);
+                    const int i = (e & 3) + 8 * (e >> 2);
                     const uint32_t v = odd ? pack_bf16(got[e], o[i + 4]) : pack_bf16(o[i], got[e]);
                     const uint32_t x = (odd ? 4 : 0) + (i & 3);  // token of 8: the swizzle's row
-                    *reinterpret_cast<uint32_t *>(to + (i - (i & 3)) * 128 + x * 128 + ((piece ^ x) << 4)) = v;
+                    *reinterpret_cast<uint32_t *>(to + (i0 + i - (i & 3)) * 128 + x * 128 + ((piece ^ x) << 4)) = v;
                 }
             }
             pa::fence_proxy_async();
