@@ -14,13 +14,12 @@
 //                   the key dimensions each): adds a chunk's K^T V' to it and gives
 //                   it to the next chunk's Q S as two bf16 terms in TMEM; in between
 //                   0, 1, 4, 5 (and 13) write P as two bf16 terms to shared memory, and
-//                   7 copies: a chunk's outputs out, the chunk after the ring's in
+//                   7 has the chunk after the ring's copied in
 //   warp 9          issues the tcgen05.mma
 //   warps 8, 10, 11 V' = l^(C-1-j) v_j as three bf16 terms in shared memory, 32 tokens at
 //                   a time (the other 32 are in use meanwhile).  P is made by warps of
 //                   schedulers 0 and 1, so 8 has a smaller share than 10 and 11
-//   warps 12-15     outputs, into the place of the chunk's q for a TMA store; without
-//                   outputs 13 has a quarter of V', and 15 copies
+//   warps 12-15     outputs; without outputs 13 has a quarter of V', and 15 copies
 // Outputs are computed transposed (lanes = value dimensions, columns = tokens), so the
 // state is an operand that lies in TMEM, where the threads that own it write it;
 // with tokens as lanes it would take 64 KB of shared memory.  Q K^T has its tokens
@@ -65,10 +64,9 @@ struct Lay {
     static constexpr int P_TERM = C * C * 2;
     static constexpr int OFF_P = OFF_VP + 3 * TILE;  // [buffer][term]
     static constexpr int OFF_BAR = OFF_P + 4 * P_TERM;
-    // full (k, v), q_full, ready (the outputs lie in the stage; without outputs: empty)
-    // [NST]; s1_full, s1_free, p_full, vp_full [2];
+    // full, empty [NST]; s1_full, s1_free, p_full, vp_full [2];
     // u_half, u_full, u_free, s_full, o1_done, o2_done, o_free, drain
-    static constexpr int N_BAR = 3 * NST + 8 + 8;
+    static constexpr int N_BAR = 2 * NST + 8 + 8;
     static constexpr int OFF_F = (OFF_BAR + N_BAR * 8 + 15) / 16 * 16;  // scale l^(i+1)
     static constexpr int OFF_W = OFF_F + C * 4;        // l^(C-1-j), and of the last chunk
     static constexpr int OFF_D = OFF_W + 2 * C * 4;    // l^x, x = 1 - C .. C - 1 (1 below 0)
@@ -151,7 +149,7 @@ __device__ __forceinline__ Work find_work(const ChunkParams &a) {
     return w;
 }
 
-// The chunk of tokens t0 .. of head h into shared memory, completing on `bar`; and out.
+// The chunk of tokens t0 .. of head h into shared memory, completing on `bar`.
 __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, int h, int t0, uint64_t *bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
@@ -159,14 +157,6 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, 
         "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(h), "r"(t0), "r"(pa::smem_u32(bar))
         : "memory");
 }
-__device__ __forceinline__ void store_rows(const CUtensorMap *map, int h, int t0, uint32_t src) {
-    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %1}], [%4];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(0), "r"(h), "r"(t0), "r"(src)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-
 // x as two or three bf16 terms, two values at a time
 __device__ __forceinline__ uint32_t take_bf16(float2 &x) {
     const uint32_t t = pack_bf16(x.x, x.y);
@@ -177,8 +167,7 @@ __device__ __forceinline__ uint32_t take_bf16(float2 &x) {
 template <int D, bool SUM>
 __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
     chunk_kernel(const ChunkParams a, const __grid_constant__ CUtensorMap qmap,
-                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                 const __grid_constant__ CUtensorMap omap) {
+                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     using L = Lay<D>;
     constexpr int NST = L::NST;
     extern __shared__ uint8_t smem_raw[];
@@ -186,7 +175,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s0 = pa::smem_u32(smem);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
-    uint64_t *full = bars, *q_full = full + NST, *ready = q_full + NST, *s1_full = ready + NST, *s1_free = s1_full + 2,
+    uint64_t *full = bars, *empty = full + NST, *s1_full = empty + NST, *s1_free = s1_full + 2,
              *p_full = s1_free + 2, *vp_full = p_full + 2, *u_half = vp_full + 2, *u_full = u_half + 1, *u_free = u_full + 1,
              *s_full = u_free + 1, *o1_done = s_full + 1, *o2_done = o1_done + 1, *o_free = o2_done + 1,
              *drain = o_free + 1;
@@ -198,12 +187,11 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
 
     // ---- set-up: barriers, TMEM ------------------------------------------------
     if (tid == 0) {
-        for (const CUtensorMap *map : {&qmap, &kmap, &vmap, &omap})
+        for (const CUtensorMap *map : {&qmap, &kmap, &vmap})
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
         for (int i = 0; i < NST; ++i) {
             pa::mbar_init(&full[i], 1);
-            pa::mbar_init(&q_full[i], 1);
-            pa::mbar_init(&ready[i], SUM ? 1 : L::LANE_WARPS);
+            pa::mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             pa::mbar_init(&s1_full[i], 1);
@@ -247,7 +235,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
     __syncthreads();
     pa::tc::fence_after();
     const uint32_t tmem = *tslot;
-    int loads_issued = 0, q_issued = 0;
+    int loads_issued = 0;
     auto signal = [&](uint64_t *bar) {  // one arrival per warp, behind its writes
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
@@ -256,47 +244,31 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
     constexpr int LOAD_WARP = SUM ? 15 : 7;
     // Copies of chunk c into its stage (that warp).  Whole tiles of 64 tokens: rows past the
     // work's tokens are other tokens' (or zeros past the last), see below.
-    auto load_kv = [&](int c) {
+    auto load = [&](int c) {
+        constexpr int FIRST = SUM ? 1 : 0;  // (no q)
         const int st = c % NST;
         if (lane == 0) {
-            pa::mbar_arrive_expect_tx(&full[st], 2 * L::TILE);
+            pa::mbar_arrive_expect_tx(&full[st], (3 - FIRST) * L::TILE);
             ++loads_issued;
-            load_rows(s0 + st * L::STAGE + L::TILE, &kmap, w.h, w.t0 + c * C, &full[st]);
-            load_rows(s0 + st * L::STAGE + 2 * L::TILE, &vmap, w.h, w.t0 + c * C, &full[st]);
+#pragma unroll
+            for (int x = FIRST; x < 3; ++x)
+                load_rows(s0 + st * L::STAGE + x * L::TILE, x == 0 ? &qmap : x == 1 ? &kmap : &vmap, w.h, w.t0 + c * C,
+                          &full[st]);
         }
         __syncwarp();
     };
-    auto load_q = [&](int c) {
-        const int st = c % NST;
-        if (lane == 0) {
-            pa::mbar_arrive_expect_tx(&q_full[st], L::TILE);
-            ++q_issued;
-            load_rows(s0 + st * L::STAGE, &qmap, w.h, w.t0 + c * C, &q_full[st]);
+    // The loads behind the ring's first, by a warp that does nothing else.
+    auto load_all = [&]() {
+        for (int c = NST; c < nc; ++c) {
+            if (!wait_all(&empty[c % NST], ((c / NST) - 1) & 1)) {
+                *fail = 1;
+                break;
+            }
+            load(c);
         }
-        __syncwarp();
-    };
-    // The outputs of chunk c out of its stage, and q of the chunk after the ring's into
-    // it.  (k and v of that chunk need not wait for the outputs: for D = 128 this warp
-    // sees the end of the chunk's products by itself.)  The last chunk's rows may end
-    // inside the tile, then the output warps have written them.
-    auto turn = [&](int c) {
-        if (c + 1 == nc && rest < C) return true;
-        if (!wait_all(&ready[c % NST], (c / NST) & 1)) return false;
-        const bool more = c + NST < nc;
-        if (D == 64 && more) load_kv(c + NST);
-        if (lane == 0) {
-            store_rows(&omap, w.h, w.t0 + c * C, s0 + (c % NST) * L::STAGE);
-            if (more) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        }
-        __syncwarp();
-        if (more) load_q(c + NST);
-        return true;
     };
     if (warp == LOAD_WARP)
-        for (int c = 0; c < min(nc, NST); ++c) {
-            load_kv(c);
-            if (!SUM) load_q(c);
-        }
+        for (int c = 0; c < min(nc, NST); ++c) load(c);
 
     // P of chunk c, columns j0 .. j1 (whole 16s): lane = token i of the chunk (warps whose
     // lanes are 0-63).  Of tokens 0-31 the columns from 32 on are 0 and stay so.
@@ -351,7 +323,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         // rows of 128 bytes, K-major; tokens as K (64 tokens per column block)
         const uint64_t row_major = pa::tc::sdesc(s0, 16, 1024), col_major = pa::tc::sdesc(s0, C * 128, 1024);
         auto issue_s1 = [&](int c) {
-            if (!wait_all(&full[c % NST], (c / NST) & 1) || !wait_all(&q_full[c % NST], (c / NST) & 1)) return false;
+            if (!wait_all(&full[c % NST], (c / NST) & 1)) return false;
             if (c >= 2 && !wait_all(&s1_free[c & 1], ((c >> 1) - 1) & 1)) return false;
             pa::tc::fence_after();
             if (pa::tc::elect_one()) {
@@ -387,7 +359,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                             pa::tc::mma_ss(tmem + L::U, vp + term * kTile + ((ks * 16 * 128) >> 4),
                                            k + ((ks * 16 * 128) >> 4), kIdU, ks + term > 0);
                     pa::tc::commit(half ? u_full : u_half);
-                    if (SUM && half) pa::tc::commit(&ready[c % NST]);
+                    if (SUM && half) pa::tc::commit(&empty[c % NST]);
                 }
                 __syncwarp();
             }
@@ -423,6 +395,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                             pa::tc::mma_ts(tmem + L::O2, tmem + L::S + term * (D / 2) + b * 32 + ks * 8,
                                            q + ((b * C * 128 + ks * 32) >> 4), kIdO2, b + ks + term > 0);
                 pa::tc::commit(o2_done);
+                if (D == 64) pa::tc::commit(&empty[c % NST]);
             }
             __syncwarp();
         }
@@ -490,16 +463,13 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                 if (!SUM && c + 1 < nc) {
                     // (the place of this P was read before the last Q S)
                     if (has_p) ok = make_p(c + 1, j0, j0 + 16);
-                    if (warp == LOAD_WARP && c > 0) ok = turn(c - 1);
                     ok = ok && wait_all(o2_done, c & 1);  // the last Q S has read its state
                     if (!ok) break;
                     pa::tc::fence_after();
-                    if (warp == LOAD_WARP && c + NST < nc) load_kv(c + NST);
+                    if (warp == LOAD_WARP && c + NST < nc) load(c + NST);
                     give();
                 }
             }
-            if (!SUM && ok && warp == LOAD_WARP)
-                for (int c = max(0, nc - 2); c < nc && ok; ++c) ok = turn(c);
             if (!ok) *fail = 1;
             else if (w.to && nc > 0) {
 #pragma unroll
@@ -509,11 +479,8 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                 }
             }
         } else if (!SUM && warp == LOAD_WARP) {  // (D = 64)
-            bool ok = true;
-            for (int c = 0; c < nc && ok; ++c) ok = turn(c);
-            if (!ok) *fail = 1;
+            load_all();
         }
-        if (!SUM && warp == LOAD_WARP && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else if (warp < 12 || (SUM && warp == 13)) {
         // ---------------- V' ----------------
         // 16 bytes at a time, at the same place of the tile: whatever the swizzle, byte
@@ -588,29 +555,22 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         }
         if (!ok) *fail = 1;
     } else if (SUM) {
-        for (int c = NST; c < nc && warp == LOAD_WARP; ++c) {  // (one warp: 12 and 14 are idle)
-            if (!wait_all(&ready[c % NST], ((c / NST) - 1) & 1)) {
-                *fail = 1;
-                break;
-            }
-            load_kv(c);
-        }
+        if (warp == LOAD_WARP) load_all();  // (12 and 14 are idle)
     } else if (warp < 12 + L::LANE_WARPS) {
         // ---------------- outputs ----------------
         const int lw = warp & 3, row = lw * 32 + lane;
         const uint32_t base = tmem + (static_cast<uint32_t>(lw * 32) << 16);
+        const int64_t step = static_cast<int64_t>(a.p.H) * D;
         bool ok = true;
         auto put_o = [&](int c) {  // row = value dimension
             if (!wait_all(o1_done, c & 1) || !wait_all(o2_done, c & 1)) return false;
             pa::tc::fence_after();
-            const int m = c + 1 < nc ? C : rest;
-            const uint32_t tile = s0 + (c % NST) * L::STAGE;  // of q, which has been used
-            // Lanes 2 x and 2 x + 1 trade: the even one writes both dimensions of token
-            // i, the odd one of token i + 4, whose 16-byte pieces the swizzle puts
-            // into the other banks.
-            uint8_t *to = smem + (c % NST) * L::STAGE + (row >> 6) * (C * 128) + (row & 6) * 2;
-            const uint32_t piece = (row & 63) >> 3;
+            // Lanes 2 x and 2 x + 1 trade: the even one writes both dimensions of token i,
+            // the odd one of token i + 4, 16 lanes 64 bytes.
             const bool odd = lane & 1;
+            const int m = (c + 1 < nc ? C : rest) - (odd ? 4 : 0);
+            __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.p.out) +
+                                (static_cast<int64_t>(w.t0 + c * C + (odd ? 4 : 0)) * a.p.H + w.h) * D + (row & ~1);
 #pragma unroll 1
             for (int i0 = 0; i0 < C; i0 += 16) {
                 uint32_t x1[16], x2[16];
@@ -639,19 +599,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                 for (int e = 0; e < 8; ++e) {
                     const int i = (e & 3) + 8 * (e >> 2);
                     const uint32_t v = odd ? pack_bf16(got[e], o[i + 4]) : pack_bf16(o[i], got[e]);
-                    const uint32_t x = (odd ? 4 : 0) + (i & 3);  // token of 8: the swizzle's row
-                    *reinterpret_cast<uint32_t *>(to + (i0 + i - (i & 3)) * 128 + x * 128 + ((piece ^ x) << 4)) = v;
-                }
-            }
-            pa::fence_proxy_async();
-            signal(&ready[c % NST]);
-            if (m < C) {  // the last chunk's rows end inside the tile: copied here
-                if (!wait_all(&ready[c % NST], (c / NST) & 1)) return false;
-                for (int x = tid - 12 * 32; x < m * (D / 8); x += L::LANE_WARPS * 32) {
-                    const int i = x / (D / 8), ch = x % (D / 8);
-                    const uint4 v = pa::lds128(tile + (ch >> 3) * (C * 128) + i * 128 + (((ch & 7) ^ (i & 7)) << 4));
-                    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.p.out) +
-                                               (static_cast<int64_t>(w.t0 + c * C + i) * a.p.H + w.h) * D + ch * 8) = v;
+                    if (i0 + i < m) *reinterpret_cast<uint32_t *>(to + (i0 + i) * step) = v;
                 }
             }
             return true;
@@ -678,10 +626,8 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
             (void)pa::mbar_wait(drain, 0);
         }
         if (warp == LOAD_WARP && lane == 0)
-            for (int st = 0; st < NST; ++st) {
-                if (st < loads_issued) (void)pa::mbar_wait(&full[st], (loads_issued - 1 - st) / NST & 1);
-                if (st < q_issued) (void)pa::mbar_wait(&q_full[st], (q_issued - 1 - st) / NST & 1);
-            }
+            for (int st = 0; st < NST && st < loads_issued; ++st)  // the last into each stage
+                (void)pa::mbar_wait(&full[st], (loads_issued - 1 - st) / NST & 1);
         pa::tc::fence_before();
         __syncthreads();
     }
@@ -764,17 +710,16 @@ int launch(const ChunkParams &a, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0}, done_sum{0};
     if (int rc = set_smem_once(chunk_kernel<D, false>, L::SMEM, &done)) return rc;
     if (int rc = set_smem_once(chunk_kernel<D, true>, L::SMEM, &done_sum)) return rc;
-    CUtensorMap q, k, v, o;
+    CUtensorMap q, k, v;
     if (int rc = pa::encode_rows_map(&q, a.p.q, a.p.T, a.p.q_stride, a.p.H, D, C)) return rc;
     if (int rc = pa::encode_rows_map(&k, a.p.k, a.p.T, a.p.k_stride, a.p.H, D, C)) return rc;
     if (int rc = pa::encode_rows_map(&v, a.p.v, a.p.T, a.p.v_stride, a.p.H, D, C)) return rc;
-    if (int rc = pa::encode_rows_map(&o, a.p.out, a.p.T, int64_t(a.p.H) * D, a.p.H, D, C)) return rc;
     const int64_t ctas = int64_t(a.seg ? a.slots : a.p.R) * a.p.H;
     if (a.seg) {
-        if (int rc = go(chunk_kernel<D, true>, ctas, L::THREADS, L::SMEM, stream, a, q, k, v, o)) return rc;
+        if (int rc = go(chunk_kernel<D, true>, ctas, L::THREADS, L::SMEM, stream, a, q, k, v)) return rc;
         if (int rc = go(chain_kernel<D>, int64_t(a.p.R) * a.p.H * (D * D / 4 / 256), 256, 0, stream, a)) return rc;
     }
-    return go(chunk_kernel<D, false>, ctas, L::THREADS, L::SMEM, stream, a, q, k, v, o);
+    return go(chunk_kernel<D, false>, ctas, L::THREADS, L::SMEM, stream, a, q, k, v);
 }
 
 }  // namespace
