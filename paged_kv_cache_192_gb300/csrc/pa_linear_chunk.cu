@@ -514,41 +514,52 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                     }
                     __syncwarp();  // (a lane reads back what it wrote)
                 }
+                // Two pieces at once, the next two on their way (an odd last one twice).
                 uint4 v[2];
                 float f[2];
-                auto fetch = [&](int k, int to) {
-                    const int x = place(half, min(k, mine - 1));
-                    v[to] = pa::lds128(vt + x);
-                    f[to] = wt[(x >> 7) & (C - 1)];
+                auto fetch = [&](int k0) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int x = place(half, min(k0 + k, mine - 1));
+                        v[k] = pa::lds128(vt + x);
+                        f[k] = wt[(x >> 7) & (C - 1)];
+                    }
                 };
-                fetch(0, 0);
+                fetch(0);
                 if (c > 0) ok = wait_all(half ? u_full : u_half, (c - 1) & 1);
                 if (!ok) break;
                 // (not unrolled further: the roles' loops together have to stay near the
                 // instruction caches)
 #pragma unroll 1
-                for (int k0 = 0; k0 < mine; k0 += 2)
+                for (int k0 = 0; k0 < mine; k0 += 2) {
+                    float2 y[2][4];
+                    uint32_t t[2][3][4];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        fetch(k0 + k + 1, k ^ 1);
-                        if (k0 + k >= mine) break;
-                        float2 y[4];
-                        pa::Elem<__nv_bfloat16>::unpack(v[k], y);
-                        uint32_t t[3][4];
+                        pa::Elem<__nv_bfloat16>::unpack(v[k], y[k]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            y[e] = __fmul2_rn(y[e], make_float2(f[k], f[k]));
-                            t[0][e] = take_bf16(y[e]);
-                            t[1][e] = take_bf16(y[e]);
-                            t[2][e] = pack_bf16(y[e].x, y[e].y);
+                        for (int e = 0; e < 4; ++e) y[k][e] = __fmul2_rn(y[k][e], make_float2(f[k], f[k]));
+                    }
+                    fetch(k0 + 2);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            t[k][0][e] = take_bf16(y[k][e]);
+                            t[k][1][e] = take_bf16(y[k][e]);
+                            t[k][2][e] = pack_bf16(y[k][e].x, y[k][e].y);
                         }
-                        const uint32_t at = s0 + L::OFF_VP + place(half, k0 + k);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t at = s0 + L::OFF_VP + place(half, min(k0 + k, mine - 1));
 #pragma unroll
                         for (int term = 0; term < 3; ++term)
                             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + term * L::TILE),
-                                         "r"(t[term][0]), "r"(t[term][1]), "r"(t[term][2]), "r"(t[term][3])
+                                         "r"(t[k][term][0]), "r"(t[k][term][1]), "r"(t[k][term][2]),
+                                         "r"(t[k][term][3])
                                          : "memory");
                     }
+                }
                 pa::fence_proxy_async();
                 signal(&vp_full[half]);
             }
