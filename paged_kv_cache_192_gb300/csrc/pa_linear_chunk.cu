@@ -490,6 +490,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         constexpr int MOST = PIECES / 32 * (SUM ? 4 : 6) / 16;  // per thread: 4 of 16 parts each, or 4, 6 and 6
         const int part = SUM ? (warp == 13 ? 12 : (warp - 8 - (warp > 8)) * 4) : warp == 8 ? 0 : warp == 10 ? 4 : 10;
         const int mine = SUM || warp > 8 ? MOST : PIECES / 32 * 4 / 16, first = PIECES / 16 * part + lane;
+        constexpr int NB = SUM && D == 128 ? 4 : 2;
         // byte offset of a thread's k-th piece
         auto place = [&](int half, int k) {
             const int y = first + k * 32;
@@ -514,12 +515,12 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                     }
                     __syncwarp();  // (a lane reads back what it wrote)
                 }
-                // Two pieces at once, the next two on their way (an odd last one twice).
-                uint4 v[2];
-                float f[2];
+                // NB pieces at once, the next on their way (the last of an odd number twice).
+                uint4 v[NB];
+                float f[NB];
                 auto fetch = [&](int k0) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                    for (int k = 0; k < NB; ++k) {
                         const int x = place(half, min(k0 + k, mine - 1));
                         v[k] = pa::lds128(vt + x);
                         f[k] = wt[(x >> 7) & (C - 1)];
@@ -531,26 +532,26 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                 // (not unrolled further: the roles' loops together have to stay near the
                 // instruction caches)
 #pragma unroll 1
-                for (int k0 = 0; k0 < mine; k0 += 2) {
-                    float2 y[2][4];
-                    uint32_t t[2][3][4];
+                for (int k0 = 0; k0 < mine; k0 += NB) {
+                    float2 y[NB][4];
+                    uint32_t t[NB][3][4];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                    for (int k = 0; k < NB; ++k) {
                         pa::Elem<__nv_bfloat16>::unpack(v[k], y[k]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) y[k][e] = __fmul2_rn(y[k][e], make_float2(f[k], f[k]));
                     }
-                    fetch(k0 + 2);
+                    fetch(k0 + NB);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
+                        for (int k = 0; k < NB; ++k) {
                             t[k][0][e] = take_bf16(y[k][e]);
                             t[k][1][e] = take_bf16(y[k][e]);
                             t[k][2][e] = pack_bf16(y[k][e].x, y[k][e].y);
                         }
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                    for (int k = 0; k < NB; ++k) {
                         const uint32_t at = s0 + L::OFF_VP + place(half, min(k0 + k, mine - 1));
 #pragma unroll
                         for (int term = 0; term < 3; ++term)
@@ -741,11 +742,26 @@ namespace lin {
 Segments segments_for(int R, int T, int max_query_len, int H) {
     Segments s{0, 0};
     constexpr int kSMs = 152;
-    const int64_t pairs = int64_t(R) * H;
-    if (pairs >= 2 * kSMs || max_query_len < 16 * C) return s;
-    // (to be measured)
-    s.tokens = 1024;
-    s.slots = static_cast<int>(int64_t(T) / s.tokens + R);
+    // In chunks: a CTA costs about OVERHEAD besides its own (set-up, state in and out),
+    // the launch that sums the segments SUM of one that does it all, and the launches
+    // between them LAUNCHES.  Waves are counted as if the tokens were spread evenly; the
+    // longest request sets how many chunks follow one another.
+    constexpr double OVERHEAD = 8, SUM = 0.6, LAUNCHES = 6;
+    const int64_t pairs = int64_t(R) * H, most = (int64_t(max_query_len) + C - 1) / C;
+    const double all = (double(T) / C + 0.5 * R) * H / kSMs;  // chunks per SM
+    auto waves = [&](double ctas) { return std::ceil(ctas / kSMs); };
+    double best = std::max(double(most + OVERHEAD), all + waves(double(pairs)) * OVERHEAD);
+    for (int64_t n = 2; n <= 64 && 2 * n <= most; ++n) {
+        const int64_t chunks = (most + n - 1) / n;
+        const double ctas = (double(T) / (C * chunks) + (R > 1 ? 0.5 * R : 0.0)) * H;
+        const double cost = waves(ctas) * (chunks + OVERHEAD) + SUM * waves(ctas - double(pairs)) * (chunks + OVERHEAD) +
+                            LAUNCHES;
+        if (cost < best) {
+            best = cost;
+            s.tokens = static_cast<int>(chunks * C);
+        }
+    }
+    if (s.tokens) s.slots = static_cast<int>(int64_t(T) / s.tokens + R);
     return s;
 }
 
