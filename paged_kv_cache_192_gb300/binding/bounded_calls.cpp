@@ -127,6 +127,15 @@ struct Place {
     at::Tensor new_like(const at::Tensor &t) const {
         return at::Tensor(at::detail::empty_cuda(t.sizes(), t.scalar_type(), t.device(), std::nullopt));
     }
+    // Part of `all`, from byte `at` on.
+    static at::Tensor part(const at::Tensor &all, int64_t at, std::initializer_list<int64_t> dims,
+                           at::ScalarType type) {
+        at::Tensor t = at::detail::make_tensor<at::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                               c10::scalarTypeToTypeMeta(type));
+        t.unsafeGetTensorImpl()->set_storage_offset(at / static_cast<int64_t>(c10::elementSize(type)));
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(at::IntArrayRef(dims.begin(), dims.size()));
+        return t;
+    }
     at::Tensor new_empty(std::initializer_list<int64_t> dims, at::ScalarType type) const {
         return at::Tensor(at::detail::empty_cuda(at::IntArrayRef(dims.begin(), dims.size()), type,
                                                  c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(device)),
@@ -409,11 +418,15 @@ PyObject *plan_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
              *rp = place(ring, "free_pages", at::kInt), *sp = place(state, "free_state", at::kInt);
         const void *ip = place(ids, "seq_ids", at::kInt), *cp = place(change, "new_tokens", at::kInt);
         if (!given) {
-            out[0] = place.new_empty({R, W}, at::kInt);
-            out[1] = place.new_empty({R}, at::kInt);
-            out[2] = place.new_empty({R + 1}, at::kInt);
-            out[3] = place.new_empty({max_tokens}, at::kLong);
-            out[4] = place.new_empty({max_tokens}, at::kLong);
+            // one allocation (each takes as long as the rest of the call), parts on 16 bytes
+            auto whole = [](int64_t bytes) { return (bytes + 15) & ~int64_t(15); };
+            const int64_t tokens = whole(8 * int64_t(max_tokens)), table = whole(4 * R * W), lens_b = whole(4 * R);
+            const at::Tensor all = place.new_empty({(2 * tokens + table + lens_b + whole(4 * (R + 1))) / 8}, at::kLong);
+            out[3] = Place::part(all, 0, {max_tokens}, at::kLong);
+            out[4] = Place::part(all, tokens, {max_tokens}, at::kLong);
+            out[0] = Place::part(all, 2 * tokens, {R, W}, at::kInt);
+            out[1] = Place::part(all, 2 * tokens + table, {R}, at::kInt);
+            out[2] = Place::part(all, 2 * tokens + table + lens_b, {R + 1}, at::kInt);
         }
         void *op[5];
         const char *names[5] = {"block_table", "context_lens", "query_start", "slots", "positions"};

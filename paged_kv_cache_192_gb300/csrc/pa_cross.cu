@@ -25,6 +25,7 @@ using namespace pa::dec;
 
 constexpr int kNW = 4;  // warps per CTA
 constexpr int kMaxCluster = 16;
+constexpr int kSortedR = 256;  // requests that a CTA puts in order
 constexpr int kMaxCols = 32;  // rows of a (request, KV head) that the streaming kernel takes
 
 struct CrossParams {
@@ -34,6 +35,7 @@ struct CrossParams {
     int *err;
     int64_t num_blocks;
     int R, T, Hq, Hkv, gq_log2, bs, bs_log2, MB;
+    bool sorted;   // more CTAs than run at once: long requests first
     float qscale;  // scale * log2(e)
 };
 
@@ -73,7 +75,8 @@ __global__ void __launch_bounds__(kNW * 32, (CLayout<D, NG>::MINB))
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::OFF_BAR) + warp * NST;
     float2 *wml = reinterpret_cast<float2 *>(smem + Lay::OFF_WML);
     const int C = cluster_nctarank(), rank = cluster_ctarank();
-    const int item = blockIdx.x / C, r = item / p.Hkv, hk = item % p.Hkv;
+    const int item = blockIdx.x / C, hk = item % p.Hkv;
+    int r = item / p.Hkv;
     if (lane == 0) {
         for (int s = 0; s < NST; ++s) pa::mbar_init(&bars[s], 1);
         pa::fence_barrier_init();
@@ -82,6 +85,19 @@ __global__ void __launch_bounds__(kNW * 32, (CLayout<D, NG>::MINB))
     if (C > 1) cluster_arrive();  // this CTA runs: the others may write to it (waited for below)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (p.sorted) {
+        // requests with the most states first: the r-th in that order
+        __shared__ int lens[kSortedR], found;
+        for (int i = threadIdx.x; i < p.R; i += kNW * 32) lens[i] = p.encoder_lens[i];
+        __syncthreads();
+        for (int i = threadIdx.x; i < p.R; i += kNW * 32) {
+            int rank = 0;
+            for (int x = 0; x < p.R; ++x) rank += lens[x] > lens[i] || (lens[x] == lens[i] && x < i);
+            if (rank == r) found = i;
+        }
+        __syncthreads();
+        r = found;
+    }
 
     const int qs = p.query_start[r], n = p.query_start[r + 1] - qs, cap = p.MB << p.bs_log2;
     int L = p.encoder_lens[r];
@@ -249,21 +265,21 @@ __global__ void __launch_bounds__(kNW * 32, (CLayout<D, NG>::MINB))
 }
 
 template <int D, int NG>
-int launch_rows(const CrossParams &p, const void *k_cache, const void *v_cache, cudaStream_t stream) {
+int launch_rows(const CrossParams &p0, const void *k_cache, const void *v_cache, cudaStream_t stream) {
     using Lay = CLayout<D, NG>;
     auto kern = cross_rows_kernel<D, NG>;
     static std::atomic<uint64_t> done{0};
     if (int rc = pa::pf::set_smem_once(kern, Lay::SMEM, &done)) return rc;
     CUtensorMap kmap, vmap;
-    const int64_t rows = (p.num_blocks * p.Hkv) << p.bs_log2;
-    const int box = std::min(Lay::TT, p.bs);
+    const int64_t rows = (p0.num_blocks * p0.Hkv) << p0.bs_log2;
+    const int box = std::min(Lay::TT, p0.bs);
     if (int rc = pa::encode_pool_map(&kmap, k_cache, rows, D, box)) return rc;
     if (int rc = pa::encode_pool_map(&vmap, v_cache, rows, D, box)) return rc;
     // Cluster size: the largest that leaves every warp two tiles and all clusters
     // running at once (as in the windowed decode: a second wave costs more than the
     // split gains).
     static std::atomic<int> cache[64][5];
-    const int64_t items = int64_t(p.R) * p.Hkv, tiles = (int64_t(p.MB) << p.bs_log2) / Lay::TT;
+    const int64_t items = int64_t(p0.R) * p0.Hkv, tiles = (int64_t(p0.MB) << p0.bs_log2) / Lay::TT;
     int c = 1;
     while (c < kMaxCluster && tiles >= 2 * kNW * 2 * c) {
         const int n = pa::pf::clusters_at_once(kern, kNW * 32, Lay::SMEM, 2 * c, cache);
@@ -271,6 +287,10 @@ int launch_rows(const CrossParams &p, const void *k_cache, const void *v_cache, 
         if (items > n) break;
         c *= 2;
     }
+    CrossParams p = p0;
+    const int at_once = pa::pf::clusters_at_once(kern, kNW * 32, Lay::SMEM, 1, cache);
+    if (at_once < 0) return pa::cuda_fail(cudaGetLastError(), "cross_attention: occupancy");
+    p.sorted = items > at_once && p.R > 1 && p.R <= kSortedR;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(items * c));
     cfg.blockDim = dim3(kNW * 32);

@@ -225,11 +225,13 @@ int launch_recurrent(const LinParams &p, int D, int dtype, cudaStream_t stream) 
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return cuda_fail(cudaGetLastError(), "linear attention: SM count");
-    // A few states leave SMs idle: then each is cut into slices of 32 columns.
+    // Columns per CTA: 64 (64 sequences of 32 heads, D 128: 42.4 us; 44.6 with 128, where
+    // two CTAs of an SM hold too few bytes on their way between loading and storing,
+    // 43.0 with 32).  A few states leave SMs idle: then 32.
     const bool cut = int64_t(p.R) * p.H < sms;
     auto go = [&](auto t) {
         using T = decltype(t);
-        if (D == 128) return cut ? launch<T, 128, 32>(p, stream) : launch<T, 128, 128>(p, stream);
+        if (D == 128) return cut ? launch<T, 128, 32>(p, stream) : launch<T, 128, 64>(p, stream);
         return cut ? launch<T, 64, 32>(p, stream) : launch<T, 64, 64>(p, stream);
     };
     return dtype == PA_BF16 ? go(__nv_bfloat16()) : go(float());

@@ -80,16 +80,27 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanParams p)
     // ---- the rows and their prefix sums ------------------------------------------
     const int first = p.state[0], count = p.state[1];
     Sums total{0, 0, 0};
-    for (int r0 = 0; r0 < p.R; r0 += kThreads) {
-        const int r = r0 + tid;
+    constexpr int PER = kMaxRows / kThreads;  // rows of a thread, their loads in two rounds
+    int id[PER], change[PER], len[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int r = k * kThreads + tid;
+        id[k] = r < p.R ? p.seq_ids[r] : -1;
+        change[k] = r < p.R ? p.change[r] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) len[k] = id[k] >= 0 && id[k] < p.S ? p.lens[id[k]] : 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        if (k * kThreads >= p.R) break;
+        const int r = k * kThreads + tid;
         Row row{-1, 0, 0, 0, 0, 0};
         Sums x{0, 0, 0};
         if (r < p.R) {
-            const int s = p.seq_ids[r], c = p.change[r];
+            const int s = id[k], c = change[k], L = len[k];
             if (s >= p.S) {
                 atomicOr(&bad, PA_DEVERR_BAD_REQUEST);
             } else if (s >= 0) {
-                const int L = p.lens[s];
                 if (L < 0 || blocks(L) > p.MB || atomicOr(&seen[s >> 5], 1u << (s & 31)) >> (s & 31) & 1) {
                     atomicOr(&bad, PA_DEVERR_BAD_REQUEST);
                 } else {
@@ -151,53 +162,60 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanParams p)
     }
     auto wrap = [&](int i) { return i >= p.NB ? i - p.NB : i; };  // (sums of two numbers up to NB)
 
-    // ---- tables: a warp per 128 entries of a row -----------------------------------
+    // ---- tables and tokens: units of a warp, two at a time so that their loads overlap --
+    // Unit u: 128 entries of a row, u < p.R * chunks; then 32 tokens.
     const int chunks = (max(p.MB, p.W) + 127) / 128;
-    const int nwarps = gridDim.x * kWarps, gw = blockIdx.x * kWarps + warp;
-    int r = gw / chunks, ch = gw % chunks;
-    const int dr = nwarps / chunks, dch = nwarps % chunks;
-    while (r < p.R) {
-        const Row row = rows[r];
-        const int b0 = blocks(row.old_len), b1 = blocks(row.new_len);
-        const int j0 = ch * 128 + lane * 4;
-        int32_t *held = p.pages + static_cast<int64_t>(max(row.seq, 0)) * p.MB;
-        int v[4];
-        if (p.vec && j0 < b0) {  // (j0 + 3 < MB: rows are whole 16-byte pieces)
-            const int4 h = *reinterpret_cast<const int4 *>(held + j0);
-            v[0] = h.x, v[1] = h.y, v[2] = h.z, v[3] = h.w;
-        } else {
+    const int64_t table_units = static_cast<int64_t>(p.R) * chunks, units = table_units + (p.max_tokens + 31) / 32;
+    const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
+    struct Part {  // lane's four entries j0 .. of row r, the pages held there
+        int r, j0, v[4];
+        bool on;
+    };
+    auto fetch = [&](int64_t u) {
+        Part t;
+        t.on = u < table_units;
+        if (t.on) {
+            t.r = static_cast<int>(table_units <= 0x7fffffff ? static_cast<unsigned>(u) / static_cast<unsigned>(chunks) : u / chunks);
+            t.j0 = static_cast<int>(u - static_cast<int64_t>(t.r) * chunks) * 128 + lane * 4;
+            const int b0 = blocks(rows[t.r].old_len);
+            const int32_t *held = p.pages + static_cast<int64_t>(max(rows[t.r].seq, 0)) * p.MB;
+            if (p.vec && t.j0 < b0) {  // (j0 + 3 < MB: rows are whole 16-byte pieces)
+                const int4 h = *reinterpret_cast<const int4 *>(held + t.j0);
+                t.v[0] = h.x, t.v[1] = h.y, t.v[2] = h.z, t.v[3] = h.w;
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = j0 + e < b0 ? held[j0 + e] : 0;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int j = j0 + e;
-            if (j >= b0 && j < b1) {
-                v[e] = p.ring[wrap(first + static_cast<int>(row.taken) + j - b0)];
-                held[j] = v[e];
-            } else if (j >= b1) {
-                if (j < b0) p.ring[wrap(wrap(first + count) + static_cast<int>(row.given) + j - b1)] = v[e];
-                v[e] = 0;
+                for (int e = 0; e < 4; ++e) t.v[e] = t.j0 + e < b0 ? held[t.j0 + e] : 0;
             }
         }
-        int32_t *out = p.table + static_cast<int64_t>(r) * p.W;
+        return t;
+    };
+    auto finish = [&](Part &t) {
+        if (!t.on) return;
+        const Row row = rows[t.r];
+        const int b0 = blocks(row.old_len), b1 = blocks(row.new_len);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = t.j0 + e;
+            if (j >= b0 && j < b1) {
+                t.v[e] = p.ring[wrap(first + static_cast<int>(row.taken) + j - b0)];
+                p.pages[static_cast<int64_t>(row.seq) * p.MB + j] = t.v[e];
+            } else if (j >= b1) {
+                if (j < b0) p.ring[wrap(wrap(first + count) + static_cast<int>(row.given) + j - b1)] = t.v[e];
+                t.v[e] = 0;
+            }
+        }
+        int32_t *out = p.table + static_cast<int64_t>(t.r) * p.W;
         if (p.vec) {
-            if (j0 < p.W) *reinterpret_cast<int4 *>(out + j0) = make_int4(v[0], v[1], v[2], v[3]);
+            if (t.j0 < p.W) *reinterpret_cast<int4 *>(out + t.j0) = make_int4(t.v[0], t.v[1], t.v[2], t.v[3]);
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (j0 + e < p.W) out[j0 + e] = v[e];
+                if (t.j0 + e < p.W) out[t.j0 + e] = t.v[e];
         }
-        r += dr;
-        ch += dch;
-        if (ch >= chunks) {
-            ch -= chunks;
-            ++r;
-        }
-    }
-    // ---- tokens -------------------------------------------------------------------
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + tid; t < p.max_tokens;
-         t += static_cast<int64_t>(gridDim.x) * kThreads) {
+    };
+    auto token = [&](int64_t u) {
+        const int64_t t = (u - table_units) * 32 + lane;
+        if (u < table_units || t >= p.max_tokens) return;
         int64_t slot = -1, pos = 0;
         if (t < total.start) {
             int lo = 0, hi = p.R - 1;  // the last row that starts at t or before: it has tokens
@@ -217,6 +235,14 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanParams p)
         }
         p.slots[t] = slot;
         p.positions[t] = pos;
+    };
+    // (CTA by CTA, so that a small step's units lie on different SMs)
+    for (int64_t u = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x; u < units; u += 2 * nwarps) {
+        Part t0 = fetch(u), t1 = fetch(u + nwarps);
+        finish(t0);
+        finish(t1);
+        token(u);
+        if (u + nwarps < units) token(u + nwarps);
     }
     if (blockIdx.x == 0) {
         for (int i = tid; i < p.R; i += kThreads) {

@@ -33,6 +33,7 @@ struct WinParams {
 struct ReqTables {
     int pre[kMaxR + 1];  // query tiles before request r
     int qs[kMaxR], n[kMaxR], L[kMaxR];
+    int row[kMaxR];  // CROSS: the request in this place
     int scan[12];
 };
 
@@ -100,16 +101,28 @@ struct Item {
 
 // The requests of a launch and the prefix sum of their query tiles of `qtok`
 // tokens into the tables; returns the number of tiles.  A request whose numbers
-// do not fit gets none.  Whole CTA of 12 warps; ends with a barrier.
+// do not fit gets none.  CROSS: in the order of their states' number, most first
+// (a long item that starts last would run alone at the end).  Whole CTA of 12 warps;
+// ends with a barrier.
 template <bool CROSS>
 __device__ __forceinline__ int read_requests(const WinParams &p, ReqTables &t, int qtok) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int carry = 0;
     for (int r0 = 0; r0 < p.R; r0 += 12 * 32) {
         const int r = r0 + tid;
-        int np = 0;
+        int np = 0, from = r;
+        if constexpr (CROSS) {  // (kMaxR requests: one round)
+            if (r < p.R) t.L[r] = p.context_lens[r];
+            __syncthreads();
+            int rank = 0;
+            if (r < p.R)
+                for (int x = 0; x < p.R; ++x) rank += t.L[x] > t.L[r] || (t.L[x] == t.L[r] && x < r);
+            if (r < p.R) t.row[rank] = r;
+            __syncthreads();
+            if (r < p.R) from = t.row[r];
+        }
         if (r < p.R) {
-            const int qs = p.query_start[r], n = p.query_start[r + 1] - qs, L = p.context_lens[r];
+            const int qs = p.query_start[from], n = p.query_start[from + 1] - qs, L = p.context_lens[from];
             if (n > 0 && qs >= 0 && n <= p.T - qs && L >= (CROSS ? 1 : n) && L <= p.MB << p.bs_log2)
                 np = (n + qtok - 1) / qtok;
             else if ((CROSS ? n < 0 || (n > 0 && (qs < 0 || n > p.T - qs)) : n != 0) || L < 0 || L > p.MB << p.bs_log2)
@@ -172,6 +185,7 @@ __device__ __forceinline__ Item make_item(const WinParams &p, const ReqTables &t
     it.qs = t.qs[lo];
     it.n = t.n[lo];
     if constexpr (CROSS) {
+        it.r = t.row[lo];
         it.P = it.lo = it.ns = it.wbase = 0;
         it.kv_end = t.L[lo];
         it.ntiles = (it.kv_end + kT2KT - 1) / kT2KT;
@@ -1049,7 +1063,21 @@ int launch(const WinParams &p, const void *q, const void *k_cache, const void *v
     const int sms = sm_count();
     if (sms <= 0) return pa::cuda_fail(cudaGetLastError(), "prefill_window: SM count");
     int64_t singles = 0;
-    if (runs_split(p.R, p.T, max_query_len, GQ, p.Hkv, sms, &singles)) {
+    bool split = runs_split(p.R, p.T, max_query_len, GQ, p.Hkv, sms, &singles);
+    if constexpr (CROSS) {
+        // More query tiles than SMs: the split kernel, one CTA per tile, where its waves
+        // take less.  A 64-state tile takes it half as long as the kernel below, which
+        // has two query tiles of its own for it; a CTA costs it about 10 such halves.
+        // 8 requests of 20 to 100 tokens (groups of 4) over 1,000 to 4,100 states: 46 us
+        // against 70; 4 of 2,048 tokens over 2,000 to 8,192: 667 below.
+        const int64_t tiles = (int64_t(p.MB) << p.bs_log2) / kT2KT + 1;
+        auto waves = [&](int64_t ctas) { return (ctas + sms - 1) / sms; };
+        // (half of the partly filled tiles, of which there may be one per request)
+        const int64_t partly = std::max<int64_t>(1, (int64_t(p.T) / (128 / GQ) + (p.R + 1) / 2) * p.Hkv);
+        split = split || (p.R <= kMaxR && waves(partly) * (tiles + 10) <
+                                              waves(query_tiles(p.R, p.T, max_query_len, 256 / GQ) * p.Hkv) * 2 * tiles);
+    }
+    if (split) {
         auto kern = prefill_window_split_kernel<D, GQ, CROSS>;
         static std::atomic<uint64_t> done{0};
         if (int rc = set_smem_once(kern, SLayout<D>::SMEM, &done)) return rc;

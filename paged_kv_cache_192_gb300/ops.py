@@ -524,8 +524,8 @@ def plan_step(state, seq_ids, new_tokens, block_size, max_tokens, table_blocks=N
     All or nothing: a step that does not fit is refused (free_state[3] counts it,
     the device error word says why) and shows the old lengths, no new token.
     out: a StepPlan to write into.  Returns the StepPlan."""
-    return StepPlan(*_calls().plan_step(state[0], state[1], state[2], state[3], seq_ids, new_tokens,
-                                        block_size, max_tokens, table_blocks, out, stream))
+    return tuple.__new__(StepPlan, _calls().plan_step(*state, seq_ids, new_tokens, block_size,
+                                                      max_tokens, table_blocks, out, stream))
 
 
 def cross_attention(q, k_cache, v_cache, block_table, query_start, encoder_lens, max_query_len,
