@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanParams p)
     }
     auto wrap = [&](int i) { return i >= p.NB ? i - p.NB : i; };  // (sums of two numbers up to NB)
 
-    // ---- tables and tokens: units of a warp, two at a time so that their loads overlap --
+    // ---- tables and tokens: units of a warp, some at once so that their loads overlap ----
+    constexpr int AT_ONCE = 2;
     // Unit u: 128 entries of a row, u < p.R * chunks; then 32 tokens.
     const int chunks = (max(p.MB, p.W) + 127) / 128;
     const int64_t table_units = static_cast<int64_t>(p.R) * chunks, units = table_units + (p.max_tokens + 31) / 32;
@@ -184,24 +185,27 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanParams p)
                 t.v[0] = h.x, t.v[1] = h.y, t.v[2] = h.z, t.v[3] = h.w;
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) t.v[e] = t.j0 + e < b0 ? held[t.j0 + e] : 0;
+                for (int e = 0; e < 4; ++e) t.v[e] = !p.vec && t.j0 + e < b0 ? held[t.j0 + e] : 0;
             }
         }
         return t;
     };
     auto finish = [&](Part &t) {
         if (!t.on) return;
-        const Row row = rows[t.r];
-        const int b0 = blocks(row.old_len), b1 = blocks(row.new_len);
+        const int b0 = blocks(rows[t.r].old_len), b1 = blocks(rows[t.r].new_len);
+        // (most entries are pages that stay, or lie behind the row's last)
+        if (t.j0 + 3 >= min(b0, b1) && t.j0 < max(b0, b1)) {
+            const Row row = rows[t.r];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int j = t.j0 + e;
-            if (j >= b0 && j < b1) {
-                t.v[e] = p.ring[wrap(first + static_cast<int>(row.taken) + j - b0)];
-                p.pages[static_cast<int64_t>(row.seq) * p.MB + j] = t.v[e];
-            } else if (j >= b1) {
-                if (j < b0) p.ring[wrap(wrap(first + count) + static_cast<int>(row.given) + j - b1)] = t.v[e];
-                t.v[e] = 0;
+            for (int e = 0; e < 4; ++e) {
+                const int j = t.j0 + e;
+                if (j >= b0 && j < b1) {
+                    t.v[e] = p.ring[wrap(first + static_cast<int>(row.taken) + j - b0)];
+                    p.pages[static_cast<int64_t>(row.seq) * p.MB + j] = t.v[e];
+                } else if (j >= b1) {
+                    if (j < b0) p.ring[wrap(wrap(first + count) + static_cast<int>(row.given) + j - b1)] = t.v[e];
+                    t.v[e] = 0;
+                }
             }
         }
         int32_t *out = p.table + static_cast<int64_t>(t.r) * p.W;
@@ -237,12 +241,14 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanParams p)
         p.positions[t] = pos;
     };
     // (CTA by CTA, so that a small step's units lie on different SMs)
-    for (int64_t u = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x; u < units; u += 2 * nwarps) {
-        Part t0 = fetch(u), t1 = fetch(u + nwarps);
-        finish(t0);
-        finish(t1);
-        token(u);
-        if (u + nwarps < units) token(u + nwarps);
+    for (int64_t u = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x; u < units; u += AT_ONCE * nwarps) {
+        Part t[AT_ONCE];
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) t[k] = fetch(u + k * nwarps);
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) finish(t[k]);
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k) token(u + k * nwarps);
     }
     if (blockIdx.x == 0) {
         for (int i = tid; i < p.R; i += kThreads) {
@@ -366,10 +372,11 @@ extern "C" int pa_plan_step(const int32_t *seq_ids, const int32_t *new_tokens, i
     static std::atomic<uint64_t> done{0};
     const size_t most = size_t(kMaxRows) * sizeof(Row) + kMaxSeqs / 8;
     if (int rc = pa::pf::set_smem_once(plan_step_kernel, most, &done)) return rc;
-    // a unit of each warp, at most two CTAs per SM
+    // a unit of each warp, at most a CTA per SM (1,024 rows of 2,048 entries: two CTAs per SM
+    // take 10 % longer, four 50 %: each makes all prefix sums)
     const int64_t units = int64_t(R) * ((std::max(p.MB, p.W) + 127) / 128) + max_tokens / 32;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(2 * sms, (units + kWarps - 1) / kWarps))));
+    cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(sms, (units + kWarps - 1) / kWarps))));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
