@@ -64,9 +64,9 @@ struct Lay {
     static constexpr int P_TERM = C * C * 2;
     static constexpr int OFF_P = OFF_VP + 3 * TILE;  // [buffer][term]
     static constexpr int OFF_BAR = OFF_P + 4 * P_TERM;
-    // full, empty [NST]; s1_full, s1_free, p_full, vp_full [2];
-    // u_half, u_full, u_free, s_full, o1_done, o2_done, o_free, drain
-    static constexpr int N_BAR = 2 * NST + 8 + 8;
+    // full, empty [NST]; s1_full, p_full, vp_full [2]; u_half, u_full, u_free, s_full,
+    // o_done, o_free, drain
+    static constexpr int N_BAR = 2 * NST + 6 + 7;
     static constexpr int OFF_F = (OFF_BAR + N_BAR * 8 + 15) / 16 * 16;  // scale l^(i+1)
     static constexpr int OFF_W = OFF_F + C * 4;        // l^(C-1-j), and of the last chunk
     static constexpr int OFF_D = OFF_W + 2 * C * 4;    // l^x, x = 1 - C .. C - 1 (1 below 0)
@@ -175,9 +175,9 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s0 = pa::smem_u32(smem);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
-    uint64_t *full = bars, *empty = full + NST, *s1_full = empty + NST, *s1_free = s1_full + 2,
-             *p_full = s1_free + 2, *vp_full = p_full + 2, *u_half = vp_full + 2, *u_full = u_half + 1, *u_free = u_full + 1,
-             *s_full = u_free + 1, *o1_done = s_full + 1, *o2_done = o1_done + 1, *o_free = o2_done + 1,
+    uint64_t *full = bars, *empty = full + NST, *s1_full = empty + NST,
+             *p_full = s1_full + 2, *vp_full = p_full + 2, *u_half = vp_full + 2, *u_full = u_half + 1, *u_free = u_full + 1,
+             *s_full = u_free + 1, *o_done = s_full + 1, *o_free = o_done + 1,
              *drain = o_free + 1;
     float *fdec = reinterpret_cast<float *>(smem + L::OFF_F), *wdec = reinterpret_cast<float *>(smem + L::OFF_W),
           *pdec = reinterpret_cast<float *>(smem + L::OFF_D) + C;
@@ -195,7 +195,6 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             pa::mbar_init(&s1_full[i], 1);
-            pa::mbar_init(&s1_free[i], 5);
             pa::mbar_init(&p_full[i], 5);
             pa::mbar_init(&vp_full[i], SUM ? 4 : 3);
         }
@@ -203,8 +202,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         pa::mbar_init(u_full, 1);
         pa::mbar_init(u_free, 2 * L::LANE_WARPS);
         pa::mbar_init(s_full, 2 * L::LANE_WARPS);
-        pa::mbar_init(o1_done, 1);
-        pa::mbar_init(o2_done, 1);
+        pa::mbar_init(o_done, 1);
         pa::mbar_init(o_free, L::LANE_WARPS);
         pa::mbar_init(drain, 1);
         *fail = 0;
@@ -307,7 +305,6 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
             }
         }
         pa::tc::fence_before();
-        signal(&s1_free[c & 1]);
         pa::fence_proxy_async();
         signal(&p_full[c & 1]);
         return true;
@@ -322,9 +319,11 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         constexpr uint32_t kStage = L::STAGE >> 4, kTile = L::TILE >> 4;
         // rows of 128 bytes, K-major; tokens as K (64 tokens per column block)
         const uint64_t row_major = pa::tc::sdesc(s0, 16, 1024), col_major = pa::tc::sdesc(s0, C * 128, 1024);
+        // The whole warp goes along and one lane issues: descriptors and waits stay uniform
+        // (one lane alone took 294 us for a prompt of 16,384 tokens instead of 219).  S1
+        // of a chunk is overwritten two chunks later, its P has been waited for by then.
         auto issue_s1 = [&](int c) {
             if (!wait_all(&full[c % NST], (c / NST) & 1)) return false;
-            if (c >= 2 && !wait_all(&s1_free[c & 1], ((c >> 1) - 1) & 1)) return false;
             pa::tc::fence_after();
             if (pa::tc::elect_one()) {
                 const uint64_t q = row_major + static_cast<uint32_t>((c % NST) * kStage), k = q + kTile;
@@ -378,7 +377,6 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                     for (int term = 0; term < 2; ++term)
                         pa::tc::mma_ss(tmem + L::O1, v + ((ks * 16 * 128) >> 4),
                                        p + ((term * L::P_TERM + ks * 32) >> 4), kIdO1, ks + term > 0);
-                pa::tc::commit(o1_done);
             }
             __syncwarp();
             ok = wait_all(s_full, c & 1);
@@ -394,7 +392,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                         for (int term = 0; term < 2; ++term)
                             pa::tc::mma_ts(tmem + L::O2, tmem + L::S + term * (D / 2) + b * 32 + ks * 8,
                                            q + ((b * C * 128 + ks * 32) >> 4), kIdO2, b + ks + term > 0);
-                pa::tc::commit(o2_done);
+                pa::tc::commit(o_done);  // (of O1 too: every product issued before)
                 if (D == 64) pa::tc::commit(&empty[c % NST]);
             }
             __syncwarp();
@@ -463,7 +461,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                 if (!SUM && c + 1 < nc) {
                     // (the place of this P was read before the last Q S)
                     if (has_p) ok = make_p(c + 1, j0, j0 + 16);
-                    ok = ok && wait_all(o2_done, c & 1);  // the last Q S has read its state
+                    ok = ok && wait_all(o_done, c & 1);  // the last Q S has read its state
                     if (!ok) break;
                     pa::tc::fence_after();
                     if (warp == LOAD_WARP && c + NST < nc) load(c + NST);
@@ -575,7 +573,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         const int64_t step = static_cast<int64_t>(a.p.H) * D;
         bool ok = true;
         auto put_o = [&](int c) {  // row = value dimension
-            if (!wait_all(o1_done, c & 1) || !wait_all(o2_done, c & 1)) return false;
+            if (!wait_all(o_done, c & 1)) return false;
             pa::tc::fence_after();
             // Lanes 2 x and 2 x + 1 trade: the even one writes both dimensions of token i,
             // the odd one of token i + 4, 16 lanes 64 bytes.

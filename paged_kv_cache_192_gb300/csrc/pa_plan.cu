@@ -75,7 +75,6 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanParams p)
     if (tid == 0) bad = 0;
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- the rows and their prefix sums ------------------------------------------
     const int first = p.state[0], count = p.state[1];
@@ -258,6 +257,8 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanParams p)
         if (tid == 0) p.query_start[p.R] = static_cast<int>(total.start);
     }
 
+    // (not earlier: CTAs of the next launch that wait beside these cost 1,024 rows a quarter)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // ---- the state advances once every CTA has read it -------------------------------
     __syncthreads();
     if (tid == 0) {
