@@ -8,8 +8,8 @@
 //
 // Bound: HBM (q, k, v and o: 8 D bytes per token and head) if the products, the
 // conversions between them and the copies overlap; a chunk of D = 128 costs 2,800
-// cycles of an SM's part of HBM, 1,800 of its tensor core and about as many
-// issue slots.  Hence one CTA per (request, head) with a warp group for each job:
+// cycles of an SM's part of HBM, 1,800 of its tensor core and 2,400 issue
+// slots of each scheduler.  Hence one CTA per (request, head) with a warp group for each job:
 //   warps 0-3, 4-7  the state, in registers in fp32 (thread = value dimension, half of
 //                   the key dimensions each): adds a chunk's K^T V' to it and gives
 //                   it to the next chunk's Q S as two bf16 terms in TMEM; in between
@@ -33,6 +33,13 @@
 // Few (request, head) pairs leave SMs idle: then a request's tokens are cut into
 // segments.  One launch sums each segment's own state (the kernel without its output
 // part), one chains them, and the segments then run like requests.
+//
+// Measured (32 heads, D 128): 8 requests of 65 to 2,048 tokens 78 us, 3.6 TB/s (0.53 of
+// HBM); a prompt of 16,384 tokens, 4 segments, 216 us (72 of them the segments' sums;
+// uncut 530 us); 100 tokens 9.2 us.  A chunk takes about 4,000 cycles: the sequence of
+// waits, issues and commits of warp 9 (each 150 to 400 cycles, with what 16 warps of five
+// roles lose to instruction fetches), beside 2,900 of V' and 2,700 of the state's warps;
+// the tensor core is busy for 38 % of the time, issue 55 %.
 #include <algorithm>
 #include <cmath>
 

