@@ -587,7 +587,8 @@ int pa_prefill_kernel_for(int R, int max_query_len, int Hq, int Hkv, int head_di
  *               its last -c (all of them if it has fewer), as rejected drafts or
  *               a finished request
  * Pages are taken from the ring's front row by row, pages that are no longer
- * needed go behind its end; sequences share no pages.  Out, all of it written:
+ * needed go behind its end; sequences share no pages.  Out, all of it written and none
+ * of it part of the state or the step's inputs:
  *   block_table   int32 [R][table_blocks]: the row's pages, 0 behind them
  *   context_lens  int32 [R]: the new lengths
  *   query_start   int32 [R + 1]: prefix sums of the added tokens
@@ -662,7 +663,10 @@ int pa_cross_attention(void *out, const void *q, const void *k_cache, const void
  *                 bytes, 16-byte aligned, scratch (may be NULL if that is 0);
  *                 calls that may overlap on the GPU need separate ones
  * A request whose numbers do not fit is left out (of a decode: zeros) and
- * PA_DEVERR_BAD_REQUEST recorded.  Sums and states are kept in fp32.
+ * PA_DEVERR_BAD_REQUEST recorded.  Sums and states are kept in fp32.  A NaN or
+ * infinity in v of a token may also reach earlier tokens of the same request and head
+ * within 64 tokens of it (their weight for it is 0, and 0 x NaN is NaN); one in q or k
+ * reaches no earlier token.  fp32 prompts run token by token on the decode's kernel.
  */
 int pa_linear_decode(void *out, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                      const void *v, int64_t v_stride, float *states, int num_states,

@@ -104,12 +104,15 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanParams p)
             if (s >= p.S) {
                 atomicOr(&bad, PA_DEVERR_BAD_REQUEST);
             } else if (s >= 0) {
-                if (L < 0 || blocks(L) > p.MB || atomicOr(&seen[s >> 5], 1u << (s & 31)) >> (s & 31) & 1) {
+                if (L < 0 || blocks(L) > p.MB) {
                     atomicOr(&bad, PA_DEVERR_BAD_REQUEST);
                 } else {
                     const int64_t n = max(static_cast<int64_t>(L) + c, int64_t(0));
                     row.seq = s;
                     row.old_len = row.new_len = L;
+                    // (which of two rows of a sequence comes second does not show: the step is
+                    // refused and both keep what there is)
+                    if (atomicOr(&seen[s >> 5], 1u << (s & 31)) >> (s & 31) & 1) atomicOr(&bad, PA_DEVERR_BAD_REQUEST);
                     if ((n + bs1) >> bs_log2 > cap) {
                         atomicOr(&bad, PA_DEVERR_NO_BLOCKS);
                     } else {

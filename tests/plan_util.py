@@ -55,7 +55,7 @@ class Model:
         given = []
         for r, (s, c) in enumerate(zip(ids, change)):
             c = 0 if why else c
-            if s < 0 or s >= self.S or (why == "request" and s in ids[:r]):
+            if s < 0 or s >= self.S:
                 lens.append(0)
                 start.append(start[-1])
                 continue

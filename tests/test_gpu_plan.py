@@ -91,6 +91,22 @@ def test_refused_steps_change_nothing(ids, change, max_tokens, W, bits):
     assert errors() == 0
 
 
+def test_two_rows_of_a_sequence_far_apart():
+    """Rows of different warps, and CTAs that see them in any order: refused, every row
+    shows what its sequence holds."""
+    m = Model(600, 8, 6000, 8)
+    m.step(list(range(600)), [1 + i % 60 for i in range(600)], 600 * 61)
+    state = m.state()
+    for _ in range(20):
+        ids = list(range(600)) + [5, 17, 599, 3]
+        plan = call(state, ids, [1] * 604, 8, 604)
+        want, why = m.step(ids, [1] * 604, 604)
+        assert why == "request"
+        same(plan, want)
+    m.check(state)
+    assert errors() == 4
+
+
 @pytest.mark.parametrize("word,value", [(0, -1), (0, 20), (1, -1), (1, 21)])
 def test_a_ring_that_cannot_be(word, value):
     m = Model(6, 8, 20, 16)

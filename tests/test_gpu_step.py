@@ -230,3 +230,112 @@ def test_linear_prompts_and_tokens_through_a_plan():
     plan = ops.plan_step(pages, y.ids_t, ints([1, 1]), BS, 2)
     y.check(ops.linear_decode(y.q, y.k, y.v, y.states, y.ids_t, plan.context_lens, y.decay_t))
     assert ops.device_error() == 0
+
+
+FIRST_CALLS = """
+import sys, torch
+sys.path.insert(0, {root!r})
+from paged_kv_cache_192_gb300 import layout, ops
+dev, bf16 = "cuda", torch.bfloat16
+g = torch.Generator().manual_seed(1)
+R = lambda *s: torch.randn(*s, generator=g).to(bf16).to(dev)
+ints = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+k, v = R(64, 2, 16, 128), R(64, 2, 16, 128)
+table = torch.arange(60, dtype=torch.int32, device=dev).view(2, 30)
+enc, one, many = ints([470, 33]), ints([0, 1, 3]), ints([0, 40, 140])
+q1, q2 = R(3, 8, 128), R(140, 8, 128)
+x1, x2 = R(2, 3, 2, 128), R(3000, 3, 2, 128)
+ids, lens1, start, lens2, decay = ints([1, 0]), ints([5, 1]), ints([0, 2500, 3000]), ints([2500, 600]), torch.tensor([-0.1, 0.0], device=dev)
+first = torch.randn(2, 2, 128, 128, generator=g).to(dev)
+seqs, grow, shrink = ints([2, -1, 0]), ints([20, 7, 3]), ints([-20, 0, -3])
+base = layout.page_state(3, 8, 30)
+def calls():
+    pages = ops.PageState(*(t.clone() for t in base))
+    state = [first.clone(), first.clone()]
+    p = ops.plan_step(pages, seqs, grow, 16, 25), ops.plan_step(pages, seqs, shrink, 16, 1)
+    c = ops.cross_attention(q1, k, v, table, one, enc, 2), ops.cross_attention(q2, k, v, table, many, enc, 100)
+    o = ops.linear_decode(*x1.unbind(1), state[0], ids, lens1, decay)
+    z = ops.linear_prefill(*x2.unbind(1), state[1], ids, start, lens2, 2500, decay)
+    return list(p[0]) + list(p[1]) + list(c) + [o, z] + state + list(pages)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(captured, calls()))
+assert ops.device_error() == 0
+# threads, a stream each
+import threading
+bad = []
+def work():
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.default_stream())
+    with torch.cuda.stream(s):
+        for _ in range(40):
+            got = calls()
+            s.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(captured, got)):
+                bad.append(1)
+threads = [threading.Thread(target=work) for _ in range(3)]
+for t in threads: t.start()
+for t in threads: t.join()
+assert not bad and ops.device_error() == 0
+print("ok")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """Nothing has to be called before a capture; and threads may call at once."""
+    import subprocess
+    import sys
+
+    from conftest import ROOT
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=ROOT)], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr
+
+
+def test_captured_branches_that_join():
+    """Two branches side by side, forked behind a plan and joined into a call: every node
+    has more than one neighbour."""
+    from paged_kv_cache_192_gb300 import layout, ops
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(40, 2, 16, 64, generator=g).to(bf16).cuda() for _ in range(2))
+    q, qs = torch.randn(140, 8, 64, generator=g).to(bf16).cuda(), torch.randn(2, 8, 64, generator=g).to(bf16).cuda()
+    x = torch.randn(1602, 3, 2, 64, generator=g).to(bf16).cuda()
+    enc, ids, decay = ints([300, 77]), ints([1, 0]), torch.tensor([-0.2, -0.001], device="cuda")
+    first = torch.randn(2, 2, 64, 64, generator=g).cuda()
+    pages, states = layout.page_state(2, 120, 240), first.clone()
+
+    def branches(side):
+        main = torch.cuda.current_stream()
+        a = ops.plan_step(pages, ids, ints_grow, 16, 1602)
+        side.wait_stream(main)
+        b = ops.linear_prefill(*x.unbind(1), states, ids, a.query_start, a.context_lens, 1500, decay)
+        with torch.cuda.stream(side):
+            c = ops.cross_attention(q, k, v, tables, starts, enc, 100)
+            d = ops.cross_attention(qs, k, v, tables, ones, enc, 1)
+        main.wait_stream(side)
+        e = ops.plan_step(pages, ids, ints_drop, 16, 1)
+        f = ops.linear_decode(*x[:2].unbind(1), states, ids, e.context_lens, decay)
+        return list(a) + [b, c, d] + list(e) + [f]
+
+    ints_grow, ints_drop = ints([1500, 102]), ints([-1500, -100])
+    tables, starts, ones = torch.arange(40, dtype=torch.int32, device="cuda").view(2, 20), ints([0, 100, 140]), ints([0, 1, 2])
+    keep = [t.clone() for t in pages]
+    side = torch.cuda.Stream()
+    eager, after = branches(side), states.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = branches(side)
+    for _ in range(3):
+        for t, old in zip(pages, keep):
+            t.copy_(old)
+        states.copy_(first)
+        for o in captured:
+            o.fill_(9)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, eager)) and torch.equal(states, after)
+    assert ops.device_error() == 0
