@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanParams p)
     // ---- the rows and their prefix sums ------------------------------------------
     const int first = p.state[0], count = p.state[1];
     Sums total{0, 0, 0};
-    constexpr int PER = kMaxRows / kThreads;  // rows of a thread, their loads in two rounds
+    constexpr int PER = kMaxRows / kThreads;  // rows of a thread: two latencies for all of them
     int id[PER], change[PER], len[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
