@@ -76,9 +76,14 @@ struct SLayout {
     static constexpr int OFF_K = QT_BYTES;
     static constexpr int OFF_V = OFF_K + NST * T_BYTES;
     static constexpr int OFF_BAR = OFF_V + NST * T_BYTES;
-    // k_full, k_empty, v_full, v_empty [NST]; s_full, s_free, p_full, o_done [2];
+    // A group waits only for its own tiles, every other one.  Tile i's barrier is number
+    // i % NF, an even number, so that the tiles of a barrier are all one group's: a wait
+    // tells two phases apart, and a group that leaves phases out could take the other's
+    // late tile for its own (copies do not land in the order of their issue).
+    static constexpr int NF = 2 * NST;
+    // k_full, v_full [NF]; k_empty, v_empty [NST]; s_full, s_free, p_full, o_done [2];
     // q_full, drain
-    static constexpr int N_BAR = 4 * NST + 8 + 2;
+    static constexpr int N_BAR = 2 * NF + 2 * NST + 8 + 2;
     static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;
     static constexpr int OFF_REQ = OFF_MISC + 16;
     static constexpr int SMEM = OFF_REQ + int(sizeof(ReqTables)) + 1024;
@@ -111,7 +116,7 @@ __device__ __forceinline__ int read_requests(const WinParams &p, ReqTables &t, i
     for (int r0 = 0; r0 < p.R; r0 += 12 * 32) {
         const int r = r0 + tid;
         int np = 0, from = r;
-        if constexpr (CROSS) {  // (kMaxR requests: one round)
+        if constexpr (CROSS) {  // (at most kMaxR requests: this loop runs once)
             if (r < p.R) t.L[r] = p.context_lens[r];
             __syncthreads();
             int rank = 0;
@@ -671,14 +676,14 @@ __global__ void __launch_bounds__(SLayout<D>::THREADS, 1)
                                 const __grid_constant__ CUtensorMap vmap,
                                 const __grid_constant__ CUtensorMap qmap) {
     using Lay = SLayout<D>;
-    constexpr int NST = Lay::NST;
+    constexpr int NST = Lay::NST, NF = Lay::NF;
     constexpr int QTOK = 128 / GQ;  // query tokens per item
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sq = pa::smem_u32(smem), sk = sq + Lay::OFF_K, sv = sq + Lay::OFF_V;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::OFF_BAR);
-    uint64_t *k_full = bars, *k_empty = k_full + NST, *v_full = k_empty + NST, *v_empty = v_full + NST;
+    uint64_t *k_full = bars, *v_full = k_full + NF, *k_empty = v_full + NF, *v_empty = k_empty + NST;
     uint64_t *s_full = v_empty + NST, *s_free = s_full + 2;  // [group]
     uint64_t *p_full = s_free + 2, *o_done = p_full + 2, *q_full = o_done + 2, *drain = q_full + 1;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + Lay::OFF_MISC);
@@ -693,10 +698,12 @@ __global__ void __launch_bounds__(SLayout<D>::THREADS, 1)
     if (tid == 0) {
         for (const CUtensorMap *map : {&kmap, &vmap, &qmap})
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-        for (int i = 0; i < NST; ++i) {
+        for (int i = 0; i < NF; ++i) {
             pa::mbar_init(&k_full[i], 1);
-            pa::mbar_init(&k_empty[i], 1);
             pa::mbar_init(&v_full[i], 1);
+        }
+        for (int i = 0; i < NST; ++i) {
+            pa::mbar_init(&k_empty[i], 1);
             pa::mbar_init(&v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -759,7 +766,7 @@ __global__ void __launch_bounds__(SLayout<D>::THREADS, 1)
                 break;
             }
             if (lane == 0) {
-                pa::mbar_arrive_expect_tx(&full[st], Lay::T_BYTES);
+                pa::mbar_arrive_expect_tx(&full[i % NF], Lay::T_BYTES);
                 ++loads_issued;
             }
             __syncwarp();
@@ -768,7 +775,7 @@ __global__ void __launch_bounds__(SLayout<D>::THREADS, 1)
 #pragma unroll
                 for (int h = 0; h < D / 64; ++h)
                     tma_load_2d(ring + st * Lay::T_BYTES + h * kT2KT * 128 + b, map, h * 64, rf.row,
-                                &full[st]);
+                                &full[i % NF]);
             }
             __syncwarp();
         }
@@ -783,7 +790,7 @@ __global__ void __launch_bounds__(SLayout<D>::THREADS, 1)
         constexpr uint32_t kStage = Lay::T_BYTES >> 4;
         // S of tile i, the group's l-th; its K is then free
         auto start = [&](int i, int l) {
-            if (!wait_all(&k_full[i % NST], (i / NST) & 1)) return false;
+            if (!wait_all(&k_full[i % NF], (i / NF) & 1)) return false;
             if (l > 0 && !wait_all(&s_free[g], (l - 1) & 1)) return false;
             pa::tc::fence_after();
             if (pa::tc::elect_one()) {
@@ -797,7 +804,7 @@ __global__ void __launch_bounds__(SLayout<D>::THREADS, 1)
         bool ok = g < nt ? wait_all(q_full, 0) && start(g, 0) : true;
         for (int i = g, l = 0; i < nt && ok; i += 2, ++l) {
             if (i + 2 < nt) ok = start(i + 2, l + 1);
-            if (ok) ok = wait_all(&v_full[i % NST], (i / NST) & 1) && wait_all(&p_full[g], l & 1);
+            if (ok) ok = wait_all(&v_full[i % NF], (i / NF) & 1) && wait_all(&p_full[g], l & 1);
             if (!ok) break;
             pa::tc::fence_after();
             if (pa::tc::elect_one()) {
@@ -832,7 +839,7 @@ __global__ void __launch_bounds__(SLayout<D>::THREADS, 1)
                 rescale_o<D>(lane_base + o_col, alpha);
             }
             if (has_hidden_rows(I, p.sinks, j0)) {
-                ok = wait_all(&v_full[i % NST], (i / NST) & 1);  // V has landed
+                ok = wait_all(&v_full[i % NF], (i / NF) & 1);  // V has landed
                 if (!ok) break;
                 zero_hidden_rows<D>(I, p.sinks, j0, sv + (i % NST) * Lay::T_BYTES, row);
             }
@@ -984,10 +991,8 @@ __global__ void __launch_bounds__(SLayout<D>::THREADS, 1)
         }
         if ((warp == Lay::K_WARP || warp == Lay::V_WARP) && lane == 0) {
             uint64_t *full = warp == Lay::V_WARP ? v_full : k_full;
-            for (int st = 0; st < NST && st < loads_issued; ++st) {
-                const int last = st + NST * ((loads_issued - 1 - st) / NST);
-                (void)pa::mbar_wait(&full[st], (last / NST) & 1);
-            }
+            for (int b = 0; b < NF && b < loads_issued; ++b)
+                (void)pa::mbar_wait(&full[b], ((loads_issued - 1 - b) / NF) & 1);
         }
         __syncthreads();
     }
