@@ -1069,18 +1069,30 @@ int launch(const WinParams &p, const void *q, const void *k_cache, const void *v
     if (sms <= 0) return pa::cuda_fail(cudaGetLastError(), "prefill_window: SM count");
     int64_t singles = 0;
     bool split = runs_split(p.R, p.T, max_query_len, GQ, p.Hkv, sms, &singles);
+    int waves_of = 0;  // CROSS, more query tiles than SMs: CTAs per tile in several waves
     if constexpr (CROSS) {
-        // More query tiles than SMs: the split kernel, one CTA per tile, where its waves
-        // take less.  A 64-state tile takes it half as long as the kernel below, which
-        // has two query tiles of its own for it; a CTA costs it about 10 such halves.
-        // 8 requests of 20 to 100 tokens (groups of 4) over 1,000 to 4,100 states: 46 us
-        // against 70; 4 of 2,048 tokens over 2,000 to 8,192: 667 below.
-        const int64_t tiles = (int64_t(p.MB) << p.bs_log2) / kT2KT + 1;
-        auto waves = [&](int64_t ctas) { return (ctas + sms - 1) / sms; };
-        // (half of the partly filled tiles, of which there may be one per request)
-        const int64_t partly = std::max<int64_t>(1, (int64_t(p.T) / (128 / GQ) + (p.R + 1) / 2) * p.Hkv);
-        split = split || (p.R <= kMaxR && waves(partly) * (tiles + 10) <
-                                              waves(query_tiles(p.R, p.T, max_query_len, 256 / GQ) * p.Hkv) * 2 * tiles);
+        if (!split && p.R <= kMaxR) {
+            // In halves of what a 64-state tile takes the kernel below (two query tiles at
+            // once), with a CTA's start as START of them: the longest item, or the SMs'
+            // average, of items whose states fill 0.6 of the table; half of the partly
+            // filled query tiles are there.  8 requests of 20 to 100 tokens (groups of 4)
+            // over 1,000 to 4,100 states: 42 us with two CTAs per tile, 47 with one, 70
+            // below; 16 of 33 to 100 (groups of 1) over 500 to 1,500: 27 with one, 46 with
+            // two, 42 below; 4 of 2,048 over 2,000 to 8,192: 657 with one, 627 below.
+            constexpr double START = 10, FILL = 0.6;
+            const double tiles = double((int64_t(p.MB) << p.bs_log2) / kT2KT + 1);
+            const double singles_there = (double(p.T) / (128 / GQ) + 0.5 * p.R) * p.Hkv;
+            double best = std::max(2 * tiles, double(query_tiles(p.R, p.T, max_query_len, 256 / GQ) * p.Hkv) * FILL * 2 *
+                                                  tiles / sms);
+            for (int c = 1; c <= SLayout<D>::MAX_C && (c == 1 || tiles >= 4 * c); c *= 2) {
+                const double cost = std::max(tiles / c + START, singles_there * (FILL * tiles + START * c) / sms);
+                if (cost < best) {
+                    best = cost;
+                    waves_of = c;
+                }
+            }
+            split = waves_of > 0;
+        }
     }
     if (split) {
         auto kern = prefill_window_split_kernel<D, GQ, CROSS>;
@@ -1094,8 +1106,8 @@ int launch(const WinParams &p, const void *q, const void *k_cache, const void *v
         static std::atomic<int> cache[64][5];
         const int64_t keys = std::min<int64_t>(int64_t(p.MB) << p.bs_log2,
                                                int64_t(p.window) + p.sinks + 128 / GQ);
-        int c = 1;
-        while (2 * c <= SLayout<D>::MAX_C && keys >= 4 * c * kT2KT) {
+        int c = std::max(1, waves_of);
+        while (waves_of == 0 && 2 * c <= SLayout<D>::MAX_C && keys >= 4 * c * kT2KT) {
             const int n = clusters_at_once(kern, SLayout<D>::THREADS, SLayout<D>::SMEM, 2 * c, cache);
             if (n < 0) return pa::cuda_fail(cudaGetLastError(), "prefill_window: occupancy");
             if (singles > n) break;

@@ -121,6 +121,16 @@ def test_clusters_and_waves(R, n, e, gq):
     x.check(x.run())
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,e,gq,Hkv", [
+    ([650, 641], [8000, 1], 8, 2),                    # long states: two CTAs per query tile
+    ([40] + [1] * 39, [6400, 0, 1, 63] * 10, 1, 4),   # most query tiles partly filled: four
+    ([100, 33, 64] * 5, [500, 40, 0] * 5, 1, 16)])    # short states: one
+def test_query_tiles_in_several_waves(n, e, gq, Hkv, d):
+    x = Cross(n, e, Hq=gq * Hkv, Hkv=Hkv, d=d, seed=len(n))
+    x.check(x.run())
+
+
 @pytest.mark.parametrize("most", [1, 30, 100])
 def test_no_states_at_all(most):
     x = Cross([most, 1, 0], [0, 0, 0])
