@@ -86,7 +86,10 @@ struct SLayout {
     static constexpr int N_BAR = 2 * NF + 2 * NST + 8 + 2;
     static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;
     static constexpr int OFF_REQ = OFF_MISC + 16;
-    static constexpr int SMEM = OFF_REQ + int(sizeof(ReqTables)) + 1024;
+    // more than half an SM's: a second CTA there would wait for the first one's TMEM, which
+    // clusters that wait for each other's CTAs in two places must not
+    static constexpr int USED = OFF_REQ + int(sizeof(ReqTables)) + 1024;
+    static constexpr int SMEM = USED > 116 * 1024 ? USED : 116 * 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static constexpr int X_BYTES = 128 * D * 4;  // received, and as much exchanged
     static_assert(2 * X_BYTES <= OFF_BAR - OFF_K, "the partial O must fit the rings");
