@@ -289,7 +289,7 @@ extern "C" int pa_linear_prefill(void *out, const void *q, int64_t q_stride, con
     p.err = pa::device_error_word();
     if (!uses_chunks(R, max_query_len, H, head_dim, dtype))
         return pa::lin::launch_recurrent(p, head_dim, dtype, stream);
-    return pa::lin::launch_chunks(p, head_dim, static_cast<float *>(workspace), seg, stream);
+    return pa::lin::launch_chunks(p, head_dim, max_query_len, static_cast<float *>(workspace), seg, stream);
 }
 
 extern "C" int pa_linear_prefill_workspace_size(int R, int total_tokens, int max_query_len, int H, int head_dim,

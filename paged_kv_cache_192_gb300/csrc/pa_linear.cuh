@@ -54,7 +54,7 @@ struct Segments {
     int tokens, slots;
 };
 Segments segments_for(int R, int T, int max_query_len, int H);
-int launch_chunks(const LinParams &p, int D, float *ws, const Segments &s, cudaStream_t stream);
+int launch_chunks(const LinParams &p, int D, int max_query_len, float *ws, const Segments &s, cudaStream_t stream);
 
 }  // namespace lin
 }  // namespace pa

@@ -189,6 +189,24 @@ def test_prefill_extreme_decays(log_decay, n):
     x.check(prefill(x), terms=TERMS)
 
 
+@pytest.mark.parametrize("R,H", [(2, 100), (33, 8), (63, 3), (64, 4), (65, 4)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_requests_of_all_lengths(R, H, d):
+    """More (request, head) pairs than SMs, in any order of lengths, equal ones too; some
+    requests without new tokens or without a state."""
+    n = [i * 37 % 131 if i % 5 else 70 for i in range(R)]
+    n[R // 2] = 200
+    ids = [-1 if i % 9 == 4 else R - i for i in range(R)]
+    x = Linear(n, [i % 3 for i in range(R)], H=H, d=d, seed=R, ids=ids)
+    got = prefill(x)
+    start = x.start.tolist()
+    for i, s in enumerate(ids):  # the rows of requests that were left out hold anything
+        if s < 0:
+            got[start[i]:start[i + 1]] = 0
+    x.check(got, terms=TERMS)
+    assert errors() == 0
+
+
 @pytest.mark.parametrize("n", [100, 2500])
 def test_prefill_many_requests_and_heads(n):
     x = Linear([n] + [10 + 7 * i for i in range(12)], [0, 3] * 6 + [1], H=16, d=64 if n == 100 else 128)
