@@ -34,7 +34,7 @@
 // segments.  One launch sums each segment's own state (the kernel without its output
 // part), one chains them, and the segments then run like requests.
 //
-// Measured (32 heads, D 128): 8 requests of 65 to 2,048 tokens 78 us, 3.6 TB/s (0.53 of
+// Measured (32 heads, D 128): 8 requests of 65 to 2,048 tokens 73 us, 3.9 TB/s (0.57 of
 // HBM); a prompt of 16,384 tokens, 4 segments, 216 us (72 of them the segments' sums;
 // uncut 530 us); 100 tokens 9.2 us.  A chunk takes about 4,000 cycles: the sequence of
 // waits, issues and commits of warp 9 (each 150 to 400 cycles, with what 16 warps of five
