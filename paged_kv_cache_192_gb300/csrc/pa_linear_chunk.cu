@@ -211,6 +211,10 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
              *drain = o_free + 1;
     float *fdec = reinterpret_cast<float *>(smem + L::OFF_F), *wdec = reinterpret_cast<float *>(smem + L::OFF_W),
           *pdec = reinterpret_cast<float *>(smem + L::OFF_D) + C;
+    // Without outputs K^T V' has two places, so that the tensor core goes on while the state
+    // takes one: the scores' barriers, which are free then, say full and taken.
+    uint64_t *sum_full = s1_full, *sum_free = p_full;
+    auto u_col = [](int c) { return L::U + (SUM ? (c & 1) * D : 0); };
     uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *fail = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             pa::mbar_init(&s1_full[i], 1);
-            pa::mbar_init(&p_full[i], 5);
+            pa::mbar_init(&p_full[i], SUM ? 2 * L::LANE_WARPS : 5);
             pa::mbar_init(&vp_full[i], SUM ? 4 : 3);
         }
         pa::mbar_init(u_half, 1);
@@ -373,7 +377,8 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         for (int c = 0; c < nc && ok; ++c) {
             const uint32_t stage = static_cast<uint32_t>((c % NST) * kStage);
             if (SUM) ok = wait_all(&full[c % NST], (c / NST) & 1);
-            if (c > 0) ok = ok && wait_all(u_free, (c - 1) & 1);
+            // the state has what lies in the place of this K^T V'
+            if (SUM ? c > 1 : c > 0) ok = ok && (SUM ? wait_all(&sum_free[c & 1], ((c >> 1) - 1) & 1) : wait_all(u_free, (c - 1) & 1));
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 ok = ok && wait_all(&vp_full[half], c & 1);
@@ -385,10 +390,13 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                     for (int ks = half * C / 32; ks < (half + 1) * C / 32; ++ks)
 #pragma unroll
                         for (int term = 0; term < 3; ++term)
-                            pa::tc::mma_ss(tmem + L::U, vp + term * kTile + ((ks * 16 * 128) >> 4),
+                            pa::tc::mma_ss(tmem + u_col(c), vp + term * kTile + ((ks * 16 * 128) >> 4),
                                            k + ((ks * 16 * 128) >> 4), kIdU, ks + term > 0);
                     pa::tc::commit(half ? u_full : u_half);
-                    if (SUM && half) pa::tc::commit(&empty[c % NST]);
+                    if (SUM && half) {
+                        pa::tc::commit(&sum_full[c & 1]);
+                        pa::tc::commit(&empty[c % NST]);
+                    }
                 }
                 __syncwarp();
             }
@@ -469,7 +477,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
             }
             const float em_full = expm1f(g * C), em_rest = expm1f(g * rest);
             for (int c = 0; c < nc && ok; ++c) {
-                ok = wait_all(u_full, c & 1);
+                ok = SUM ? wait_all(&sum_full[c & 1], (c >> 1) & 1) : wait_all(u_full, c & 1);
                 if (!ok) break;
                 pa::tc::fence_after();
                 // l^m S = S + (l^m - 1) S: as exact as its rounding where l is close to 1, and
@@ -479,7 +487,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
 #pragma unroll
                 for (int k = 0; k < HALF / 2; k += 8) {
                     uint32_t u[16];
-                    pa::tc::ld16(base + L::U + k0 + 2 * k, u);
+                    pa::tc::ld16(base + u_col(c) + k0 + 2 * k, u);
                     pa::tc::wait_ld();
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -487,7 +495,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                                               make_float2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1])));
                 }
                 pa::tc::fence_before();
-                signal(u_free);
+                signal(SUM ? &sum_free[c & 1] : u_free);
                 if (!SUM && c + 1 < nc) {
                     // (the place of this P was read before the last Q S)
                     if (has_p) ok = make_p(c + 1, j0, j0 + 16);
