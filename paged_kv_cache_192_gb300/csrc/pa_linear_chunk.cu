@@ -35,11 +35,14 @@
 // part), one chains them, and the segments then run like requests.
 //
 // Measured (32 heads, D 128): 8 requests of 65 to 2,048 tokens 73 us, 3.9 TB/s (0.57 of
-// HBM); a prompt of 16,384 tokens, 4 segments, 216 us (72 of them the segments' sums;
+// HBM); a prompt of 16,384 tokens, 4 segments, 214 us (70 of them the segments' sums;
 // uncut 530 us); 100 tokens 9.2 us.  A chunk takes about 4,000 cycles: the sequence of
 // waits, issues and commits of warp 9 (each 150 to 400 cycles, with what 16 warps of five
 // roles lose to instruction fetches), beside 2,900 of V' and 2,700 of the state's warps;
-// the tensor core is busy for 38 % of the time, issue 55 %.
+// the tensor core is busy for 38 % of the time, issue 55 %.  Shared memory has 2,800 cycles
+// of it to move, at 128 bytes each: 48 KB copied in, 224 KB of operands (96 of K^T V', whose
+// three terms read K three times), 64 KB for V', 16 for P; without outputs 1,500 of 2,100,
+// and more warps for V' gain nothing there (220 us for the prompt with six).
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -378,7 +381,8 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
             const uint32_t stage = static_cast<uint32_t>((c % NST) * kStage);
             if (SUM) ok = wait_all(&full[c % NST], (c / NST) & 1);
             // the state has what lies in the place of this K^T V'
-            if (SUM ? c > 1 : c > 0) ok = ok && (SUM ? wait_all(&sum_free[c & 1], ((c >> 1) - 1) & 1) : wait_all(u_free, (c - 1) & 1));
+            if (SUM && c > 1) ok = ok && wait_all(&sum_free[c & 1], ((c >> 1) - 1) & 1);
+            if (!SUM && c > 0) ok = ok && wait_all(u_free, (c - 1) & 1);
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 ok = ok && wait_all(&vp_full[half], c & 1);
