@@ -15,9 +15,9 @@
 // Measured: 64 requests of 1 to 5 rows over 400 to 1,500 states (16 KV heads, d 64)
 // 41.3 us, 6.1 TB/s (0.89 of HBM; 46.9 in the requests' own order); one row over 1,500
 // states 5.1 us on the GPU.  8 requests of 20 to 100 rows over 1,000 to 4,100 states (32/8
-// heads, d 128) 46 us: 120 items of up to 65 tiles, one CTA each, of which the longest
-// takes it all.  4 of 2,048 rows over 2,000 to 8,192 states 631 to 665 us, 1,060 to 1,110
-// TFLOP/s (0.61 to 0.64 of sustained bf16; tensor pipe 73 % of active cycles).
+// heads, d 128) 41 us: 120 items of up to 65 tiles, two CTAs each (47 with one, of which
+// the longest takes it all).  4 of 2,048 rows over 2,000 to 8,192 states 627 to 671 us,
+// 1,050 to 1,120 TFLOP/s (0.60 to 0.65 of sustained bf16; tensor pipe 73 % of active cycles).
 #include <algorithm>
 #include <atomic>
 #include <cmath>

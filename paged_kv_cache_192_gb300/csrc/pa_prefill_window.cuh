@@ -118,26 +118,34 @@ __device__ __forceinline__ int read_requests(const WinParams &p, ReqTables &t, i
     int carry = 0;
     for (int r0 = 0; r0 < p.R; r0 += 12 * 32) {
         const int r = r0 + tid;
-        int np = 0, from = r;
-        if constexpr (CROSS) {  // (at most kMaxR requests: this loop runs once)
-            if (r < p.R) t.L[r] = p.context_lens[r];
-            __syncthreads();
-            int rank = 0;
-            if (r < p.R)
-                for (int x = 0; x < p.R; ++x) rank += t.L[x] > t.L[r] || (t.L[x] == t.L[r] && x < r);
-            if (r < p.R) t.row[rank] = r;
-            __syncthreads();
-            if (r < p.R) from = t.row[r];
-        }
+        int np = 0, qs = 0, n = 0, L = 0;
         if (r < p.R) {
-            const int qs = p.query_start[from], n = p.query_start[from + 1] - qs, L = p.context_lens[from];
+            qs = p.query_start[r], n = p.query_start[r + 1] - qs, L = p.context_lens[r];
             if (n > 0 && qs >= 0 && n <= p.T - qs && L >= (CROSS ? 1 : n) && L <= p.MB << p.bs_log2)
                 np = (n + qtok - 1) / qtok;
             else if ((CROSS ? n < 0 || (n > 0 && (qs < 0 || n > p.T - qs)) : n != 0) || L < 0 || L > p.MB << p.bs_log2)
                 pa::record_error(p.err, CROSS ? PA_DEVERR_BAD_REQUEST : PA_DEVERR_BAD_BLOCK);
-            t.qs[r] = qs;
-            t.n[r] = n;
             t.L[r] = L;
+            if constexpr (!CROSS) {
+                t.qs[r] = qs;
+                t.n[r] = n;
+            }
+        }
+        if constexpr (CROSS) {  // (at most kMaxR requests: this loop runs once)
+            __syncthreads();
+            int rank = 0;
+            if (r < p.R) {
+                for (int x = 0; x < p.R; ++x) rank += t.L[x] > L || (t.L[x] == L && x < r);
+                t.row[rank] = r;
+                t.qs[rank] = qs;
+                t.n[rank] = n;
+                t.pre[rank + 1] = np;
+            }
+            __syncthreads();
+            if (r < p.R) {
+                t.L[rank] = L;
+                np = t.pre[r + 1];  // (of the request in this place; its sum goes there below)
+            }
         }
         int x = np;
 #pragma unroll
