@@ -34,7 +34,7 @@ template <>
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 template <typename T, int D, int CW>
-__global__ void __launch_bounds__(256) recurrent_kernel(const LinParams p) {
+__global__ void __launch_bounds__(256, D == 64 ? 5 : 4) recurrent_kernel(const LinParams p) {
     constexpr int NT = 256, LPR = CW / 4;   // lanes per row of the slice
     constexpr int RG = NT / LPR;            // rows at a time
     constexpr int NR = D / RG;              // rows per thread
@@ -59,13 +59,14 @@ __global__ void __launch_bounds__(256) recurrent_kernel(const LinParams p) {
         return;
     }
     float *S = p.states + (static_cast<int64_t>(x.state) * p.H + h) * (D * D) + c0 + c;
-    float4 s[NR];
+    float2 s[NR][2];
 #pragma unroll
-    for (int i = 0; i < NR; ++i)
-        s[i] = x.held ? *reinterpret_cast<const float4 *>(S + (row0 + i * RG) * D) : make_float4(0.f, 0.f, 0.f, 0.f);
-    // l S = S + (l - 1) S: as exact as its rounding where l is close to 1 and a state
-    // lives long (and before k v is added, of which S may be many times larger)
-    const float lm1 = expm1f(pa::lin::log_decay(p, h));
+    for (int i = 0; i < NR; ++i) {
+        const float4 x4 = x.held ? *reinterpret_cast<const float4 *>(S + (row0 + i * RG) * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+        s[i][0] = make_float2(x4.x, x4.y), s[i][1] = make_float2(x4.z, x4.w);
+    }
+    const pa::lin::Decay l = pa::lin::decay_factor(pa::lin::log_decay(p, h), 1);
+    const float2 hi = make_float2(l.hi, l.hi), lo = make_float2(l.lo, l.lo);
     auto stage = [&](int t) {
         const int64_t tok = x.t0 + t;
         for (int i = tid; i < 2 * D + CW; i += NT) {
@@ -80,19 +81,18 @@ __global__ void __launch_bounds__(256) recurrent_kernel(const LinParams p) {
         const int b = t & 1;
         if (t + 1 < x.n) stage(t + 1);
         const float4 vv = *reinterpret_cast<const float4 *>(&sv[b][c]);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float2 v01 = make_float2(vv.x, vv.y), v23 = make_float2(vv.z, vv.w);
+        float2 o01 = make_float2(0.f, 0.f), o23 = o01;
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             const float ki = sk[b][row0 + i * RG], qi = sq[b][row0 + i * RG];
-            s[i].x = fmaf(ki, vv.x, fmaf(lm1, s[i].x, s[i].x));
-            s[i].y = fmaf(ki, vv.y, fmaf(lm1, s[i].y, s[i].y));
-            s[i].z = fmaf(ki, vv.z, fmaf(lm1, s[i].z, s[i].z));
-            s[i].w = fmaf(ki, vv.w, fmaf(lm1, s[i].w, s[i].w));
-            o.x = fmaf(qi, s[i].x, o.x);
-            o.y = fmaf(qi, s[i].y, o.y);
-            o.z = fmaf(qi, s[i].z, o.z);
-            o.w = fmaf(qi, s[i].w, o.w);
+            const float2 kk = make_float2(ki, ki), qq = make_float2(qi, qi);
+            s[i][0] = pa::ffma2(hi, s[i][0], pa::ffma2(lo, s[i][0], __fmul2_rn(kk, v01)));
+            s[i][1] = pa::ffma2(hi, s[i][1], pa::ffma2(lo, s[i][1], __fmul2_rn(kk, v23)));
+            o01 = pa::ffma2(qq, s[i][0], o01);
+            o23 = pa::ffma2(qq, s[i][1], o23);
         }
+        float4 o = make_float4(o01.x, o01.y, o23.x, o23.y);
 #pragma unroll
         for (int off = LPR; off < 32; off <<= 1) {
             o.x += __shfl_xor_sync(pa::kFull, o.x, off);
@@ -111,7 +111,8 @@ __global__ void __launch_bounds__(256) recurrent_kernel(const LinParams p) {
         // (part[b] and the vectors [b] are written again after the next barrier)
     }
 #pragma unroll
-    for (int i = 0; i < NR; ++i) *reinterpret_cast<float4 *>(S + (row0 + i * RG) * D) = s[i];
+    for (int i = 0; i < NR; ++i)
+        *reinterpret_cast<float4 *>(S + (row0 + i * RG) * D) = make_float4(s[i][0].x, s[i][0].y, s[i][1].x, s[i][1].y);
 }
 
 template <typename T, int D, int CW>

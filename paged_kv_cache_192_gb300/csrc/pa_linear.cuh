@@ -44,6 +44,39 @@ __device__ __forceinline__ Request request(const LinParams &p, int r) {
 // stays finite, so that l^0 is 1.
 __device__ __forceinline__ float log_decay(const LinParams &p, int h) { return fmaxf(p.log_decay[h], -1e4f); }
 
+// x^n = e^(g n) to within 2 ulp: g n is exact as y + rest, e^rest = 1 + rest (rest is
+// below 2^-24 |y|).
+__device__ __forceinline__ float decay_power(float g, int n) {
+    const float y = g * n, rest = fmaf(g, static_cast<float>(n), -y), x = expf(y);
+    return fmaf(x, rest, x);
+}
+
+// l^n as a sum of two numbers, so that l^n S + x is decayed(l^n, S, x): one rounding of
+// the sum and one of a part that is 2^-24 of it, whatever l^n is.
+//   l^n >= 1/2: hi = 1 + (l^n - 1) cut to 24 bits and what that leaves, exact: a state
+//     that lives long collects no error of the factor;
+//   below: hi alone (lo would add nothing to the 2 ulp of e^y; as 1 + (l^n - 1) it would
+//     have an absolute error of 2^-25, all of it where l^n is small).
+// lo is never 0 beside a hi that is not, so that an infinite S stays infinite.
+struct Decay {
+    float hi, lo;
+};
+__device__ __forceinline__ Decay decay_factor(float g, int n) {
+    const float y = g * n;
+    Decay f;
+    if (y > -0.69f) {
+        const float rest = fmaf(g, static_cast<float>(n), -y), e = expm1f(y), em = fmaf(rest, 1.f + e, e);
+        f.hi = __fadd_rz(1.f, em);
+        f.lo = em - (f.hi - 1.f);
+    } else {
+        f.hi = decay_power(g, n);
+        f.lo = 0.f;
+    }
+    if (f.hi > 0.f) f.lo = fmaxf(f.lo, fmaxf(f.hi * 0x1p-60f, 0x1p-149f));
+    return f;
+}
+__device__ __forceinline__ float decayed(const Decay &f, float s, float x) { return fmaf(f.hi, s, fmaf(f.lo, s, x)); }
+
 // The recurrent kernel (pa_linear.cu), any number of tokens and both types.
 int launch_recurrent(const LinParams &p, int D, int dtype, cudaStream_t stream);
 

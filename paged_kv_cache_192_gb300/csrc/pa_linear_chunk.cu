@@ -84,7 +84,8 @@ struct Lay {
     static constexpr int OFF_W = OFF_F + C * 4;        // l^(C-1-j), and of the last chunk
     static constexpr int OFF_D = OFF_W + 2 * C * 4;    // l^x, x = 1 - C .. C - 1 (1 below 0)
     static constexpr int OFF_MISC = OFF_D + 2 * C * 4; // TMEM slot, fail flag
-    static constexpr int SMEM = OFF_MISC + 16 + 1024;
+    static constexpr int OFF_L = OFF_MISC + 16;        // l^C, l^(tokens of the last chunk)
+    static constexpr int SMEM = OFF_L + 16 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(OFF_VP % 1024 == 0 && OFF_P % 1024 == 0 && OFF_BAR % 8 == 0 && OFF_F % 16 == 0 && OFF_MISC % 8 == 0,
                   "alignment");
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
              *drain = o_free + 1;
     float *fdec = reinterpret_cast<float *>(smem + L::OFF_F), *wdec = reinterpret_cast<float *>(smem + L::OFF_W),
           *pdec = reinterpret_cast<float *>(smem + L::OFF_D) + C;
+    pa::lin::Decay *chunk_decay = reinterpret_cast<pa::lin::Decay *>(smem + L::OFF_L);
     // Without outputs K^T V' has two places, so that the tensor core goes on while the state
     // takes one: the scores' barriers, which are free then, say full and taken.
     uint64_t *sum_full = s1_full, *sum_free = p_full;
@@ -257,14 +259,22 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Work w = find_work<D, SUM>(a, reinterpret_cast<int *>(smem + L::OFF_VP));
-    const float g = pa::lin::log_decay(a.p, w.h), g2 = g * kLog2e;
+    const float g = pa::lin::log_decay(a.p, w.h);
     const int nc = (w.n + C - 1) / C, rest = w.n - (nc - 1) * C;  // chunks, tokens of the last
-    if (tid < C) {
-        fdec[tid] = a.p.scale * exp2f(g2 * (tid + 1));
-        wdec[tid] = exp2f(g2 * (C - 1 - tid));
-        pdec[tid] = exp2f(g2 * tid);
-        pdec[tid - C] = 1.f;
-        wdec[C + tid] = tid < rest ? exp2f(g2 * (rest - 1 - tid)) : 0.f;
+    {  // a power for each of 4 C threads
+        const int i = tid % C, what = tid / C;
+        if (what < 4) {
+            const int n = what == 0 ? i + 1 : what == 1 ? C - 1 - i : what == 2 ? i : max(rest - 1 - i, 0);
+            const float x = pa::lin::decay_power(g, n);
+            if (what == 0) fdec[i] = a.p.scale * x;
+            else if (what == 1) wdec[i] = x;
+            else if (what == 2) pdec[i] = x;
+            else wdec[C + i] = i < rest ? x : 0.f;
+        } else if (what == 4) {
+            pdec[i - C] = 1.f;
+        } else if (what == 5 && i < 2) {
+            chunk_decay[i] = pa::lin::decay_factor(g, i ? rest : C);
+        }
     }
     pa::tc::fence_before();
     __syncthreads();
@@ -479,15 +489,12 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                 give();
                 if (has_p) ok = make_p(0, j0, j0 + 16);
             }
-            const float em_full = expm1f(g * C), em_rest = expm1f(g * rest);
             for (int c = 0; c < nc && ok; ++c) {
+                const pa::lin::Decay l = chunk_decay[c + 1 == nc];  // (kept there: registers are short)
+                const float2 hi = make_float2(l.hi, l.hi), lo = make_float2(l.lo, l.lo);
                 ok = SUM ? wait_all(&sum_full[c & 1], (c >> 1) & 1) : wait_all(u_full, c & 1);
                 if (!ok) break;
                 pa::tc::fence_after();
-                // l^m S = S + (l^m - 1) S: as exact as its rounding where l is close to 1, and
-                // before anything is added, of which S may be many times larger
-                const float em = c + 1 < nc ? em_full : em_rest;
-                const float2 em2 = make_float2(em, em);
 #pragma unroll
                 for (int k = 0; k < HALF / 2; k += 8) {
                     uint32_t u[16];
@@ -495,8 +502,9 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
                     pa::tc::wait_ld();
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        s[k + e] = __fadd2_rn(pa::ffma2(em2, s[k + e], s[k + e]),
-                                              make_float2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1])));
+                        s[k + e] = pa::ffma2(hi, s[k + e],
+                                             pa::ffma2(lo, s[k + e], make_float2(__uint_as_float(u[2 * e]),
+                                                                                 __uint_as_float(u[2 * e + 1]))));
                 }
                 pa::tc::fence_before();
                 signal(SUM ? &sum_free[c & 1] : u_free);
@@ -714,7 +722,7 @@ __global__ void __launch_bounds__(256) chain_kernel(const ChunkParams a) {
         return;
     }
     constexpr int64_t DD4 = D * D / 4;
-    const float em = expm1f(pa::lin::log_decay(a.p, h) * a.seg);
+    const pa::lin::Decay l = pa::lin::decay_factor(pa::lin::log_decay(a.p, h), a.seg);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (q.held) s = reinterpret_cast<const float4 *>(a.p.states)[(static_cast<int64_t>(q.state) * a.p.H + h) * DD4 + e];
     float4 *at = reinterpret_cast<float4 *>(a.ws) + (static_cast<int64_t>(before) * a.p.H + h) * DD4 + e;
@@ -730,10 +738,10 @@ __global__ void __launch_bounds__(256) chain_kernel(const ChunkParams a) {
             if (i0 + k >= ns) break;
             at[(i0 + k) * step] = s;
             if (i0 + k == ns - 1) break;
-            s.x = fmaf(em, s.x, s.x) + u[k].x;
-            s.y = fmaf(em, s.y, s.y) + u[k].y;
-            s.z = fmaf(em, s.z, s.z) + u[k].z;
-            s.w = fmaf(em, s.w, s.w) + u[k].w;
+            s.x = pa::lin::decayed(l, s.x, u[k].x);
+            s.y = pa::lin::decayed(l, s.y, u[k].y);
+            s.z = pa::lin::decayed(l, s.z, u[k].z);
+            s.w = pa::lin::decayed(l, s.w, u[k].w);
         }
     }
 }

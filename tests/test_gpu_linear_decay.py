@@ -1,0 +1,105 @@
+"""Linear attention where the old state is what counts: large states from before, tokens
+whose keys are 0, decays of every strength.  A factor l^n has to be right relative to
+itself; what it multiplies may be all that is left."""
+import pytest
+import torch
+
+from linear_util import Linear
+from test_gpu_linear import TERMS, _built, decode, errors, prefill  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+bf16, f32 = torch.bfloat16, torch.float32
+
+
+def large(n, prior, log_decay, keys=0, **kw):
+    """Requests whose states hold about 3e6 and whose tokens from the `keys`-th on add
+    nothing."""
+    x = Linear(n, prior, H=len(log_decay), log_decay=log_decay, **kw)
+    at = 0
+    for m in n:
+        x.qkv[at + keys:at + m, 1] = 0
+        at += m
+    if not kw.get("fused", True):
+        x.q, x.k, x.v = (t.contiguous() for t in x.qkv.unbind(1))
+    x.states0 *= 1e6
+    x.states = x.states0.cuda()
+    return x
+
+
+@pytest.mark.parametrize("dtype", [bf16, f32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B", [2, 40])
+def test_decode(dtype, d, B):
+    """One token: l S is all that the state is."""
+    x = large([1] * B, [5] * B, [-1e-6, -0.3, -0.69, -0.7, -2.0, -4.0, -5.5, -8.0, -10.0, -12.0, -15.0, -17.0, -24.0, -60.0],
+              d=d, dtype=dtype, seed=B)
+    x.check(decode(x))
+    assert errors() == 0
+
+
+@pytest.mark.parametrize("dtype", [bf16, f32])
+def test_decode_beside_small_products(dtype):
+    """The products are there, and far smaller than what the state was."""
+    x = large([1] * 3, [5] * 3, [-4.0, -8.0, -12.0, -17.0], keys=1, d=128, dtype=dtype)
+    x.check(decode(x))
+
+
+@pytest.mark.parametrize("dtype", [bf16, f32])
+@pytest.mark.parametrize("n", [2, 5, 8])
+def test_few_tokens(dtype, n):
+    """Token by token, l^n in n steps."""
+    x = large([n, 1], [5, 1], [-0.05, -0.693, -0.694, -2.0, -4.0, -7.0], d=128, dtype=dtype, seed=n)
+    x.check(prefill(x), terms=TERMS)
+
+
+@pytest.mark.parametrize("keys", [0, 1])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,log_decay", [
+    (63, [-0.01, -0.1, -0.2, -0.231, -0.3, -0.4, -0.9]), (64, [-0.0107, -0.0109, -0.2, -0.231, -0.3, -0.4, -0.9]),
+    (65, [-0.1, -0.2, -0.231, -0.3, -0.4, -0.8]), (66, [-0.25, -0.3, -0.5, -0.9]),
+    (130, [-0.05, -0.1, -0.2, -0.231, -0.3, -0.4]), (200, [-0.05, -0.1, -0.2, -0.231, -0.28])])
+def test_chunks(n, log_decay, d, keys):
+    """l^64 and l^(tokens of the last chunk) of a state whose chunks add nothing, or the
+    first token's product alone."""
+    x = large([n, 30], [5, 0], log_decay, keys=keys, d=d, seed=n)
+    x.check(prefill(x), terms=TERMS)
+    assert errors() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1100, 2500])
+def test_segments(n, d):
+    """l^(tokens of a segment) where a request is cut: the state from before, and the
+    first token's product, through all segments."""
+    from paged_kv_cache_192_gb300 import ops
+    decay = [-1e-4, -0.004, -20.0 / n, -70.0 / n]
+    assert ops.linear_prefill_workspace_size(1, n, n, len(decay), d) > 0
+    for keys, prior in ((0, 5), (1, 5), (1, 0)):
+        x = large([n], [prior], decay, keys=keys, d=d, seed=n)
+        x.check(prefill(x), terms=TERMS)
+    assert errors() == 0
+
+
+def check_with_infinities(x, out, terms=(0.0, 0.0)):
+    """x.check's bounds where the result is finite, the same infinities elsewhere."""
+    ref, rs, oa, ob, sa, sb = x.reference()
+    for got, want, tol in (
+            (x.states.double(), rs, (2.0 ** -22 + 2.0 ** -20 + terms[1]) * sa + (2.0 ** -22 + 2.0 ** -24) * sb),
+            (out.double(), ref, torch.finfo(x.dtype).eps / 2 * ref.abs() + ((x.d + 20) * 2.0 ** -24 + terms[0]) * oa +
+             (2.0 ** -22 + 2.0 ** -24) * ob)):
+        inf = torch.isinf(want)
+        assert bool(inf.any()) and torch.equal(got[inf], want[inf])
+        fin = torch.isfinite(want)
+        assert bool((got[fin] - want[fin]).abs().le(tol[fin]).all())
+        assert bool(torch.isnan(got[torch.isnan(want)]).all())
+
+
+@pytest.mark.parametrize("dtype", [bf16, f32])
+@pytest.mark.parametrize("n", [1, 3])
+def test_an_infinite_state_stays_infinite(dtype, n):
+    """Decays of both kinds and none; an output sees it with the sign of its query."""
+    x = Linear([n, n], [5, 3], H=5, d=64, dtype=dtype, log_decay=[0.0, -0.01, -0.69, -3.0, -30.0])
+    x.states0[x.ids[0], :, 7, 11] = float("inf")
+    x.states0[x.ids[1], :, 60, 3] = -float("inf")
+    x.states = x.states0.cuda()
+    check_with_infinities(x, decode(x) if n == 1 else prefill(x))
