@@ -652,7 +652,7 @@ int pa_cross_attention(void *out, const void *q, const void *k_cache, const void
  *   context_lens  int32 [R]: tokens of the sequence, the new ones included, as
  *                 pa_plan_step gives them.  A request whose context is its new
  *                 tokens alone starts from nothing, whatever its state holds.
- *   log_decay     float32 [H], each at most 0
+ *   log_decay     float32 [H], each at most 0 (a NaN makes the head's outputs and states NaN)
  * pa_linear_decode: one token per request (R = B rows).  A row with a negative
  * state id or context length 0 is padding: zeros, and no state is touched.
  * pa_linear_prefill: request r has the rows query_start[r] .. query_start[r + 1]

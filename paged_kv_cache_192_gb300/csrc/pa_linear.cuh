@@ -41,8 +41,11 @@ __device__ __forceinline__ Request request(const LinParams &p, int r) {
 }
 
 // Logarithm of a head's decay.  Below -1e4 (the decay is 0 in 32 bits long before) it
-// stays finite, so that l^0 is 1.
-__device__ __forceinline__ float log_decay(const LinParams &p, int h) { return fmaxf(p.log_decay[h], -1e4f); }
+// stays finite, so that l^0 is 1; a NaN stays one.
+__device__ __forceinline__ float log_decay(const LinParams &p, int h) {
+    const float g = p.log_decay[h];
+    return g < -1e4f ? -1e4f : g;
+}
 
 // x^n = e^(g n) to within 2 ulp: g n is exact as y + rest, e^rest = 1 + rest (rest is
 // below 2^-24 |y|).

@@ -103,3 +103,22 @@ def test_an_infinite_state_stays_infinite(dtype, n):
     x.states0[x.ids[1], :, 60, 3] = -float("inf")
     x.states = x.states0.cuda()
     check_with_infinities(x, decode(x) if n == 1 else prefill(x))
+
+
+@pytest.mark.parametrize("dtype", [bf16, f32])
+@pytest.mark.parametrize("n", [1, 4, 100, 1500])
+def test_a_decay_that_is_nan_shows(n, dtype):
+    """In every output and state of its head, and in no other's."""
+    if dtype == f32 and n > 100:
+        n = 130
+    x = Linear([n, n], [5, 0], H=3, d=64, dtype=dtype, log_decay=[-0.1, float("nan"), -2.0])
+    y = Linear([n, n], [5, 0], H=3, d=64, dtype=dtype, log_decay=[-0.1, -0.5, -2.0])
+    got, want = prefill(x), prefill(y)
+    assert bool(torch.isnan(got[:, 1]).all()) and torch.equal(got[:, ::2], want[:, ::2])
+    assert bool(torch.isnan(x.states[x.ids, 1]).all()) and torch.equal(x.states[x.ids][:, ::2], y.states[y.ids][:, ::2])
+    if n == 1:
+        x.states.copy_(x.states0)
+        got = decode(x)
+        assert bool(torch.isnan(got[:, 1]).all()) and torch.equal(got[:, ::2], want[:, ::2])
+        assert bool(torch.isnan(x.states[x.ids, 1]).all())
+    assert errors() == 0
