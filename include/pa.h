@@ -663,10 +663,15 @@ int pa_cross_attention(void *out, const void *q, const void *k_cache, const void
  *                 bytes, 16-byte aligned, scratch (may be NULL if that is 0);
  *                 calls that may overlap on the GPU need separate ones
  * A request whose numbers do not fit is left out (of a decode: zeros) and
- * PA_DEVERR_BAD_REQUEST recorded.  Sums and states are kept in fp32.  A NaN or
- * infinity in v of a token may also reach earlier tokens of the same request and head
- * within 64 tokens of it (their weight for it is 0, and 0 x NaN is NaN); one in q or k
- * reaches no earlier token.  fp32 prompts run token by token on the decode's kernel.
+ * PA_DEVERR_BAD_REQUEST recorded.  Sums and states are kept in fp32.  fp32 prompts run
+ * token by token on the decode's kernel, as do bf16 prompts of few tokens.  Others run in
+ * chunks of 64 tokens, where what is not finite reaches more than the formula says:
+ *   - a NaN or infinity in v of a token may also make earlier outputs of the same
+ *     request and head within 64 tokens of it NaN (their weight for it is 0, and 0 x NaN
+ *     is NaN); one in q or k reaches no earlier token;
+ *   - an infinity in q, k or v may come out as NaN where the formula has an infinity.  An
+ *     infinite state stays infinite, and v's infinities reach the state as such, as long
+ *     as the decays between are not 0 in fp32.
  */
 int pa_linear_decode(void *out, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                      const void *v, int64_t v_stride, float *states, int num_states,

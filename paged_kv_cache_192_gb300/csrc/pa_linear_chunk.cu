@@ -191,9 +191,12 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, 
         "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(h), "r"(t0), "r"(pa::smem_u32(bar))
         : "memory");
 }
-// x as two or three bf16 terms, two values at a time
+// x as two or three bf16 terms, two values at a time: a term that is not the last, and
+// what it leaves.  It stays finite: an infinity, or a number past bf16's range, is left to
+// the last term, where inf - inf would be NaN.
 __device__ __forceinline__ uint32_t take_bf16(float2 &x) {
-    const uint32_t t = pack_bf16(x.x, x.y);
+    uint32_t t;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(t) : "f"(x.y), "f"(x.x));
     x = pa::ffma2(pa::bf16x2_to_float2(t), make_float2(-1.f, -1.f), x);
     return t;
 }

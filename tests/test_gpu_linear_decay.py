@@ -122,3 +122,49 @@ def test_a_decay_that_is_nan_shows(n, dtype):
         assert bool(torch.isnan(got[:, 1]).all()) and torch.equal(got[:, ::2], want[:, ::2])
         assert bool(torch.isnan(x.states[x.ids, 1]).all())
     assert errors() == 0
+
+
+@pytest.mark.parametrize("n", [30, 100, 1500])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompts_keep_an_infinite_state(n, d):
+    """One that was there before, through chunks and segments, and its outputs."""
+    x = Linear([n, n], [5, 3], H=3, d=d, log_decay=[0.0, -0.001, -20.0 / n])
+    x.states0[x.ids[0], :, 7, 11] = float("inf")
+    x.states0[x.ids[1], :, d - 4, 3] = -float("inf")
+    x.qkv[..., [7, d - 4]] += (x.qkv[..., [7, d - 4]] == 0).to(bf16)  # (0 x inf is NaN in the formula too)
+    x.states = x.states0.cuda()
+    check_with_infinities(x, prefill(x), terms=TERMS)
+
+
+@pytest.mark.parametrize("n,at", [(30, 3), (100, 99), (100, 70), (1500, 20), (1500, 800), (1500, 1499)])
+def test_prompts_with_an_infinite_value(n, at):
+    """It reaches the state with the sign of k v, and no other dimension of v."""
+    x = Linear([n, 40], [5, 0], H=2, d=64, log_decay=[0.0, -0.01], seed=at)
+    x.qkv[at, 1] += (x.qkv[at, 1] == 0).to(bf16)
+    x.qkv[at, 2, :, 9] = float("inf")
+    x.qkv[at, 2, :, 50] = -float("inf")
+    out = prefill(x)
+    ref, rs, oa, ob, sa, sb = x.reference()
+    got, want = x.states[x.ids].double(), rs[x.ids]
+    assert bool(torch.isinf(want[0, :, :, [9, 50]]).all()) and torch.equal(got[0, :, :, [9, 50]], want[0, :, :, [9, 50]])
+    keep = torch.ones(64, dtype=torch.bool)
+    keep[[9, 50]] = False
+    tol = (2.0 ** -22 + 2.0 ** -20 + TERMS[1]) * sa + (2.0 ** -22 + 2.0 ** -24) * sb
+    assert bool(((got - want).abs() <= tol[x.ids])[..., keep].all()) and bool(torch.isfinite(got[1]).all())
+    tol = 2.0 ** -8 * ref.abs() + ((64 + 20) * 2.0 ** -24 + TERMS[0]) * oa + (2.0 ** -22 + 2.0 ** -24) * ob
+    assert bool(((out.double() - ref).abs() <= tol)[..., keep].all())
+    # behind it the state's part is not finite; 64 tokens and more before it all is
+    assert not bool(torch.isfinite(out[at:n, :, [9, 50]]).any())
+    early = out[:max(0, at - 63), :, [9, 50]].double() - ref[:max(0, at - 63), :, [9, 50]]
+    assert bool((early.abs() <= tol[:max(0, at - 63), :, [9, 50]]).all())
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_prompts_of_states_past_the_range_of_bf16(sign):
+    """Between bf16's largest number and fp32's."""
+    x = Linear([70], [5], H=1, d=64, log_decay=[-0.5])
+    x.qkv[:, 0, :, 4] *= 2.0 ** -10
+    x.qkv[:, 1] = 0
+    x.states0[x.ids[0], 0, 4, 4] = sign * 3.4e38
+    x.states = x.states0.cuda()
+    x.check(prefill(x), terms=TERMS)
