@@ -594,6 +594,10 @@ int pa_prefill_kernel_for(int R, int max_query_len, int Hq, int Hkv, int head_di
  *   query_start   int32 [R + 1]: prefix sums of the added tokens
  *   slots         int64 [max_tokens]: slot of each added token, -1 behind the last
  *   positions     int64 [max_tokens]: its position, 0 behind the last
+ * slots and positions go by added token, the calls of single tokens (pa_decode_window,
+ * pa_linear_decode) by row: the two agree where every row gains one token, or rows that
+ * gain none stand behind the others.  In other steps tokens are taken by query_start
+ * (pa_prefill_window, pa_cross_attention, pa_linear_prefill).
  * All or nothing: a step that does not fit changes no state, adds no token and
  * shows the old lengths and pages; free_state[3] counts it and PA_DEVERR_NO_BLOCKS
  * (pages, a table too narrow for a row, max_tokens) or PA_DEVERR_BAD_REQUEST (an id
@@ -638,8 +642,8 @@ int pa_cross_attention(void *out, const void *q, const void *k_cache, const void
                        pa_stream_t stream);
 
 /*
- * pa_linear_decode, pa_linear_prefill -- linear attention with a decay for each
- * head, whose state is all that a sequence keeps:
+ * pa_linear_decode, pa_linear_decode_planned, pa_linear_prefill -- linear attention
+ * with a decay for each head, whose state is all that a sequence keeps:
  *   S_t = l_h S_{t-1} + k_t v_t^T,   o_t = scale * q_t S_t,   l_h = exp(log_decay[h])
  *   out, q, k, v  [tokens][H][head_dim] (dtype); out is contiguous, the others have
  *                 q_stride .. v_stride elements between tokens (heads of a token
@@ -655,6 +659,16 @@ int pa_cross_attention(void *out, const void *q, const void *k_cache, const void
  *   log_decay     float32 [H], each at most 0 (a NaN makes the head's outputs and states NaN)
  * pa_linear_decode: one token per request (R = B rows).  A row with a negative
  * state id or context length 0 is padding: zeros, and no state is touched.
+ * pa_linear_decode_planned: the same for the rows of a planned step.  query_start,
+ * int32 [B + 1], are the step's (NULL: pa_linear_decode).  A row that gained no token
+ * (query_start[r + 1] == query_start[r]) is padding too: one that drops tokens or waits,
+ * and every row of a step that was refused, which shows the old lengths; without
+ * query_start each of them would take a token that its sequence does not have, and a
+ * state cannot be taken back.  A row that gained more than one does not fit.  The token
+ * of row r is row r of q, k and v, so that a plan's slots, which go by added token, are
+ * those of the rows only if rows without a token stand behind the others
+ * (pa_linear_prefill with max_query_len 1 takes tokens by query_start, at the same cost).
+ * Tokens that a plan drops are not taken out of a state: keep a copy of it before drafts.
  * pa_linear_prefill: request r has the rows query_start[r] .. query_start[r + 1]
  * of total_tokens; a request without new tokens, or with a negative state id, is
  * left out, and rows outside every request are left as they are.  max_query_len
@@ -677,6 +691,11 @@ int pa_linear_decode(void *out, const void *q, int64_t q_stride, const void *k, 
                      const void *v, int64_t v_stride, float *states, int num_states,
                      const int32_t *state_ids, const int32_t *context_lens, const float *log_decay,
                      int B, int H, int head_dim, float scale, int dtype, pa_stream_t stream);
+int pa_linear_decode_planned(void *out, const void *q, int64_t q_stride, const void *k,
+                             int64_t k_stride, const void *v, int64_t v_stride, float *states,
+                             int num_states, const int32_t *state_ids, const int32_t *query_start,
+                             const int32_t *context_lens, const float *log_decay, int B, int H,
+                             int head_dim, float scale, int dtype, pa_stream_t stream);
 int pa_linear_prefill_workspace_size(int R, int total_tokens, int max_query_len, int H, int head_dim,
                                      int dtype, size_t *bytes);
 int pa_linear_prefill(void *out, const void *q, int64_t q_stride, const void *k, int64_t k_stride,

@@ -509,11 +509,15 @@ struct Linear {
     }
 };
 
-// q, k, v, states, state_ids, context_lens, log_decay, scale, out, stream
+// q, k, v, states, state_ids, context_lens, log_decay, scale, out, stream, query_start
+// (None: every row has its token)
 PyObject *linear_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded("linear_decode", 10, n, [&]() -> PyObject * {
+    return guarded("linear_decode", 11, n, [&]() -> PyObject * {
         const Linear x(a, a[5], a[6]);
         if (x.R != x.T) value_error("state_ids must be " + shape({x.T}));
+        const bool planned = a[10] != Py_None;
+        if (planned && !sized(tensor(a[10], "query_start"), {x.R + 1}))
+            value_error("query_start must be " + shape({x.R + 1}));
         const bool given = a[8] != Py_None;
         if (given && tensor(a[8], "out").sizes() != x.q.sizes()) value_error("out must have the shape of q");
         const float scale = scale_of(a[7], x.d);
@@ -522,16 +526,18 @@ PyObject *linear_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int code = dtype_of(x.q);
         const void *qp = place(x.q, "q", dt, false), *kp = place(x.k, "k", dt, false),
                    *vp = place(x.v, "v", dt, false), *ip = place(x.ids, "state_ids", at::kInt),
-                   *lp = place(x.lens, "context_lens", at::kInt), *dp = place(x.decay, "log_decay", at::kFloat);
+                   *lp = place(x.lens, "context_lens", at::kInt), *dp = place(x.decay, "log_decay", at::kFloat),
+                   *tp = planned ? place(tensor(a[10], "query_start"), "query_start", at::kInt) : nullptr;
         void *sp = place(x.states, "states", at::kFloat);
         const at::Tensor out = given ? tensor(a[8], "out") : place.new_like(x.q);
         void *op = place(out, "out", dt);
         const int ns = int32_of(x.states.size(0), "num_states"), B = int32_of(x.R, "B"), H = int32_of(x.H, "H"),
                   d = int32_of(x.d, "head_dim");
         launch([&] {
-            return pa_linear_decode(op, qp, x.qs, kp, x.ks, vp, x.vs, static_cast<float *>(sp), ns,
-                                    static_cast<const int32_t *>(ip), static_cast<const int32_t *>(lp),
-                                    static_cast<const float *>(dp), B, H, d, scale, code, place.stream);
+            return pa_linear_decode_planned(op, qp, x.qs, kp, x.ks, vp, x.vs, static_cast<float *>(sp), ns,
+                                            static_cast<const int32_t *>(ip), static_cast<const int32_t *>(tp),
+                                            static_cast<const int32_t *>(lp), static_cast<const float *>(dp), B, H, d,
+                                            scale, code, place.stream);
         });
         return THPVariable_Wrap(out);
     });

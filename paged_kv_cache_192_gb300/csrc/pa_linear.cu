@@ -34,7 +34,7 @@ template <>
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 template <typename T, int D, int CW>
-__global__ void __launch_bounds__(256, D == 64 ? 5 : 4) recurrent_kernel(const LinParams p) {
+__global__ void __launch_bounds__(256, D == 64 ? 5 : 4) recurrent_kernel(const LinParams p, const int32_t *added) {
     constexpr int NT = 256, LPR = CW / 4;   // lanes per row of the slice
     constexpr int RG = NT / LPR;            // rows at a time
     constexpr int NR = D / RG;              // rows per thread
@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 5 : 4) recurrent_kernel(const L
     const int c0 = slice * CW, c = tid % LPR * 4, row0 = tid / LPR;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Request x = pa::lin::request(p, r);
+    const Request x = pa::lin::request(p, r, added);
     const T *q = static_cast<const T *>(p.q) + h * D, *k = static_cast<const T *>(p.k) + h * D,
             *v = static_cast<const T *>(p.v) + h * D + c0;
     T *out = static_cast<T *>(p.out) + static_cast<int64_t>(h) * D + c0;
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 5 : 4) recurrent_kernel(const L
 }
 
 template <typename T, int D, int CW>
-int launch(const LinParams &p, cudaStream_t stream) {
+int launch(const LinParams &p, const int32_t *added, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(int64_t(p.R) * p.H * (D / CW)));
     cfg.blockDim = dim3(256);
@@ -127,24 +127,24 @@ int launch(const LinParams &p, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     (void)cudaGetLastError();  // drop a stale error that is not ours
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, recurrent_kernel<T, D, CW>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, recurrent_kernel<T, D, CW>, p, added);
     if (e != cudaSuccess) return pa::cuda_fail(e, "linear attention launch");
     return pa::check_launch("linear attention launch");
 }
 
 // Validate mode: states in the pool and none for two requests, rows inside the
 // call, lengths that hold the new tokens, decays at most 1.
-int validate_linear(const LinParams &p, int max_query_len, cudaStream_t stream) try {
+int validate_linear(const LinParams &p, const int32_t *added, int max_query_len, cudaStream_t stream) try {
     std::vector<int32_t> ids(p.R), lens(p.R), qs(size_t(p.R) + 1);
     std::vector<float> decay(p.H);
     if (int rc = pa::fetch(ids.data(), p.state_ids, ids.size() * 4, stream)) return rc;
     if (int rc = pa::fetch(lens.data(), p.context_lens, lens.size() * 4, stream)) return rc;
     if (int rc = pa::fetch(decay.data(), p.log_decay, decay.size() * 4, stream)) return rc;
-    if (p.query_start)
-        if (int rc = pa::fetch(qs.data(), p.query_start, qs.size() * 4, stream)) return rc;
+    if (const int32_t *rows = p.query_start ? p.query_start : added)
+        if (int rc = pa::fetch(qs.data(), rows, qs.size() * 4, stream)) return rc;
     std::vector<bool> used(p.num_states);
     for (int r = 0; r < p.R; ++r) {
-        const int64_t n = p.query_start ? int64_t(qs[r + 1]) - qs[r] : lens[r] != 0;
+        const int64_t n = p.query_start || added ? int64_t(qs[r + 1]) - qs[r] : lens[r] != 0;
         if (n < 0 || n > max_query_len || lens[r] < n ||
             (p.query_start && n > 0 && (qs[r] < 0 || qs[r + 1] > p.T)))
             return pa::fail(PA_ERR_INVALID, "validate: request %d has %lld new tokens of %d, rows of %d, max_query_len %d",
@@ -230,7 +230,7 @@ LinParams make(void *out, const void *q, int64_t q_stride, const void *k, int64_
 namespace pa {
 namespace lin {
 
-int launch_recurrent(const LinParams &p, int D, int dtype, cudaStream_t stream) {
+int launch_recurrent(const LinParams &p, int D, int dtype, cudaStream_t stream, const int32_t *added) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -241,8 +241,8 @@ int launch_recurrent(const LinParams &p, int D, int dtype, cudaStream_t stream) 
     const bool cut = int64_t(p.R) * p.H < sms;
     auto go = [&](auto t) {
         using T = decltype(t);
-        if (D == 128) return cut ? launch<T, 128, 32>(p, stream) : launch<T, 128, 64>(p, stream);
-        return cut ? launch<T, 64, 32>(p, stream) : launch<T, 64, 64>(p, stream);
+        if (D == 128) return cut ? launch<T, 128, 32>(p, added, stream) : launch<T, 128, 64>(p, added, stream);
+        return cut ? launch<T, 64, 32>(p, added, stream) : launch<T, 64, 64>(p, added, stream);
     };
     return dtype == PA_BF16 ? go(__nv_bfloat16()) : go(float());
 }
@@ -250,10 +250,11 @@ int launch_recurrent(const LinParams &p, int D, int dtype, cudaStream_t stream) 
 }  // namespace lin
 }  // namespace pa
 
-extern "C" int pa_linear_decode(void *out, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
-                                const void *v, int64_t v_stride, float *states, int num_states,
-                                const int32_t *state_ids, const int32_t *context_lens, const float *log_decay, int B,
-                                int H, int head_dim, float scale, int dtype, pa_stream_t stream) {
+extern "C" int pa_linear_decode_planned(void *out, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                        const void *v, int64_t v_stride, float *states, int num_states,
+                                        const int32_t *state_ids, const int32_t *query_start,
+                                        const int32_t *context_lens, const float *log_decay, int B, int H, int head_dim,
+                                        float scale, int dtype, pa_stream_t stream) {
     pa::clear_error();
     LinParams p = make(out, q, q_stride, k, k_stride, v, v_stride, states, num_states, state_ids, nullptr,
                        context_lens, log_decay, B, B, H, scale);
@@ -261,9 +262,17 @@ extern "C" int pa_linear_decode(void *out, const void *q, int64_t q_stride, cons
     if (int rc = check("linear_decode", p, 1, head_dim, dtype, &empty)) return rc;
     if (empty) return PA_OK;
     if (pa::validate_on())
-        if (int rc = validate_linear(p, 1, stream)) return rc;
+        if (int rc = validate_linear(p, query_start, 1, stream)) return rc;
     p.err = pa::device_error_word();
-    return pa::lin::launch_recurrent(p, head_dim, dtype, stream);
+    return pa::lin::launch_recurrent(p, head_dim, dtype, stream, query_start);
+}
+
+extern "C" int pa_linear_decode(void *out, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                const void *v, int64_t v_stride, float *states, int num_states,
+                                const int32_t *state_ids, const int32_t *context_lens, const float *log_decay, int B,
+                                int H, int head_dim, float scale, int dtype, pa_stream_t stream) {
+    return pa_linear_decode_planned(out, q, q_stride, k, k_stride, v, v_stride, states, num_states, state_ids, nullptr,
+                                    context_lens, log_decay, B, H, head_dim, scale, dtype, stream);
 }
 
 extern "C" int pa_linear_prefill(void *out, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
@@ -286,7 +295,7 @@ extern "C" int pa_linear_prefill(void *out, const void *q, int64_t q_stride, con
     if (need && !pa::aligned16(workspace))
         return pa::fail(PA_ERR_INVALID, "linear_prefill: workspace must be 16-byte aligned");
     if (pa::validate_on())
-        if (int rc = validate_linear(p, max_query_len, stream)) return rc;
+        if (int rc = validate_linear(p, nullptr, max_query_len, stream)) return rc;
     p.err = pa::device_error_word();
     if (!uses_chunks(R, max_query_len, H, head_dim, dtype))
         return pa::lin::launch_recurrent(p, head_dim, dtype, stream);

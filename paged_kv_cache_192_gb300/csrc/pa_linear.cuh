@@ -25,15 +25,16 @@ struct Request {
     bool held;
 };
 
-__device__ __forceinline__ Request request(const LinParams &p, int r) {
+__device__ __forceinline__ Request request(const LinParams &p, int r, const int32_t *added = nullptr) {
     Request x;
     const int L = p.context_lens[r];
     x.state = p.state_ids[r];
     x.t0 = p.query_start ? p.query_start[r] : r;
-    x.n = p.query_start ? p.query_start[r + 1] - x.t0 : (L != 0);
+    x.n = p.query_start ? p.query_start[r + 1] - x.t0 : added ? added[r + 1] - added[r] : (L != 0);
     x.held = L > x.n;
     const bool padding = x.n == 0 || x.state < 0;
-    if (padding || x.state >= p.num_states || x.t0 < 0 || x.n < 0 || x.n > p.T - x.t0 || L < x.n) {
+    if (padding || x.state >= p.num_states || x.t0 < 0 || x.n < 0 || x.n > p.T - x.t0 || L < x.n ||
+        (added && x.n != 1)) {
         if (!padding) record_error(p.err, PA_DEVERR_BAD_REQUEST);
         x.state = -1;
     }
@@ -80,8 +81,9 @@ __device__ __forceinline__ Decay decay_factor(float g, int n) {
 }
 __device__ __forceinline__ float decayed(const Decay &f, float s, float x) { return fmaf(f.hi, s, fmaf(f.lo, s, x)); }
 
-// The recurrent kernel (pa_linear.cu), any number of tokens and both types.
-int launch_recurrent(const LinParams &p, int D, int dtype, cudaStream_t stream);
+// The recurrent kernel (pa_linear.cu), any number of tokens and both types.  `added`: of a
+// call without query_start, the prefix sums of the tokens that the rows gained, or NULL.
+int launch_recurrent(const LinParams &p, int D, int dtype, cudaStream_t stream, const int32_t *added = nullptr);
 
 // The kernels of long prompts (pa_linear_chunk.cu), bf16.  A call cuts its requests
 // into segments of `tokens` tokens (0: it does not), at most `slots` of them, whose

@@ -522,7 +522,10 @@ def plan_step(state, seq_ids, new_tokens, block_size, max_tokens, table_blocks=N
     ring row by row and given back behind its end.  max_tokens: length of slots
     and positions; table_blocks: width of block_table (seq_pages' by default).
     All or nothing: a step that does not fit is refused (free_state[3] counts it,
-    the device error word says why) and shows the old lengths, no new token.
+    the device error word says why) and shows the old lengths, no new token: calls that
+    take query_start then do nothing, decode calls that go by row read what there was.
+    slots and positions go by added token, decode calls by row: the two agree where
+    every row gains a token, or those that gain none stand behind the others.
     out: a StepPlan to write into.  Returns the StepPlan."""
     return tuple.__new__(StepPlan, _calls().plan_step(*state, seq_ids, new_tokens, block_size,
                                                       max_tokens, table_blocks, out, stream))
@@ -544,7 +547,7 @@ def cross_attention(q, k_cache, v_cache, block_table, query_start, encoder_lens,
 
 
 def linear_decode(q, k, v, states, state_ids, context_lens, log_decay, scale=None, out=None,
-                  stream=None):
+                  stream=None, query_start=None):
     """Linear attention with a decay for each head, one token per sequence
     (pa_linear_decode).
 
@@ -553,9 +556,13 @@ def linear_decode(q, k, v, states, state_ids, context_lens, log_decay, scale=Non
     in place: S = exp(log_decay) S + k v^T; out = scale q S (scale: 1/sqrt(d) by
     default).  state_ids: int32 [B], each state at most once.  context_lens: int32
     [B]: 1 starts from nothing, whatever the state holds; 0, or a negative state
-    id, is padding (zeros).  log_decay: float32 [H], at most 0.  Returns out."""
+    id, is padding (zeros).  log_decay: float32 [H], at most 0.  query_start: int32 [B + 1],
+    a plan's (pa_linear_decode_planned): a row that gained no token, as every row of a step
+    that was refused, is padding too.  Give it behind every plan_step: without it such a
+    row's state takes a token that its sequence does not have.  Tokens that a plan drops
+    stay in a state.  Returns out."""
     return _calls().linear_decode(q, k, v, states, state_ids, context_lens, log_decay, scale, out,
-                                  stream)
+                                  stream, query_start)
 
 
 def linear_prefill_workspace_size(R, total_tokens, max_query_len, H, head_dim, dtype=torch.bfloat16):
