@@ -40,7 +40,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 5 : 4) recurrent_kernel(const L
     constexpr int NR = D / RG;              // rows per thread
     constexpr int SLICES = D / CW;
     static_assert(RG <= D && LPR <= 32, "a warp covers whole rows");
-    __shared__ float sq[2][D], sk[2][D], sv[2][CW];  // the token's vectors, the next token's
+    __shared__ float sq[2][D], sk[2][D];  // the token's vectors, the next token's
+    __shared__ __align__(16) float sv[2][CW];  // (read 16 bytes at a time)
     __shared__ float4 part[2][NT / 32][LPR];         // o of each warp's rows
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int slice = blockIdx.x % SLICES, rh = blockIdx.x / SLICES;
