@@ -672,7 +672,9 @@ int pa_cross_attention(void *out, const void *q, const void *k_cache, const void
  * pa_linear_prefill: request r has the rows query_start[r] .. query_start[r + 1]
  * of total_tokens; a request without new tokens, or with a negative state id, is
  * left out, and rows outside every request are left as they are.  max_query_len
- * >= every request's new tokens.
+ * >= every request's new tokens; the kernel is chosen by it (or by total_tokens where that
+ * is less), so a bound far above the lengths costs time: 64 requests of one token, 32
+ * heads of 128, take 43 us with 1 and 105 with 2048.
  *   workspace     device buffer of at least pa_linear_prefill_workspace_size
  *                 bytes, 16-byte aligned, scratch (may be NULL if that is 0);
  *                 calls that may overlap on the GPU need separate ones

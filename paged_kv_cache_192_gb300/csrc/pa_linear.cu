@@ -193,13 +193,14 @@ int check(const char *what, const LinParams &p, int max_query_len, int D, int dt
 // 7.3 us here and 6.9 there, of 2,048 pairs 107 and 99; 4 tokens 4.6 and 6.9, 71 and 97.
 // D 64: of 32 pairs 5.2 and 5.4, but 24 tokens of 2,048 pairs 56 and 68, as an SM has room
 // for many of these CTAs and one of those.
-bool uses_chunks(int R, int max_query_len, int H, int D, int dtype) {
+// The lengths are on the device: the call's bound and its tokens are all there is to go by.
+bool uses_chunks(int R, int T, int max_query_len, int H, int D, int dtype) {
     const int most = D == 64 && int64_t(R) * H >= 4 * 152 ? 24 : 8;
-    return dtype == PA_BF16 && max_query_len > most;
+    return dtype == PA_BF16 && std::min(max_query_len, T) > most;
 }
 
-size_t workspace_bytes_for(const pa::lin::Segments &s, int R, int max_query_len, int H, int D, int dtype) {
-    return uses_chunks(R, max_query_len, H, D, dtype) && s.tokens ? size_t(s.slots) * H * D * D * 4 : 0;
+size_t workspace_bytes_for(const pa::lin::Segments &s, int R, int T, int max_query_len, int H, int D, int dtype) {
+    return uses_chunks(R, T, max_query_len, H, D, dtype) && s.tokens ? size_t(s.slots) * H * D * D * 4 : 0;
 }
 
 LinParams make(void *out, const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -290,7 +291,7 @@ extern "C" int pa_linear_prefill(void *out, const void *q, int64_t q_stride, con
     if (empty) return PA_OK;
     if (!query_start) return pa::fail(PA_ERR_INVALID, "linear_prefill: NULL pointer");
     const pa::lin::Segments seg = pa::lin::segments_for(R, total_tokens, max_query_len, H);
-    const size_t need = workspace_bytes_for(seg, R, max_query_len, H, head_dim, dtype);
+    const size_t need = workspace_bytes_for(seg, R, total_tokens, max_query_len, H, head_dim, dtype);
     if (need && (!workspace || workspace_bytes < need))
         return pa::fail(PA_ERR_INVALID, "linear_prefill: workspace of %zu bytes, %zu needed", workspace_bytes, need);
     if (need && !pa::aligned16(workspace))
@@ -298,7 +299,7 @@ extern "C" int pa_linear_prefill(void *out, const void *q, int64_t q_stride, con
     if (pa::validate_on())
         if (int rc = validate_linear(p, nullptr, max_query_len, stream)) return rc;
     p.err = pa::device_error_word();
-    if (!uses_chunks(R, max_query_len, H, head_dim, dtype))
+    if (!uses_chunks(R, total_tokens, max_query_len, H, head_dim, dtype))
         return pa::lin::launch_recurrent(p, head_dim, dtype, stream);
     return pa::lin::launch_chunks(p, head_dim, max_query_len, static_cast<float *>(workspace), seg, stream);
 }
@@ -310,7 +311,7 @@ extern "C" int pa_linear_prefill_workspace_size(int R, int total_tokens, int max
     if (R < 0 || R > 65535 || total_tokens < 0 || max_query_len < 0 || H <= 0 || H > 1024 ||
         (head_dim != 64 && head_dim != 128) || (dtype != PA_BF16 && dtype != PA_F32))
         return pa::fail(PA_ERR_INVALID, "linear_prefill_workspace_size: bad sizes");
-    *bytes = workspace_bytes_for(pa::lin::segments_for(R, total_tokens, max_query_len, H), R, max_query_len, H, head_dim,
-                                 dtype);
+    *bytes = workspace_bytes_for(pa::lin::segments_for(R, total_tokens, max_query_len, H), R, total_tokens,
+                                 max_query_len, H, head_dim, dtype);
     return PA_OK;
 }
