@@ -195,7 +195,7 @@ int check(const char *what, const LinParams &p, int max_query_len, int D, int dt
 // for many of these CTAs and one of those.
 // The lengths are on the device: the call's bound and its tokens are all there is to go by.
 bool uses_chunks(int R, int T, int max_query_len, int H, int D, int dtype) {
-    const int most = D == 64 && int64_t(R) * H >= 4 * 152 ? 24 : 8;
+    const int most = D == 64 && int64_t(R) * H >= 4 * pa::lin::sm_count() ? 24 : 8;
     return dtype == PA_BF16 && std::min(max_query_len, T) > most;
 }
 
@@ -232,15 +232,20 @@ LinParams make(void *out, const void *q, int64_t q_stride, const void *k, int64_
 namespace pa {
 namespace lin {
 
-int launch_recurrent(const LinParams &p, int D, int dtype, cudaStream_t stream, const int32_t *added) {
+int sm_count() {
     int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return cuda_fail(cudaGetLastError(), "linear attention: SM count");
+    if (cudaGetDevice(&dev) == cudaSuccess &&
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && sms > 0)
+        return sms;
+    (void)cudaGetLastError();
+    return 152;
+}
+
+int launch_recurrent(const LinParams &p, int D, int dtype, cudaStream_t stream, const int32_t *added) {
     // Columns per CTA: 64 (64 sequences of 32 heads, D 128: 42.4 us; 44.6 with 128, where
     // two CTAs of an SM hold too few bytes on their way between loading and storing,
     // 43.0 with 32).  A few states leave SMs idle: then 32.
-    const bool cut = int64_t(p.R) * p.H < sms;
+    const bool cut = int64_t(p.R) * p.H < sm_count();
     auto go = [&](auto t) {
         using T = decltype(t);
         if (D == 128) return cut ? launch<T, 128, 32>(p, added, stream) : launch<T, 128, 64>(p, added, stream);

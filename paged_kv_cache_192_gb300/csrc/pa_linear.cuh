@@ -81,6 +81,10 @@ __device__ __forceinline__ Decay decay_factor(float g, int n) {
 }
 __device__ __forceinline__ float decayed(const Decay &f, float s, float x) { return fmaf(f.hi, s, fmaf(f.lo, s, x)); }
 
+// SMs of the current device; a GB300's where there is none (a workspace's size may be asked
+// for anywhere).
+int sm_count();
+
 // The recurrent kernel (pa_linear.cu), any number of tokens and both types.  `added`: of a
 // call without query_start, the prefix sums of the tokens that the rows gained, or NULL.
 int launch_recurrent(const LinParams &p, int D, int dtype, cudaStream_t stream, const int32_t *added = nullptr);

@@ -56,7 +56,7 @@ using pa::lin::LinParams;
 using pa::lin::Request;
 
 constexpr int C = 64;  // tokens per chunk
-constexpr int kSMs = 152, kSortedR = 64;  // requests that a CTA puts in order
+constexpr int kSortedR = 64;  // requests that a CTA puts in order
 
 struct ChunkParams {
     LinParams p;
@@ -802,8 +802,9 @@ Segments segments_for(int R, int T, int max_query_len, int H) {
     // 4 219, 9 228, 14 248, 16 282.
     constexpr double OVERHEAD = 8, SUM = 0.6, LAUNCHES = 6;
     const int64_t pairs = int64_t(R) * H, most = (int64_t(std::min(max_query_len, T)) + C - 1) / C;
-    const double all = (double(T) / C + 0.5 * R) * H / kSMs;  // chunks per SM
-    auto waves = [&](double ctas) { return std::ceil(ctas / kSMs); };
+    const int sms = sm_count();
+    const double all = (double(T) / C + 0.5 * R) * H / sms;  // chunks per SM
+    auto waves = [&](double ctas) { return std::ceil(ctas / sms); };
     double best = std::max(double(most + OVERHEAD), all + waves(double(pairs)) * OVERHEAD);
     for (int64_t n = 2; n <= 64 && 2 * n <= most; ++n) {
         const int64_t chunks = (most + n - 1) / n;
@@ -824,7 +825,7 @@ int launch_chunks(const LinParams &p, int D, int max_query_len, float *ws, const
     // as long: a long one that starts last runs alone at the end.  8 of 65 to 2,048 tokens, 32
     // heads: 113 us with the longest last, 83 first and the others as they come, 78.5 in
     // order; 40 of 65 to 1,000, 8 heads: 72 and 60; 60 of 1 to 300: 48 both.
-    const bool sorted = !s.tokens && p.R > 1 && p.R <= kSortedR && int64_t(p.R) * p.H > kSMs &&
+    const bool sorted = !s.tokens && p.R > 1 && p.R <= kSortedR && int64_t(p.R) * p.H > sm_count() &&
                         4 * int64_t(std::min(max_query_len, p.T)) * p.R > 5 * int64_t(p.T);
     const ChunkParams a{p, ws, s.tokens, s.slots, sorted};
     return D == 128 ? launch<128>(a, stream) : launch<64>(a, stream);
