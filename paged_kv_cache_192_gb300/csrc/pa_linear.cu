@@ -12,8 +12,9 @@
 // The same kernel takes the tokens of a request one after another, with the state
 // loaded and stored once.
 //
-// Measured: 64 sequences of 32 heads, D 128: 42.4 us, 6.3 TB/s (0.93 of HBM); one
-// sequence of 16 heads, D 64: 2.0 us on the GPU, 4.4 through the Python call.
+// Measured: 64 sequences of 32 heads, D 128: 42.6 us, 6.3 TB/s (0.93 of HBM); one
+// sequence of 16 heads, D 64: 2.0 us on the GPU, 4.1 through the Python call; 500 tokens of
+// 16 heads, D 64, fp32: 192 us, 0.38 us per token (its barrier and its sums over rows).
 #include <algorithm>
 #include <cmath>
 #include <new>
@@ -33,6 +34,8 @@ __device__ __forceinline__ float to_float(float x) { return x; }
 template <>
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
+// (Five CTAs per SM for D 64: 256 sequences of 16 heads, states in L2, 15.2 us; with four, to
+// which the compiler's own choice of registers led, 17.3.)
 template <typename T, int D, int CW>
 __global__ void __launch_bounds__(256, D == 64 ? 5 : 4) recurrent_kernel(const LinParams p, const int32_t *added) {
     constexpr int NT = 256, LPR = CW / 4;   // lanes per row of the slice
@@ -190,8 +193,8 @@ int check(const char *what, const LinParams &p, int max_query_len, int D, int dt
 
 // Whether a prompt runs on the chunk kernels: bf16 of more tokens than the recurrent
 // kernel takes in the time of one chunk.  D 128: 8 tokens of 32 (request, head) pairs
-// 7.3 us here and 6.9 there, of 2,048 pairs 107 and 99; 4 tokens 4.6 and 6.9, 71 and 97.
-// D 64: of 32 pairs 5.2 and 5.4, but 24 tokens of 2,048 pairs 56 and 68, as an SM has room
+// 7.3 us here and 6.9 there, of 2,048 pairs 106 and 104; 4 tokens 4.7 and 6.9, 71 and 108.
+// D 64: of 32 pairs 5.1 and 5.4, but 24 tokens of 2,048 pairs 62 and 70, as an SM has room
 // for many of these CTAs and one of those.
 // The lengths are on the device: the call's bound and its tokens are all there is to go by.
 bool uses_chunks(int R, int T, int max_query_len, int H, int D, int dtype) {

@@ -35,8 +35,8 @@
 // part), one chains them, and the segments then run like requests.
 //
 // Measured (32 heads, D 128): 8 requests of 65 to 2,048 tokens 73 us, 3.9 TB/s (0.57 of
-// HBM); a prompt of 16,384 tokens, 4 segments, 214 us (70 of them the segments' sums;
-// uncut 530 us); 100 tokens 9.2 us.  A chunk takes about 4,000 cycles: the sequence of
+// HBM); a prompt of 16,384 tokens, 4 segments, 214 us call after call (70 of them the
+// segments' sums; 219 with an L2 that holds nothing of it, and 529 uncut); 100 tokens 9.5 us.  A chunk takes about 4,000 cycles: the sequence of
 // waits, issues and commits of warp 9 (each 150 to 400 cycles, with what 16 warps of five
 // roles lose to instruction fetches), beside 2,900 of V' and 2,700 of the state's warps;
 // the tensor core is busy for 38 % of the time, issue 55 %.  Shared memory has 2,800 cycles
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(Lay<D>::THREADS, 1)
         // rows of 128 bytes, K-major; tokens as K (64 tokens per column block)
         const uint64_t row_major = pa::tc::sdesc(s0, 16, 1024), col_major = pa::tc::sdesc(s0, C * 128, 1024);
         // The whole warp goes along and one lane issues: descriptors and waits stay uniform
-        // (one lane alone took 294 us for a prompt of 16,384 tokens instead of 219).  S1
+        // (one lane alone took 294 us for a prompt of 16,384 tokens, then 219 with all).  S1
         // of a chunk is overwritten two chunks later, its P has been waited for by then.
         auto issue_s1 = [&](int c) {
             if (!wait_all(&full[c % NST], (c / NST) & 1)) return false;
@@ -798,8 +798,9 @@ Segments segments_for(int R, int T, int max_query_len, int H) {
     // longest request sets how many chunks follow one another.  Of 15 batches (1 to 32
     // heads, 400 to 16,000 tokens, 1 to 4 requests) the choice was the fastest of up to ten
     // cuts in ten, within 20 % of it in four, and 162 against 122 us for one request of
-    // 8,000 tokens among short ones.  A prompt of 16,384 tokens, 32 heads: 1 piece 530 us,
-    // 4 219, 9 228, 14 248, 16 282.
+    // 8,000 tokens among short ones (137 and 123 beside one of 500).  L2 flushed, 32 heads: a
+    // prompt of 16,384 tokens 529 us in 1 piece, 284 in 3, 219 in 4 (chosen), 280 in 5, 238 in
+    // 8, 223 in 9, 237 in 14, 275 in 16; two of 4,000 tokens 140 in 1 (chosen), 124 in 2.
     constexpr double OVERHEAD = 8, SUM = 0.6, LAUNCHES = 6;
     const int64_t pairs = int64_t(R) * H, most = (int64_t(std::min(max_query_len, T)) + C - 1) / C;
     const int sms = sm_count();
