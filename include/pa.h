@@ -625,7 +625,8 @@ int pa_plan_step(const int32_t *seq_ids, const int32_t *new_tokens, int R, int32
  *                 [0, total_tokens]
  *   encoder_lens  int32 [R], each in [0, capacity]
  *   max_query_len host int >= every request's query tokens (with less, rows may be
- *                 left out and PA_DEVERR_BAD_REQUEST recorded)
+ *                 left out and PA_DEVERR_BAD_REQUEST recorded); the kernel is chosen by
+ *                 it, or by total_tokens where that is less
  * The states of a request are read once for all of its tokens (beams that share an
  * encoder run are the query tokens of one request).  Slots behind the last state
  * do not enter the result, whatever they hold, nor are table entries behind it

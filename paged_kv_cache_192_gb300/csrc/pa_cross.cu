@@ -397,7 +397,7 @@ extern "C" int pa_cross_attention(void *out, const void *q, const void *k_cache,
     if (pa::validate_on())
         if (int rc = validate_cross(c, max_query_len, stream)) return rc;
     c.err = pa::device_error_word();
-    const int64_t cols = int64_t(max_query_len) * gq;
+    const int64_t cols = int64_t(std::min(max_query_len, total_tokens)) * gq;  // (a bound may be generous)
     if (cols <= kMaxCols) {
         auto pick = [&](auto d) -> int {
             constexpr int DD = decltype(d)::value;
